@@ -100,7 +100,7 @@ typedef enum {
                               * by fa_check_device_error; info = the mask tile or top-k bucket) */
 } fa_status;
 
-typedef enum { FA_DTYPE_BF16 = 1, FA_DTYPE_F32 = 2, FA_DTYPE_I32 = 3, FA_DTYPE_F16 = 4 } fa_dtype;
+typedef enum { FA_DTYPE_BF16 = 1, FA_DTYPE_F32 = 2, FA_DTYPE_I32 = 3, FA_DTYPE_F16 = 4, FA_DTYPE_F64 = 5 } fa_dtype;
 
 /* A strided view of device memory; shape/stride are in elements, outermost
  * first; only the first ndim entries are read. */
@@ -335,6 +335,93 @@ int fa_fwd_kvcache_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_t
                         const fa_tensor* cache_seqlens, const fa_tensor* block_table,
                         int32_t window_left, int32_t window_right, float softcap, float scale,
                         int32_t causal, int32_t append, const fa_opts* opts, fa_plan* plan_out);
+
+/* Rotary positions.  Row r of x, at position p, has its first `rot` columns
+ * rotated in pairs, pair i (0 <= i < rot/2) by the angle p * inv_freq[i]:
+ *     a' = mscale * (a cos - b sin),   b' = mscale * (a sin + b cos)
+ * with (a, b) columns (i, i + rot/2) (interleaved == 0) or (2i, 2i + 1)
+ * (interleaved != 0); columns rot .. d-1 are copied.  inverse != 0 rotates by
+ * the negative angle, with the same mscale: the gradient with respect to x of
+ * a loss whose gradient with respect to the rotated rows is given (dq and dk
+ * of fa_bwd on their way back to the projections).
+ *   q, q_out     [B, S, Hq, d] or packed [total, Hq, d]; one element type
+ *                (bf16 or fp16) and the layout rules of fa_fwd; q_out may be
+ *                q itself (same pointer and strides), else must not overlap it
+ *   k, k_out     as q with Hkv heads (any Hkv >= 1); both NULL: q alone
+ *   positions    int32 [B, S] (a stride of 0 broadcasts over B) or [total];
+ *                NULL: rows of [B, S, ...] are at positions 0 .. S-1 (a packed
+ *                call needs positions).  Any int32 value; a negative one
+ *                rotates backwards.
+ *   inv_freq     fp64 [rot/2], device memory, radians per position (finite);
+ *                rot is even, 2 <= rot <= d; d is 64 or 128
+ * The angle is reduced modulo a turn in 64-bit fixed point, so its error does
+ * not grow with the position beyond that of p * inv_freq in fp64; the sine,
+ * cosine and products are fp32 and each element is rounded once.
+ * opts: stream and the event_begin / event_end pair are used; no workspace. */
+int fa_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_out, const fa_tensor* k_out,
+            const fa_tensor* positions, const fa_tensor* inv_freq, float mscale, int32_t interleaved,
+            int32_t inverse, const fa_opts* opts);
+
+/* Frequencies scaled for contexts longer than the trained one. */
+typedef enum {
+  FA_ROPE_PLAIN = 0,  /* base^(-2i/rot) */
+  FA_ROPE_LINEAR = 1, /* positions divided by `factor` */
+  FA_ROPE_NTK = 2,    /* base * factor^(rot / (rot - 2)): the lowest frequency is
+                       * divided by `factor`, the highest kept */
+  FA_ROPE_BLEND = 3,  /* by wavelength: pairs that turn at least `high` times in
+                       * original_len positions are kept, those that turn at most
+                       * `low` times are divided by `factor`, between them the two
+                       * are mixed linearly in the number of turns */
+  FA_ROPE_YARN = 4    /* as BLEND, but mixed linearly in the pair index (between the
+                       * indices that turn `high` and `low` times, rounded outwards),
+                       * and mscale = 0.1 ln(factor) + 1 */
+} fa_rope_scaling_kind;
+typedef struct {
+  int32_t kind;         /* fa_rope_scaling_kind */
+  int32_t original_len; /* BLEND, YARN: trained context length, >= 1 */
+  double factor;        /* all but PLAIN: >= 1 */
+  double low, high;     /* BLEND, YARN: turns, 0 < low < high */
+} fa_rope_scaling;
+
+/* Host-only: the rot/2 frequencies (radians per position) of a rotary
+ * embedding with this base (> 1; > 0 and != 1 is not enough), and the mscale
+ * that goes with them, written to host memory.  scaling NULL = PLAIN.  NTK
+ * needs rot > 2. */
+int fa_rope_inv_freq(int32_t rot, double base, const fa_rope_scaling* scaling, double* inv_freq, float* mscale);
+
+/* Append to a KV cache, with the rotation applied on the way: for row i of
+ * sequence s (q_len_s new rows, L_s = cache_seqlens[s] keys cached before), at
+ * position p = positions[row] (NULL: L_s + i),
+ *     cache row L_s + i of s  <-  (rope(k_new row, p), v_new row),
+ *     q_out row               <-  rope(q row, p),
+ *     seqlens_out[s]          <-  L_s + q_len_s
+ * with rope() as for fa_rope (v is copied).  One launch; a step of serving is
+ * this call and then fa_fwd_chunk with seqlens_k = seqlens_out.
+ *   k_new, v_new   [B, Sq, Hkv, d], or [total_q, Hkv, d] with cu_seqlens_q
+ *                  (int32 [n_seq + 1]); rows of a packed call outside
+ *                  [cu_seqlens_q[0], cu_seqlens_q[n_seq]) belong to no sequence:
+ *                  they are not read and their q_out rows are left as they were
+ *   q, q_out       NULL, or laid out like k_new with Hq heads (any Hq >= 1);
+ *                  q_out may be q itself, else must not overlap it
+ *   k_cache, v_cache, block_table, cache_seqlens  as for fa_fwd_kvcache
+ *   positions      NULL, or int32 [B, Sq] / [total_q]
+ *   inv_freq       fp64 [rot/2] device memory, or NULL: no rotation (bit-exact
+ *                  copies; mscale is then ignored)
+ *   seqlens_out    NULL, or int32 [n_seq], not overlapping cache_seqlens
+ * opts->workspace holds the error word alone: FA_KVCACHE_APPEND_WORKSPACE_BYTES,
+ * 256-byte aligned, zero-filled before its first use; it may be the workspace
+ * of the fa_fwd_chunk call that follows on the same stream.  A sequence with
+ * L_s < 0, q_len_s < 0 or L_s + q_len_s beyond the cache (block table width x
+ * page_size, or cap) is recorded as FA_ERR_DEVICE_BOUNDS: none of its rows is
+ * read or written, and its seqlens_out is L_s.  A page index outside the cache is
+ * recorded the same way and that row's cache write is skipped.  Two sequences
+ * must not append to the same cache row. */
+#define FA_KVCACHE_APPEND_WORKSPACE_BYTES ((size_t)256)
+int fa_kvcache_append(const fa_tensor* q, const fa_tensor* q_out, const fa_tensor* k_new, const fa_tensor* v_new,
+                      const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* cu_seqlens_q,
+                      const fa_tensor* cache_seqlens, const fa_tensor* block_table, const fa_tensor* positions,
+                      const fa_tensor* inv_freq, float mscale, int32_t interleaved, const fa_tensor* seqlens_out,
+                      const fa_opts* opts);
 
 /* Backward pass: dq, dk, dv of the forward for the same arguments
  * (InfiniTrain pull request 193, "FlashAttention native backend": the

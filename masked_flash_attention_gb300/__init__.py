@@ -27,3 +27,8 @@ from ._lib import (  # noqa: F401
     fa_status_string,
     lib,
 )
+from ._ops import (  # noqa: F401
+    fa_kvcache_append,
+    fa_rope,
+    fa_rope_inv_freq,
+)

@@ -31,16 +31,18 @@ FA_ERR_DEVICE_BOUNDS = 6
 FA_ERR_NO_DEVICE = 7
 FA_ERR_DEVICE_VALUE = 8
 
-FA_DTYPE_BF16, FA_DTYPE_F32, FA_DTYPE_I32, FA_DTYPE_F16 = 1, 2, 3, 4
+FA_DTYPE_BF16, FA_DTYPE_F32, FA_DTYPE_I32, FA_DTYPE_F16, FA_DTYPE_F64 = 1, 2, 3, 4, 5
 FA_MASK_NONE, FA_MASK_DENSE, FA_MASK_TOPK = 0, 1, 2
 FA_DEBUG_NO_SKIP = 0x1
 FA_DEBUG_WITHHOLD = 0x2
 FA_DEBUG_VALIDATE = 0x4
 FA_PATH_DECODE, FA_PATH_PREFILL = 1, 2
 FA_TILE_EMPTY, FA_TILE_FULL, FA_TILE_PARTIAL = 0, 1, 2
+FA_ROPE_PLAIN, FA_ROPE_LINEAR, FA_ROPE_NTK, FA_ROPE_BLEND, FA_ROPE_YARN = 0, 1, 2, 3, 4
+FA_KVCACHE_APPEND_WORKSPACE_BYTES = 256
 
 _DTYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float32: FA_DTYPE_F32, torch.int32: FA_DTYPE_I32,
-           torch.float16: FA_DTYPE_F16}
+           torch.float16: FA_DTYPE_F16, torch.float64: FA_DTYPE_F64}
 
 
 class fa_tensor(ctypes.Structure):
@@ -77,6 +79,11 @@ class fa_plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class fa_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_len", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
 _P = ctypes.POINTER
 _ARGS = [_P(fa_tensor), _P(fa_tensor), _P(fa_tensor), _P(fa_tensor), _P(fa_tensor),
          _P(fa_tensor), _P(fa_tensor), _P(fa_tensor), _P(fa_mask), ctypes.c_int32,
@@ -93,9 +100,17 @@ _KV_ARGS = [_P(fa_tensor)] * 10 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_floa
 _BWD_ARGS = [_P(fa_tensor)] * 11 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_float,
                                     ctypes.c_int32, _P(fa_opts)]
 
+# fa_rope: q, k, q_out, k_out, positions, inv_freq, mscale, interleaved, inverse, opts
+_ROPE_ARGS = [_P(fa_tensor)] * 6 + [ctypes.c_float, ctypes.c_int32, ctypes.c_int32, _P(fa_opts)]
+
+# fa_kvcache_append: q, q_out, k_new, v_new, k_cache, v_cache, cu_seqlens_q, cache_seqlens,
+# block_table, positions, inv_freq, mscale, interleaved, seqlens_out, opts
+_APPEND_ARGS = [_P(fa_tensor)] * 11 + [ctypes.c_float, ctypes.c_int32, _P(fa_tensor), _P(fa_opts)]
+
 EXPORTS = ("fa_fwd", "fa_fwd_plan", "fa_fwd_workspace_size", "fa_fwd_kvcache", "fa_fwd_kvcache_plan",
            "fa_bwd", "fa_bwd_plan", "fa_fwd_noalloc", "fa_check_device_error", "fa_status_string",
-           "fa_abi_version", "fa_fwd_debug_dump", "fa_debug_dump_bytes")
+           "fa_abi_version", "fa_fwd_debug_dump", "fa_debug_dump_bytes", "fa_rope", "fa_rope_inv_freq",
+           "fa_kvcache_append")
 
 
 def _load():
@@ -137,6 +152,13 @@ def _load():
     lib.fa_fwd_debug_dump.restype = ctypes.c_int
     lib.fa_debug_dump_bytes.argtypes = [ctypes.c_int64]
     lib.fa_debug_dump_bytes.restype = ctypes.c_size_t
+    lib.fa_rope.argtypes = _ROPE_ARGS
+    lib.fa_rope.restype = ctypes.c_int
+    lib.fa_rope_inv_freq.argtypes = [ctypes.c_int32, ctypes.c_double, _P(fa_rope_scaling), _P(ctypes.c_double),
+                                     _P(ctypes.c_float)]
+    lib.fa_rope_inv_freq.restype = ctypes.c_int
+    lib.fa_kvcache_append.argtypes = _APPEND_ARGS
+    lib.fa_kvcache_append.restype = ctypes.c_int
     # a library built from other headers would read these structures wrongly
     if lib.fa_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI {lib.fa_abi_version()}, this binding describes ABI {ABI_VERSION}: "

@@ -13,41 +13,13 @@
 #include <cstring>
 
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
+#include "api_util.h"
 #include "fa_internal.h"
 
 using namespace mfa;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-
-// An activation/cache tensor: bf16 or fp16, rank, unit head-dim stride,
-// other strides multiples of 8 elements (16 bytes), 16-byte aligned base.
-int check_bf16(const fa_tensor* t, int ndim) {
-  if (!t || !t->data) return FA_ERR_INVALID_ARG;
-  if ((t->dtype != FA_DTYPE_BF16 && t->dtype != FA_DTYPE_F16) || t->ndim != ndim) return FA_ERR_INVALID_ARG;
-  for (int i = 0; i < ndim; ++i)
-    if (t->shape[i] < 0) return FA_ERR_INVALID_ARG;
-  if (t->stride[ndim - 1] != 1) return FA_ERR_INVALID_ARG;
-  for (int i = 0; i < ndim - 1; ++i)
-    if (t->stride[i] < 0 || (t->stride[i] % 8) != 0) return FA_ERR_INVALID_ARG;
-  if (!aligned16(t->data)) return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
-
-int check_i32_vec(const fa_tensor* t, int64_t len) {
-  if (!t || !t->data || t->dtype != FA_DTYPE_I32 || t->ndim != 1) return FA_ERR_INVALID_ARG;
-  if (t->shape[0] != len || t->stride[0] != 1) return FA_ERR_INVALID_ARG;
-  return FA_OK;
-}
 
 // The second key source of fa_fwd_kvcache (null for fa_fwd).
 struct KvNew {
@@ -415,27 +387,6 @@ void bind_workspace(Plan* pl, void* ws) {
   P.tail_flags = reinterpret_cast<uint32_t*>(base + kTailFlagsOff);
 }
 
-// The device must be an sm_103 part (checked once per device).
-int check_device() {
-  static std::atomic<int> cached[64];  // 0 unknown, 1 ok, 2 bad
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_NO_DEVICE;
-  if (dev < 0 || dev >= 64) return FA_ERR_NO_DEVICE;
-  int c = cached[dev].load(std::memory_order_relaxed);
-  if (c == 0) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return FA_ERR_NO_DEVICE;
-    }
-    c = (major == 10 && minor == 3) ? 1 : 2;
-    cached[dev].store(c, std::memory_order_relaxed);
-  }
-  return c == 1 ? FA_OK : FA_ERR_NO_DEVICE;
-}
-
-
 int run_plan(Plan& pl, const fa_opts* opts);  // enqueue a validated plan (below)
 
 // fa_bwd: the forward's arguments (validated by make_plan, without mask or
@@ -597,20 +548,6 @@ int fa_fwd_kvcache_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_t
 thread_local bool mfa::g_trace_ranges = true;
 
 namespace {
-
-// NVTX range around the host-side enqueue of one stage (a profiler's trace
-// shows it beside the stage's kernels); none while g_trace_ranges is off.
-struct TraceRange {
-  bool on;
-  explicit TraceRange(const char* name) : on(mfa::g_trace_ranges) {
-    if (on) nvtxRangePushA(name);
-  }
-  ~TraceRange() {
-    if (on) nvtxRangePop();
-  }
-  TraceRange(const TraceRange&) = delete;
-  TraceRange& operator=(const TraceRange&) = delete;
-};
 
 // Bind the workspace and enqueue a validated plan's kernels on opts->stream.
 int run_plan(Plan& pl, const fa_opts* opts) {
