@@ -7,37 +7,72 @@ the current one are refused.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
 import torch
 
 from . import _lib
-from ._lib import FA_ERR_INVALID_ARG, FA_OK, FaError, _ref, describe, fa_rope_scaling, lib, make_opts
+from ._lib import _DTYPES, FA_ERR_INVALID_ARG, FA_OK, FaError, _ref, fa_rope_scaling, lib
 
 _SCALINGS = {"linear": _lib.FA_ROPE_LINEAR, "ntk": _lib.FA_ROPE_NTK, "blend": _lib.FA_ROPE_BLEND,
              "yarn": _lib.FA_ROPE_YARN}
 
+# These calls are short enough for their host side to count (one token's rotation runs 3 us on the
+# device), so the structures of one call are packed into one buffer by one struct call and passed
+# as addresses: the prototypes below take plain pointers where _lib's take typed ones.  One call of
+# fa_rope with its outputs given took 18.7 us when every structure was built on its own.
+_raw = ctypes.CDLL(_lib.LIB_PATH)
+_TENSOR = ctypes.sizeof(_lib.fa_tensor)
+_OPTS = ctypes.sizeof(_lib.fa_opts)
+_LAYOUTS = {}  # number of tensors -> (Struct of one fa_opts and that many fa_tensors, buffer type)
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+_OPTS_FMT = "PPNiiIiPPPP"
+assert struct.calcsize("@" + _OPTS_FMT) == _OPTS and _TENSOR % 8 == 0
 
-def _check_cuda(where, *tensors):
-    """Every given tensor lives on the current CUDA device."""
-    dev = None
+
+def _prototype(name, n_tensors, scalars):
+    f = getattr(_raw, name)
+    f.argtypes = [ctypes.c_void_p] * n_tensors + scalars
+    f.restype = ctypes.c_int
+    return f
+
+
+_i32, _f32, _ptr = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
+_fa_rope = _prototype("fa_rope", 6, [_f32, _i32, _i32, _ptr])
+_fa_kvcache_append = _prototype("fa_kvcache_append", 11, [_f32, _i32, _ptr, _ptr])
+
+try:  # the raw handle of the current stream, without the Stream object around it
+    _current_raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _current_raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _device_of(where, tensors):
+    """The current CUDA device, on which every given tensor has to be."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     for t in tensors:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise FaError(FA_ERR_INVALID_ARG, f"{where} (tensors must be CUDA tensors)")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise FaError(FA_ERR_INVALID_ARG, f"{where} (tensors must be on the current device, cuda:{dev})")
+        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0):
+            raise FaError(FA_ERR_INVALID_ARG, f"{where} (tensors must be CUDA tensors on the current device)")
+    return dev
 
 
-def _allocating_on(stream, device):
-    """Allocations inside belong to ``stream`` (a raw handle; None: the current stream)."""
-    if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+class _on_stream:
+    """Allocations inside belong to the call's stream, if that is not the current one."""
+
+    def __init__(self, stream, dev):
+        self.other = None
+        if stream is not None and stream != _current_raw_stream(dev):
+            self.other = torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev))
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
 
 
 def _workspace(nbytes, device):
@@ -47,9 +82,42 @@ def _workspace(nbytes, device):
     return ws
 
 
-def _set_workspace(opts, workspace):
-    opts.workspace = workspace.data_ptr()
-    opts.workspace_bytes = workspace.numel() * workspace.element_size()
+def _event(e):
+    return e.cuda_event if e is not None else 0
+
+
+def _pack(tensors, dev, stream, workspace=None, max_q=0, max_k=0, debug_flags=0, event_begin=None, event_end=None,
+          event_attn_end=None, alibi=None):
+    """fa_opts and the fa_tensors of ``tensors`` in one buffer: ``(buffer,
+    address of the opts, addresses of the tensors, 0 where None)``.  The buffer
+    has to live until the call returns."""
+    at, vals, base = [], [], _OPTS
+    ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (0, 0)
+    vals = [_current_raw_stream(dev) if stream is None else stream, ws_ptr, ws_bytes, max_q or 0, max_k or 0, debug_flags, 0,
+            _event(event_begin), _event(event_end), alibi.data_ptr() if alibi is not None else 0, _event(event_attn_end)]
+    n = 0
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        shape = t.shape
+        nd = len(shape)
+        if nd > 4:
+            raise ValueError("at most 4 dimensions")
+        pad = _PAD[nd]
+        # an empty tensor may have no storage: a dummy non-null pointer (never read)
+        vals += (t.data_ptr() or 16, _DTYPES.get(t.dtype, 0), nd, *shape, *pad, *t.stride(), *pad)
+        at.append(base)
+        base += _TENSOR
+        n += 1
+    try:
+        layout, kind = _LAYOUTS[n]
+    except KeyError:
+        layout, kind = _LAYOUTS[n] = (struct.Struct("@" + _OPTS_FMT + "Qii4q4q" * n), ctypes.c_char * (_OPTS + n * _TENSOR))
+    buf = kind()
+    layout.pack_into(buf, 0, *vals)
+    addr = ctypes.addressof(buf)
+    return buf, addr, [x if x is None else addr + x for x in at]
 
 
 def fa_rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original_len=0, low=1.0, high=4.0):
@@ -80,18 +148,17 @@ def fa_rope(q, k=None, *, inv_freq, positions=None, q_out=None, k_out=None, msca
     [total], optional for [B, S, H, d].  Returns ``(q_out, k_out)``, allocated
     with torch when not given (k_out is None without k).  Raises FaError on a
     non-zero status."""
-    _check_cuda("fa_rope", q, k, inv_freq, positions, q_out, k_out)
+    dev = _device_of("fa_rope", (q, k, inv_freq, positions, q_out, k_out))
     if k is None and k_out is not None:
         raise FaError(FA_ERR_INVALID_ARG, "fa_rope (k_out without k)")
-    with _allocating_on(stream, q.device):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    opts = make_opts(stream=stream, event_begin=event_begin, event_end=event_end)
-    descs = [describe(x) for x in (q, k, q_out, k_out, positions, inv_freq)]
-    rc = lib.fa_rope(*[_ref(x) for x in descs], float(mscale), int(bool(interleaved)), int(bool(inverse)),
-                     ctypes.byref(opts))
+    if q_out is None or (k is not None and k_out is None):
+        with _on_stream(stream, dev):
+            if q_out is None:
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            if k is not None and k_out is None:
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    buf, opts, at = _pack((q, k, q_out, k_out, positions, inv_freq), dev, stream, event_begin=event_begin, event_end=event_end)
+    rc = _fa_rope(*at, mscale, 1 if interleaved else 0, 1 if inverse else 0, opts)
     if rc != FA_OK:
         raise FaError(rc, "fa_rope")
     return q_out, k_out
@@ -105,24 +172,20 @@ def fa_kvcache_append(k_new, v_new, k_cache, v_cache, cache_seqlens, *, q=None, 
     ``(q_out, seqlens_out, workspace)``: q_out (None without q), the int32
     lengths after the append, and the workspace holding the error word; each is
     allocated with torch when not given.  Raises FaError on a non-zero status."""
-    _check_cuda("fa_kvcache_append", k_new, v_new, k_cache, v_cache, cache_seqlens, q, q_out, cu_seqlens_q,
-                block_table, positions, inv_freq, seqlens_out, workspace)
+    dev = _device_of("fa_kvcache_append", (k_new, v_new, k_cache, v_cache, cache_seqlens, q, q_out, cu_seqlens_q,
+                                           block_table, positions, inv_freq, seqlens_out, workspace))
     if q is None and q_out is not None:
         raise FaError(FA_ERR_INVALID_ARG, "fa_kvcache_append (q_out without q)")
-    with _allocating_on(stream, k_new.device):
+    with _on_stream(stream, dev):
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if seqlens_out is None:
-            seqlens_out = torch.empty(cache_seqlens.shape, dtype=torch.int32, device=k_new.device)
+            seqlens_out = torch.empty_like(cache_seqlens, dtype=torch.int32)
         if workspace is None:
             workspace = _workspace(_lib.FA_KVCACHE_APPEND_WORKSPACE_BYTES, k_new.device)
-    opts = make_opts(stream=stream, event_begin=event_begin, event_end=event_end)
-    _set_workspace(opts, workspace)
-    descs = [describe(x) for x in (q, q_out, k_new, v_new, k_cache, v_cache, cu_seqlens_q, cache_seqlens,
-                                   block_table, positions, inv_freq)]
-    lens = describe(seqlens_out)
-    rc = lib.fa_kvcache_append(*[_ref(x) for x in descs], float(mscale), int(bool(interleaved)), _ref(lens),
-                               ctypes.byref(opts))
+    buf, opts, at = _pack((q, q_out, k_new, v_new, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table, positions,
+                           inv_freq, seqlens_out), dev, stream, workspace, event_begin=event_begin, event_end=event_end)
+    rc = _fa_kvcache_append(*at[:11], mscale, 1 if interleaved else 0, at[11], opts)
     if rc != FA_OK:
         raise FaError(rc, "fa_kvcache_append")
     return q_out, seqlens_out, workspace
