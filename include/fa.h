@@ -423,6 +423,49 @@ int fa_kvcache_append(const fa_tensor* q, const fa_tensor* q_out, const fa_tenso
                       const fa_tensor* inv_freq, float mscale, int32_t interleaved, const fa_tensor* seqlens_out,
                       const fa_opts* opts);
 
+/* Attention of a chunk of new tokens per sequence over a KV cache that holds
+ * their keys already (fa_kvcache_append): from one token a sequence (a decoding
+ * step) to long pieces of prompts, in any mix, on the tensor-core kernel.  The
+ * logits, the soft-cap, ALiBi, the windows, grouped-query heads and the rule for
+ * fully masked rows are those of fa_fwd, with off = kv_len - q_len, and
+ *     causal: key j is kept for query row i when j <= i + off, or when
+ *     j < prefix_lens[s]: a sequence's first prefix_lens[s] keys are seen by
+ *     every row, those among them both ways (a prefix language model, an image
+ *     before the text).
+ *   q, out         [B, Sq, Hq, d], or packed [total_q, Hq, d] with cu_seqlens_q;
+ *                  rows of a packed call in no sequence are left as they were
+ *   k_cache, v_cache  paged [num_pages, page_size, Hkv, d] with block_table, or
+ *                  padded [n_seq, cap, Hkv, d]
+ *   seqlens_k      int32 [n_seq], device: each sequence's keys in the cache,
+ *                  the chunk's own among them; shorter than its chunk is allowed
+ *                  (the first rows then see no key)
+ *   prefix_lens    int32 [n_seq], device, >= 0, or NULL; only with causal
+ *   lse            as for fa_fwd
+ * opts->max_seqlen_k is required, max_seqlen_q with cu_seqlens_q.  A length
+ * above its maximum or below zero is recorded as FA_ERR_DEVICE_BOUNDS and the
+ * sequence's rows are not computed; a page index outside the cache likewise,
+ * and the outputs that would have read it are not valid.  Entries of the block
+ * table past a sequence's keys, and cache rows past them, are never read.
+ * Any page size is taken; a multiple of 16 is copied fastest (the copies are
+ * as high as the largest power of two that divides it).
+ * FA_ERR_UNSUPPORTED: a stride of 0 along more than one element of q, k_cache
+ * or v_cache.  The result does not depend on scheduling.  Workspace:
+ * fa_fwd_chunk_plan's workspace_bytes, its first 256 bytes zero-filled once. */
+int fa_fwd_chunk(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* out,
+                 const fa_tensor* lse, const fa_tensor* cu_seqlens_q, const fa_tensor* seqlens_k,
+                 const fa_tensor* block_table, const fa_tensor* prefix_lens, int32_t window_left,
+                 int32_t window_right, float softcap, float scale, int32_t causal, const fa_opts* opts);
+
+/* Host-only: validate the arguments of fa_fwd_chunk and describe its plan:
+ * n_heads_sched = groups of q-heads that share a query tile, rows_per_tile =
+ * tokens per query tile, n_splits = partial results the workspace holds (units
+ * are split on the device, from the actual lengths), n_items = units at most. */
+int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* out,
+                      const fa_tensor* lse, const fa_tensor* cu_seqlens_q, const fa_tensor* seqlens_k,
+                      const fa_tensor* block_table, const fa_tensor* prefix_lens, int32_t window_left,
+                      int32_t window_right, float softcap, float scale, int32_t causal, const fa_opts* opts,
+                      fa_plan* plan_out);
+
 /* Backward pass: dq, dk, dv of the forward for the same arguments
  * (InfiniTrain pull request 193, "FlashAttention native backend": the
  * FlashAttention-2 causal forward and backward kernels it builds; "Framework

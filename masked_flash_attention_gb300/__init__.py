@@ -28,6 +28,8 @@ from ._lib import (  # noqa: F401
     lib,
 )
 from ._ops import (  # noqa: F401
+    fa_fwd_chunk,
+    fa_fwd_chunk_plan,
     fa_kvcache_append,
     fa_rope,
     fa_rope_inv_freq,

@@ -107,10 +107,15 @@ _ROPE_ARGS = [_P(fa_tensor)] * 6 + [ctypes.c_float, ctypes.c_int32, ctypes.c_int
 # block_table, positions, inv_freq, mscale, interleaved, seqlens_out, opts
 _APPEND_ARGS = [_P(fa_tensor)] * 11 + [ctypes.c_float, ctypes.c_int32, _P(fa_tensor), _P(fa_opts)]
 
+# fa_fwd_chunk / fa_fwd_chunk_plan: q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k,
+# block_table, prefix_lens, window_left, window_right, softcap, scale, causal, opts
+_CHUNK_ARGS = [_P(fa_tensor)] * 9 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_float,
+                                     ctypes.c_int32, _P(fa_opts)]
+
 EXPORTS = ("fa_fwd", "fa_fwd_plan", "fa_fwd_workspace_size", "fa_fwd_kvcache", "fa_fwd_kvcache_plan",
            "fa_bwd", "fa_bwd_plan", "fa_fwd_noalloc", "fa_check_device_error", "fa_status_string",
            "fa_abi_version", "fa_fwd_debug_dump", "fa_debug_dump_bytes", "fa_rope", "fa_rope_inv_freq",
-           "fa_kvcache_append")
+           "fa_kvcache_append", "fa_fwd_chunk", "fa_fwd_chunk_plan")
 
 
 def _load():
@@ -159,6 +164,10 @@ def _load():
     lib.fa_rope_inv_freq.restype = ctypes.c_int
     lib.fa_kvcache_append.argtypes = _APPEND_ARGS
     lib.fa_kvcache_append.restype = ctypes.c_int
+    lib.fa_fwd_chunk.argtypes = _CHUNK_ARGS
+    lib.fa_fwd_chunk.restype = ctypes.c_int
+    lib.fa_fwd_chunk_plan.argtypes = _CHUNK_ARGS + [_P(fa_plan)]
+    lib.fa_fwd_chunk_plan.restype = ctypes.c_int
     # a library built from other headers would read these structures wrongly
     if lib.fa_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI {lib.fa_abi_version()}, this binding describes ABI {ABI_VERSION}: "

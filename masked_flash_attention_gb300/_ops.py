@@ -1,5 +1,6 @@
-"""Binding of the operators around attention: rotary positions and the
-rotated append to a KV cache (argument marshalling only, as in ``_lib``).
+"""Binding of the operators around the KV cache: rotary positions, the rotated
+append and the attention of a chunk over the cache (argument marshalling only,
+as in ``_lib``).
 
 Outputs and workspaces that a call allocates belong to the stream it runs on
 (``stream`` if given, else the current one); tensors of another device than
@@ -41,6 +42,9 @@ def _prototype(name, n_tensors, scalars):
 _i32, _f32, _ptr = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 _fa_rope = _prototype("fa_rope", 6, [_f32, _i32, _i32, _ptr])
 _fa_kvcache_append = _prototype("fa_kvcache_append", 11, [_f32, _i32, _ptr, _ptr])
+_CHUNK_SCALARS = [_i32, _i32, _f32, _f32, _i32, _ptr]
+_fa_fwd_chunk = _prototype("fa_fwd_chunk", 9, _CHUNK_SCALARS)
+_fa_fwd_chunk_plan = _prototype("fa_fwd_chunk_plan", 9, _CHUNK_SCALARS + [_ptr])
 
 try:  # the raw handle of the current stream, without the Stream object around it
     _current_raw_stream = torch._C._cuda_getCurrentRawStream
@@ -189,3 +193,57 @@ def fa_kvcache_append(k_new, v_new, k_cache, v_cache, cache_seqlens, *, q=None, 
     if rc != FA_OK:
         raise FaError(rc, "fa_kvcache_append")
     return q_out, seqlens_out, workspace
+
+
+def _lse_shape(q, cu_seqlens_q):
+    return (q.shape[1], q.shape[0]) if cu_seqlens_q is not None else (q.shape[0], q.shape[2], q.shape[1])
+
+
+def fa_fwd_chunk_plan(q, k_cache, v_cache, seqlens_k, *, out=None, lse=None, cu_seqlens_q=None, block_table=None,
+                      prefix_lens=None, window_left=-1, window_right=-1, softcap=0.0, scale=None, causal=True,
+                      max_seqlen_q=None, max_seqlen_k=None, debug_flags=0, stream=0, **_):
+    """Host-only plan query of fa_fwd_chunk; returns (status, plan dict)."""
+    if lse is None:
+        lse = torch.empty(_lse_shape(q, cu_seqlens_q), dtype=torch.float32, device=q.device)
+    buf, opts, at = _pack((q, k_cache, v_cache, q if out is None else out, lse, cu_seqlens_q, seqlens_k, block_table,
+                           prefix_lens), -1, stream, max_q=max_seqlen_q, max_k=max_seqlen_k, debug_flags=debug_flags)
+    plan = _lib.fa_plan()
+    rc = _fa_fwd_chunk_plan(*at, window_left, window_right, softcap, scale or 0.0, 1 if causal else 0, opts,
+                            ctypes.addressof(plan))
+    return rc, plan.as_dict()
+
+
+def fa_fwd_chunk(q, k_cache, v_cache, seqlens_k, *, out=None, lse=None, cu_seqlens_q=None, block_table=None,
+                 prefix_lens=None, window_left=-1, window_right=-1, softcap=0.0, scale=None, causal=True,
+                 max_seqlen_q=None, max_seqlen_k=None, workspace=None, stream=None, debug_flags=0, event_begin=None,
+                 event_end=None, event_attn_end=None, alibi_slopes=None):
+    """Attention of each sequence's chunk of new tokens over the KV cache
+    (fa_fwd_chunk of the C ABI): sequence s sees its first ``seqlens_k[s]``
+    cached keys, the chunk's own among them.  ``max_seqlen_k`` is required,
+    ``max_seqlen_q`` with ``cu_seqlens_q``.  Returns ``(out, lse, workspace)``,
+    allocated with torch when not given; raises FaError on a non-zero status."""
+    dev = _device_of("fa_fwd_chunk", (q, k_cache, v_cache, seqlens_k, out, lse, cu_seqlens_q, block_table, prefix_lens,
+                                      workspace, alibi_slopes))
+    if alibi_slopes is not None:
+        alibi_slopes = _lib._alibi(alibi_slopes, q)
+    tensors = [q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens]
+    scalars = (window_left, window_right, softcap, scale or 0.0, 1 if causal else 0)
+    if out is None or lse is None or workspace is None:
+        with _on_stream(stream, dev):
+            if out is None:
+                tensors[3] = out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            if lse is None:
+                tensors[4] = lse = torch.empty(_lse_shape(q, cu_seqlens_q), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                buf, opts, at = _pack(tensors, dev, stream, max_q=max_seqlen_q, max_k=max_seqlen_k)
+                plan = _lib.fa_plan()
+                rc = _fa_fwd_chunk_plan(*at, *scalars, opts, ctypes.addressof(plan))
+                if rc != FA_OK:
+                    raise FaError(rc, "fa_fwd_chunk_plan")
+                workspace = _workspace(plan.workspace_bytes, q.device)
+    buf, opts, at = _pack(tensors, dev, stream, workspace, max_seqlen_q, max_seqlen_k, debug_flags, event_begin, event_end,
+                          event_attn_end, alibi_slopes)
+    rc = _fa_fwd_chunk(*at, *scalars, opts)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_chunk")
+    return out, lse, workspace

@@ -1,0 +1,568 @@
+// chunk.cu -- fa_fwd_chunk: attention of a chunk of new tokens per sequence over
+// a paged (or padded) KV cache.  This file holds the entry points, the planner
+// kernel, which cuts the step into pieces of work from the sequences' actual
+// lengths, and the kernel that joins the pieces of a unit; the attention itself
+// is chunk_sm103.cu.
+//
+// A unit is one query tile of one head group; units are independent and cover a
+// run of key tiles that the pair rules leave.  A serving step's units differ
+// widely (prompts' pieces beside single tokens, caches of any length), and may
+// be far fewer than the SMs, so the planner chooses one length T in key tiles,
+// cuts units longer than T into even pieces, and lists all pieces longest first;
+// the attention kernel's CTAs take them in rounds.  The pieces of a cut unit
+// leave normalised fp32 rows and their log-sum-exp, which are joined by
+// O = sum 2^(L_k - L) O_k, 2^L = sum 2^(L_k), in the order of the keys: the
+// result does not depend on scheduling.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "chunk.h"
+#include "fa_device.cuh"
+
+namespace mfa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBins = 1024;
+constexpr int kSeqSmem = 2048;  // sequences whose row-tile offsets are kept in shared memory
+// Cost model, in key tiles: what a piece costs beside its tiles (its start, Q,
+// the epilogue), what leaving a partial and joining it costs more, and the
+// join's launch.
+constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 4.f;
+
+__device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
+  if (atomicCAS(&p.ws->error, 0u, code) == 0u) atomicExch(&p.ws->error_info, info);
+}
+
+// Key tiles of row tile rt of sequence b (kt0, count) and the range [fl, fh]
+// of them, relative to kt0, whose every pair is kept.
+__device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int b, int rt, int& kt0, int& count, int& fl,
+                                              int& fh) {
+  const int q_len = chunk_qlen(p, b), kv = p.kv_len[b], off = kv - q_len;
+  const int pre = p.prefix ? p.prefix[b] : 0;
+  const int i0 = rt * p.rt_tokens, i1 = min(i0 + p.rt_tokens, q_len) - 1;
+  int lo0, hi0, lo1, hi1;  // both ends move right with the row
+  chunk_row_keys(p, i0, off, kv, pre, lo0, hi0);
+  chunk_row_keys(p, i1, off, kv, pre, lo1, hi1);
+  kt0 = count = 0;
+  fl = 1;
+  fh = 0;
+  if (p.debug_flags & FA_DEBUG_NO_SKIP) {
+    count = (kv + kKeysPerTile - 1) / kKeysPerTile;
+    return;
+  }
+  if (lo0 > hi1) return;
+  kt0 = lo0 / kKeysPerTile;
+  count = hi1 / kKeysPerTile - kt0 + 1;
+  // FULL: first key at least lo1, last key at most hi0 (which may be negative)
+  fl = (lo1 + kKeysPerTile - 1) / kKeysPerTile - kt0;
+  fh = (hi0 + 1) / kKeysPerTile - 1 - kt0;
+}
+
+// Block-wide exclusive prefix sum; `total` gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[32 + lane] = w;
+  }
+  __syncthreads();
+  total = s_warp[32 + 31];
+  const int r = x - v + (warp ? s_warp[32 + warp - 1] : 0);
+  __syncthreads();
+  return r;
+}
+
+// Number of pieces of a unit of n key tiles cut at T.
+__device__ __forceinline__ int pieces_of(int n, int T) { return n <= T ? 1 : (n + T - 1) / T; }
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ int s_off[kSeqSmem + 1];
+  __shared__ int s_hist[kBins];
+  __shared__ int s_warp[64];
+  __shared__ float s_cost[32];
+  __shared__ int s_T[32];
+  __shared__ int s_nmax, s_slots, s_splits;
+  __shared__ unsigned long long s_work;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool in_smem = p.n_seq <= kSeqSmem;
+  if (tid == 0) {
+    s_nmax = s_slots = s_splits = 0;
+    s_work = 0;
+  }
+  s_hist[tid] = 0;
+
+  // ---- row tiles per sequence; sequences whose lengths do not fit get none
+  int base = 0;
+  for (int s0 = 0; s0 < p.n_seq; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int nt = 0;
+    if (s < p.n_seq) {
+      const int64_t c0 = p.cu_q ? p.cu_q[s] : 0, c1 = p.cu_q ? p.cu_q[s + 1] : p.Sq;
+      const int64_t q_len = c1 - c0, kv = p.kv_len[s];
+      if (c0 < 0 || q_len < 0 || q_len > p.Sq || (p.cu_q && c1 > p.tot_q) || kv < 0 || kv > p.Sk ||
+          (p.prefix && p.prefix[s] < 0))
+        chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)s);
+      else
+        nt = (int)((q_len + p.rt_tokens - 1) / p.rt_tokens);
+    }
+    int total;
+    const int at = base + block_scan(nt, s_warp, total);
+    if (s < p.n_seq) {
+      p.rt_off[s] = at;
+      if (in_smem) s_off[s] = at;
+    }
+    base += total;
+  }
+  // (overlapping cu_seqlens_q could list more tiles than the workspace holds)
+  const int R = min(base, p.max_rtiles);
+  if (base > R && tid == 0) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)p.n_seq);
+  __syncthreads();
+
+  // ---- key tiles of each row tile
+  int nmax = 0;
+  unsigned long long work = 0;
+  for (int r = tid; r < R; r += kPlanThreads) {
+    int lo = 0, hi = p.n_seq;  // the last sequence whose first tile is at or before r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((in_smem ? s_off[mid] : p.rt_off[mid]) <= r) lo = mid;
+      else hi = mid;
+    }
+    const int rt = r - (in_smem ? s_off[lo] : p.rt_off[lo]);
+    int kt0, n, fl, fh;
+    row_tile_keys(p, lo, rt, kt0, n, fl, fh);
+    p.rtiles[r] = make_int4(lo, rt, kt0, n);
+    nmax = max(nmax, n);
+    work += n;
+  }
+  atomicMax(&s_nmax, nmax);
+  atomicAdd(&s_work, work);
+  __syncthreads();
+  nmax = s_nmax;
+  work = s_work * p.n_hg;
+
+  // ---- the length T: one candidate per warp.  A round of the grid takes as
+  // long as its longest piece; t0 tiles each would fill one round evenly, so
+  // the candidates are whole units, t0 up to twice as much (one round with room
+  // for the units' odd lengths), and the same for two, three and four rounds.
+  {
+    const float P = (float)p.grid;
+    const int t0 = (int)((work + p.grid - 1) / p.grid);
+    float f = 0.f;
+    if (warp >= 1 && warp <= 16) f = 1.f + (warp - 1) / 16.f;
+    else if (warp <= 24) f = (1.f + (warp - 17) / 8.f) / 2.f;
+    else if (warp <= 28) f = (1.f + (warp - 25) / 4.f) / 3.f;
+    else f = (1.f + (warp - 29) / 4.f) / 4.f;
+    int T = warp == 0 ? nmax : (int)ceilf(f * t0);
+    T = max(1, min(T, nmax));
+    float cost = 3e38f;
+    if (warp == 0 || (T < nmax && p.max_slots > 0)) {
+      int m = 0, part = 0, longest = 0;
+      for (int r = lane; r < R; r += 32) {
+        const int n = p.rtiles[r].w, k = pieces_of(n, T);
+        m += k;
+        if (k > 1) part += k;
+        longest = max(longest, (n + k - 1) / k);
+      }
+      m = __reduce_add_sync(0xffffffffu, m) * p.n_hg;
+      part = __reduce_add_sync(0xffffffffu, part) * p.n_hg;
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      const float total = (float)work + kPieceCost * m + kPartialCost * part;
+      const float rounds = ceilf(m / P);
+      if (m > 0)
+        cost = fmaxf(longest + kPieceCost, total / P) + (rounds - m / P) * total / m + (part ? kJoinCost : 0.f);
+      if (part > p.max_slots) cost = 3e38f;
+    }
+    if (lane == 0) {
+      s_cost[warp] = cost;
+      s_T[warp] = T;
+    }
+  }
+  __syncthreads();
+  int T = s_T[0];
+  float best = s_cost[0];
+  for (int w = 1; w < 32; ++w)
+    if (s_cost[w] < best) {
+      best = s_cost[w];
+      T = s_T[w];
+    }
+
+  // ---- list the pieces, longest first (a counting sort by length)
+  int shift = 0;
+  while ((T >> shift) >= kBins) ++shift;
+  auto bin_of = [&](int len) { return kBins - 1 - (len >> shift); };
+  for (int r = tid; r < R; r += kPlanThreads) {
+    const int n = p.rtiles[r].w, k = pieces_of(n, T), len = n / k, more = n - len * k;
+    if (more) atomicAdd(&s_hist[bin_of(len + 1)], more * p.n_hg);
+    atomicAdd(&s_hist[bin_of(len)], (k - more) * p.n_hg);
+  }
+  __syncthreads();
+  int total;
+  const int start = block_scan(s_hist[tid], s_warp, total);
+  s_hist[tid] = start;
+  __syncthreads();
+  const int64_t units = (int64_t)R * p.n_hg;
+  for (int64_t u = tid; u < units; u += kPlanThreads) {
+    const int r = (int)(u / p.n_hg), hg = (int)(u - (int64_t)r * p.n_hg);
+    const int4 t = p.rtiles[r];
+    int kt0, n, fl, fh;
+    row_tile_keys(p, t.x, t.y, kt0, n, fl, fh);
+    const int k = pieces_of(n, T), len = n / k, more = n - len * k;
+    int slot0 = -1;
+    if (k > 1) {
+      slot0 = atomicAdd(&s_slots, k);
+      ChunkSplit sp;
+      sp.b = t.x; sp.rt = t.y; sp.hg = hg; sp.slot0 = slot0; sp.n = k;
+      sp.pad[0] = sp.pad[1] = sp.pad[2] = 0;
+      p.splits[atomicAdd(&s_splits, 1)] = sp;
+    }
+    int done = 0;
+    for (int i = 0; i < k; ++i) {
+      const int c = len + (i < more ? 1 : 0);
+      ChunkPiece pc;
+      pc.b = t.x; pc.rt = t.y; pc.hg = hg; pc.kt0 = kt0 + done; pc.count = c;
+      pc.slot = k > 1 ? slot0 + i : -1;
+      pc.fl = fl - done; pc.fh = fh - done;
+      p.pieces[atomicAdd(&s_hist[bin_of(c)], 1)] = pc;
+      done += c;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    ChunkCounts c;
+    c.n_pieces = total; c.n_slots = s_slots; c.n_splits = s_splits; c.n_rtiles = R;
+    *p.counts = c;
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (F16) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  } else {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+}
+
+// One warp per row of a split unit: the weights of its pieces from their
+// log-sum-exps, then the weighted sum of their rows (a lane holds D / 32
+// columns).  Bound by L2 reads of the partials, 4 D bytes per row and piece.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int n_warps = gridDim.x * 8;
+  const int n_rows = p.counts->n_splits * kChunkRows;
+  for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < n_rows; w += n_warps) {
+    const ChunkSplit sp = p.splits[w / kChunkRows];
+    const int row = w % kChunkRows;
+    const int tok = fast_div(row, p.div_gp), i = sp.rt * p.rt_tokens + tok;
+    if (tok >= p.rt_tokens || i >= chunk_qlen(p, sp.b)) continue;
+    const int h = sp.hg * p.gp + row - tok * p.gp;
+    float mx = -INFINITY;
+    for (int k = lane; k < sp.n; k += 32) mx = fmaxf(mx, p.part_lse[(int64_t)(sp.slot0 + k) * kChunkRows + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float acc[kPer], sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+    if (mx != -INFINITY) {
+      const float* po = p.part_o + ((int64_t)sp.slot0 * kChunkRows + row) * D + lane * kPer;
+      const float* pl = p.part_lse + (int64_t)sp.slot0 * kChunkRows + row;
+#pragma unroll 4
+      for (int k = 0; k < sp.n; ++k) {
+        const float f = fast_exp2(pl[(int64_t)k * kChunkRows] - mx);
+        sum += f;
+        const float* src = po + (int64_t)k * kChunkRows * D;
+        if constexpr (kPer == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] += f * v.x; acc[1] += f * v.y; acc[2] += f * v.z; acc[3] += f * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] += f * v.x; acc[1] += f * v.y;
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t qrow = (p.cu_q ? p.cu_q[sp.b] : 0) + i, ob = p.cu_q ? 0 : sp.b;
+    uint16_t* o = p.o + ob * p.o_sb + qrow * p.o_ss + (int64_t)h * p.o_sh + lane * kPer;
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2) reinterpret_cast<uint32_t*>(o)[c / 2] = pack2<F16>(acc[c] * inv, acc[c + 1] * inv);
+    if (lane == 0)
+      p.lse[ob * p.lse_sb + (int64_t)h * p.lse_sh + qrow * p.lse_ss] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 152;
+  }
+  const int n = cached[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+    cudaGetLastError();
+    return 152;
+  }
+  cached[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
+// Arguments checked, geometry and workspace laid out (offsets from `base`,
+// which may be null for a plan).
+int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_tensor* out, const fa_tensor* lse,
+               const fa_tensor* cu_q, const fa_tensor* seqlens_k, const fa_tensor* block_table,
+               const fa_tensor* prefix, int32_t wl, int32_t wr, float softcap, float scale, int32_t causal,
+               const fa_opts* opts, ChunkParams* P, fa_plan* pub) {
+  if (!q || !k || !v || !out || !lse || !seqlens_k || !opts) return FA_ERR_INVALID_ARG;
+  memset(P, 0, sizeof(*P));
+  memset(pub, 0, sizeof(*pub));
+  ChunkParams& p = *P;
+  int rc;
+  const int nd = cu_q ? 3 : 4;
+  if ((rc = check_bf16(q, nd)) || (rc = check_bf16(out, nd)) || (rc = check_bf16(k, 4)) || (rc = check_bf16(v, 4)))
+    return rc;
+  int64_t n_seq, Sq;
+  if (cu_q) {
+    if (cu_q->ndim != 1 || cu_q->shape[0] < 1) return FA_ERR_INVALID_ARG;
+    n_seq = cu_q->shape[0] - 1;
+    if ((rc = check_i32_vec(cu_q, n_seq + 1))) return rc;
+    Sq = opts->max_seqlen_q;
+    if (Sq < 0 || (Sq == 0 && q->shape[0] > 0)) return FA_ERR_INVALID_ARG;
+    p.cu_q = static_cast<const int32_t*>(cu_q->data);
+    p.tot_q = q->shape[0];
+    p.q_sb = q->stride[0]; p.q_ss = q->stride[0]; p.q_sh = q->stride[1];
+    p.o_sb = 0; p.o_ss = out->stride[0]; p.o_sh = out->stride[1];
+  } else {
+    n_seq = q->shape[0];
+    Sq = q->shape[1];
+    p.q_sb = q->stride[0]; p.q_ss = q->stride[1]; p.q_sh = q->stride[2];
+    p.o_sb = out->stride[0]; p.o_ss = out->stride[1]; p.o_sh = out->stride[2];
+  }
+  const int64_t Hq = q->shape[nd - 2], d = q->shape[nd - 1], Hkv = k->shape[2], Sk = opts->max_seqlen_k;
+  if ((d != 64 && d != 128) || k->shape[3] != d || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (n_seq > INT32_MAX / 64 || Sq > INT32_MAX / 64 || Sk < 0 || Sk > INT32_MAX / 64 || Hq > INT32_MAX / 1024)
+    return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < nd; ++i) {
+    if (out->shape[i] != q->shape[i]) return FA_ERR_INVALID_ARG;
+    if (out->shape[i] > 1 && out->stride[i] == 0) return FA_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < 4; ++i)
+    if (v->shape[i] != k->shape[i]) return FA_ERR_INVALID_ARG;
+  if (k->dtype != q->dtype || v->dtype != q->dtype || out->dtype != q->dtype) return FA_ERR_INVALID_ARG;
+  if ((rc = check_i32_vec(seqlens_k, n_seq))) return rc;
+  if (prefix && ((rc = check_i32_vec(prefix, n_seq)) || !causal)) return FA_ERR_INVALID_ARG;
+  // ---- LSE
+  if (!lse->data || lse->dtype != FA_DTYPE_F32 || (reinterpret_cast<uintptr_t>(lse->data) & 3u) != 0)
+    return FA_ERR_INVALID_ARG;
+  if (cu_q) {
+    if (lse->ndim != 2 || lse->shape[0] != Hq || lse->shape[1] != p.tot_q) return FA_ERR_INVALID_ARG;
+    p.lse_sb = 0; p.lse_sh = lse->stride[0]; p.lse_ss = lse->stride[1];
+  } else {
+    if (lse->ndim != 3 || lse->shape[0] != n_seq || lse->shape[1] != Hq || lse->shape[2] != Sq)
+      return FA_ERR_INVALID_ARG;
+    p.lse_sb = lse->stride[0]; p.lse_sh = lse->stride[1]; p.lse_ss = lse->stride[2];
+  }
+  // ---- cache
+  if (block_table) {
+    const int64_t page = k->shape[1];
+    if (!block_table->data || block_table->dtype != FA_DTYPE_I32 || block_table->ndim != 2 ||
+        block_table->shape[0] != n_seq || block_table->stride[1] != 1 || block_table->stride[0] < 0 ||
+        block_table->shape[1] < 1 || page < 1 || page > INT32_MAX / 2 || k->shape[0] > INT32_MAX)
+      return FA_ERR_INVALID_ARG;
+    if (Sk > block_table->shape[1] * page || (Sk > 0 && k->shape[0] == 0)) return FA_ERR_INVALID_ARG;
+    p.block_table = static_cast<const int32_t*>(block_table->data);
+    p.bt_stride = block_table->stride[0];
+    p.page_size = (int32_t)page;
+    p.num_pages = (int32_t)k->shape[0];
+    // rows per copy: the largest power of two that divides a page and a tile
+    p.box_rows = (int32_t)std::min<int64_t>(page & -page, kKeysPerTile);
+  } else {
+    // a padded cache is one page per sequence
+    if (k->shape[0] != n_seq || Sk > k->shape[1]) return FA_ERR_INVALID_ARG;
+    p.page_size = INT32_MAX / 2;
+    p.num_pages = (int32_t)n_seq;
+    p.box_rows = kKeysPerTile;
+  }
+  p.div_page = make_fastdiv((uint32_t)p.page_size);
+  p.cache_rows = k->shape[1];
+  p.cache_outer = k->shape[0];
+  // TMA reads q and the cache: no stride of 0 along more than one element
+  const fa_tensor* in[3] = {q, k, v};
+  for (const fa_tensor* t : in)
+    for (int i = 0; i < t->ndim; ++i)
+      if (t->shape[i] > 1 && t->stride[i] == 0) return FA_ERR_UNSUPPORTED;
+  p.k_sb = k->stride[0]; p.k_ss = k->stride[1]; p.k_sh = k->stride[2];
+  p.v_sb = v->stride[0]; p.v_ss = v->stride[1]; p.v_sh = v->stride[2];
+  // ---- scalars
+  if (wl < -1 || wr < -1 || !(softcap >= 0.f) || !std::isfinite(softcap) || !std::isfinite(scale))
+    return FA_ERR_INVALID_ARG;
+  if (scale <= 0.f) scale = 1.0f / std::sqrt((float)d);
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.k = static_cast<const uint16_t*>(k->data);
+  p.v = static_cast<const uint16_t*>(v->data);
+  p.o = static_cast<uint16_t*>(out->data);
+  p.lse = static_cast<float*>(lse->data);
+  p.kv_len = static_cast<const int32_t*>(seqlens_k->data);
+  p.prefix = prefix ? static_cast<const int32_t*>(prefix->data) : nullptr;
+  p.n_seq = (int32_t)n_seq;
+  p.Sq = (int32_t)Sq;
+  p.Sk = (int32_t)Sk;
+  p.Hq = (int32_t)Hq;
+  p.G = (int32_t)(Hq / Hkv);
+  p.d = (int32_t)d;
+  p.f16 = q->dtype == FA_DTYPE_F16;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.softcap = softcap;
+  p.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
+  p.alibi = static_cast<const float*>(opts->alibi_slopes);
+  p.causal = causal ? 1 : 0;
+  // (lengths stay below 2^25, so a wider window is no window; sums with it stay in 32 bits)
+  p.wl = std::min(wl, 1 << 30);
+  p.wr = std::min(wr, 1 << 30);
+  p.debug_flags = opts->debug_flags;
+  // q-heads packed into a query tile: as many of a K/V head's as divide them
+  // and leave at most an eighth of the tile empty
+  p.gp = 1;
+  for (int g = 1; g <= p.G && g <= kChunkRows; ++g)
+    if (p.G % g == 0 && g * (kChunkRows / g) >= 112) p.gp = g;
+  p.rt_tokens = kChunkRows / p.gp;
+  p.n_hg = p.Hq / p.gp;
+  p.div_gp = make_fastdiv((uint32_t)p.gp);
+
+  // ---- bounds of the work, workspace
+  int64_t rtiles = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens);
+  if (cu_q) rtiles = std::min(rtiles, p.tot_q / p.rt_tokens + n_seq);
+  if (rtiles * p.n_hg > (1 << 27)) return FA_ERR_INVALID_ARG;
+  const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
+  const int64_t ctas = (int64_t)sm_count() * chunk_ctas_per_sm(p.d);
+  // partials: at most two rounds of the grid, and no more than all tiles alone
+  const int64_t slots = n_kt > 1 ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
+  const int64_t pieces = units + slots;
+  p.max_rtiles = (int32_t)rtiles;
+  p.max_slots = (int32_t)slots;
+  p.grid = (int32_t)std::min<int64_t>(ctas, std::max<int64_t>(1, pieces));
+  size_t off = kWsHeadBytes;
+  unsigned char* base = static_cast<unsigned char*>(opts->workspace);
+  auto take = [&](size_t bytes) {
+    unsigned char* at = base + off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  p.ws = reinterpret_cast<WsHeader*>(base);
+  p.counts = reinterpret_cast<ChunkCounts*>(take(sizeof(ChunkCounts)));
+  p.rt_off = reinterpret_cast<int32_t*>(take((size_t)(n_seq + 1) * 4));
+  p.rtiles = reinterpret_cast<int4*>(take((size_t)rtiles * sizeof(int4)));
+  p.pieces = reinterpret_cast<ChunkPiece*>(take((size_t)pieces * sizeof(ChunkPiece)));
+  p.splits = reinterpret_cast<ChunkSplit*>(take((size_t)(slots / 2) * sizeof(ChunkSplit)));
+  p.part_lse = reinterpret_cast<float*>(take((size_t)slots * kChunkRows * 4));
+  p.part_o = reinterpret_cast<float*>(take((size_t)slots * kChunkRows * d * 4));
+
+  pub->path = FA_PATH_PREFILL;
+  pub->n_seq = p.n_seq;
+  pub->n_heads_sched = p.n_hg;
+  pub->n_row_tiles = (int32_t)((Sq + p.rt_tokens - 1) / p.rt_tokens);
+  pub->rows_per_tile = p.rt_tokens;
+  pub->keys_per_tile = kKeysPerTile;
+  pub->n_k_tiles = (int32_t)n_kt;
+  pub->n_splits = p.max_slots;
+  pub->n_items = units;
+  pub->n_kernels = units > 0 ? 2 + (slots > 0) : 0;
+  pub->workspace_bytes = off;
+  return FA_OK;
+}
+
+template <int D, bool F16>
+void launch_join(const ChunkParams& p, cudaStream_t st) {
+  const int64_t warps = (int64_t)p.max_slots / 2 * kChunkRows;
+  const int blocks = (int)std::min<int64_t>((warps + 7) / 8, 152 * 4);
+  chunk_join_kernel<D, F16><<<blocks, 256, 0, st>>>(p);
+}
+
+}  // namespace
+}  // namespace mfa
+
+using namespace mfa;
+
+extern "C" {
+
+int fa_fwd_chunk(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* out,
+                 const fa_tensor* lse, const fa_tensor* cu_seqlens_q, const fa_tensor* seqlens_k,
+                 const fa_tensor* block_table, const fa_tensor* prefix_lens, int32_t window_left,
+                 int32_t window_right, float softcap, float scale, int32_t causal, const fa_opts* opts) {
+  ChunkParams p;
+  fa_plan pub;
+  int rc = plan_chunk(q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens, window_left,
+                      window_right, softcap, scale, causal, opts, &p, &pub);
+  if (rc != FA_OK) return rc;
+  if (!opts->workspace || (reinterpret_cast<uintptr_t>(opts->workspace) % kAlign) != 0 ||
+      opts->workspace_bytes < pub.workspace_bytes)
+    return FA_ERR_WORKSPACE;
+  if ((rc = check_device()) != FA_OK) return rc;
+  TraceRange tr("mfa.fwd_chunk");
+  cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
+  cudaError_t e = cudaSuccess;
+  auto record = [&](void* ev) {
+    if (e == cudaSuccess && ev) e = cudaEventRecord(static_cast<cudaEvent_t>(ev), st);
+  };
+  const bool any = pub.n_items > 0;
+  if (any) {
+    chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+    e = cudaGetLastError();
+  }
+  record(opts->event_begin);
+  if (any && e == cudaSuccess) e = p.f16 ? launch_chunk_attn_f16(p, st) : launch_chunk_attn(p, st);
+  record(opts->event_attn_end);
+  if (any && e == cudaSuccess && p.max_slots > 0) {
+    if (p.d == 64) p.f16 ? launch_join<64, true>(p, st) : launch_join<64, false>(p, st);
+    else p.f16 ? launch_join<128, true>(p, st) : launch_join<128, false>(p, st);
+    e = cudaGetLastError();
+  }
+  record(opts->event_end);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* out,
+                      const fa_tensor* lse, const fa_tensor* cu_seqlens_q, const fa_tensor* seqlens_k,
+                      const fa_tensor* block_table, const fa_tensor* prefix_lens, int32_t window_left,
+                      int32_t window_right, float softcap, float scale, int32_t causal, const fa_opts* opts,
+                      fa_plan* plan_out) {
+  ChunkParams p;
+  fa_plan pub;
+  int rc = plan_chunk(q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens, window_left,
+                      window_right, softcap, scale, causal, opts, &p, &pub);
+  if (rc == FA_OK && plan_out) *plan_out = pub;
+  return rc;
+}
+
+}  // extern "C"

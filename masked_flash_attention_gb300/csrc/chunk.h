@@ -1,0 +1,92 @@
+// chunk.h -- parameters of fa_fwd_chunk, shared by its planner, its attention
+// kernel and its combine kernel.
+#pragma once
+
+#include <cstdint>
+
+#include "fa_internal.h"
+
+namespace mfa {
+
+constexpr int kChunkRows = 128;  // rows of a query tile (tcgen05 M)
+
+// A piece of work: one query tile of one group of q-heads over a run of key
+// tiles (two 16-byte words in the workspace).
+struct ChunkPiece {
+  int32_t b, rt, hg;   // sequence, row tile, head group
+  int32_t kt0, count;  // key tiles kt0 .. kt0 + count - 1
+  int32_t slot;        // where its partial rows go; -1: it holds all the unit's keys
+  int32_t fl, fh;      // tiles kt0 + fl .. kt0 + fh are FULL, the others PARTIAL
+};
+static_assert(sizeof(ChunkPiece) == 32, "two 16-byte loads");
+
+// A unit whose keys were split: its pieces' partials are slots slot0 .. slot0 + n - 1.
+struct ChunkSplit {
+  int32_t b, rt, hg, slot0, n, pad[3];
+};
+
+struct ChunkCounts {
+  int32_t n_pieces, n_slots, n_splits, n_rtiles;
+};
+
+// A query tile's 128 rows are (token, q-head) pairs: `rt_tokens` tokens of `gp`
+// q-heads that share a K/V head, row = token * gp + head, so that a K/V tile
+// is read once for all of them and a few tokens still fill the tile.
+struct ChunkParams {
+  uint16_t* o;
+  float* lse;
+  int64_t o_sb, o_ss, o_sh, lse_sb, lse_sh, lse_ss;
+  const int32_t* cu_q;         // nullable
+  const int32_t* kv_len;       // [n_seq]
+  const int32_t* prefix;       // nullable [n_seq]
+  const int32_t* block_table;  // nullable: padded cache
+  int64_t bt_stride;
+  int32_t page_size, num_pages, box_rows;
+  FastDiv div_page;
+  int32_t n_seq, Sq, Sk;  // Sq/Sk: fixed or maximum lengths
+  int64_t tot_q;
+  int32_t Hq, G, gp, rt_tokens, n_hg;  // G = Hq / Hkv; n_hg = Hq / gp
+  FastDiv div_gp;
+  int32_t d, f16;
+  float scale, scale_log2, softcap, inv_softcap;
+  const float* alibi;
+  int32_t causal, wl, wr;
+  uint32_t debug_flags;
+  // workspace
+  WsHeader* ws;
+  ChunkCounts* counts;
+  int32_t* rt_off;    // [n_seq + 1] first row tile of each sequence
+  int4* rtiles;       // [max_rtiles] {sequence, row tile, first key tile, key tiles}
+  ChunkPiece* pieces;
+  ChunkSplit* splits;
+  float* part_o;      // [max_slots][128][d]
+  float* part_lse;    // [max_slots][128] log2 units
+  int32_t max_rtiles, max_slots, grid;
+  // layouts for the tensor maps (element strides)
+  const uint16_t *q, *k, *v;
+  int64_t q_sb, q_ss, q_sh, k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;
+  int64_t cache_rows, cache_outer;  // page_size x num_pages, or cap x n_seq
+};
+
+cudaError_t launch_chunk_attn(const ChunkParams& p, cudaStream_t st);      // bf16
+cudaError_t launch_chunk_attn_f16(const ChunkParams& p, cudaStream_t st);  // fp16
+int chunk_ctas_per_sm(int d);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int chunk_qlen(const ChunkParams& p, int b) {
+  return p.cu_q ? (p.cu_q[b + 1] - p.cu_q[b]) : p.Sq;
+}
+
+// Keys [lo, hi] that query row i (token) of a sequence may see: the pair rules
+// of fa_fwd, with the first `prefix` keys exempt from the causal one.
+__device__ __forceinline__ void chunk_row_keys(const ChunkParams& p, int i, int off, int kv_len, int prefix, int& lo,
+                                               int& hi) {
+  lo = 0;
+  hi = kv_len - 1;
+  if (p.causal) hi = min(hi, max(i + off, prefix - 1));
+  if (p.wl >= 0) lo = max(lo, i + off - p.wl);
+  if (p.wr >= 0) hi = min(hi, i + off + p.wr);
+}
+#endif
+
+}  // namespace mfa

@@ -1,0 +1,345 @@
+"""GPU tests of fa_fwd_chunk against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from chunk_util import BF, DEV, H, assert_close, case, check, dev, oracle, rnd, run
+
+pytestmark = pytest.mark.gpu
+
+
+def fa():
+    import masked_flash_attention_gb300 as m
+    return m
+
+
+def test_one_token_one_tile():
+    check(case(0, [1], [100], hq=4, hkv=1, page=16))
+
+
+@pytest.mark.parametrize("page", [16, 64, 128, 256, 24, 8, 5, 2, 1, None])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, H)])
+def test_pages(page, d, dtype):
+    """Lengths on, before and after the edges of tiles, pages and MMA steps; a
+    sequence without new tokens, one without keys, one with a single key."""
+    check(case(1, [3, 1, 0, 130, 2, 1, 17], [127, 128, 50, 129, 0, 1, 300], page=page, d=d, dtype=dtype, hq=6, hkv=2), f"page {page}")
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (5, 5), (8, 2), (5, 1), (12, 2), (14, 2), (32, 1), (40, 1), (64, 1), (130, 1), (22, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_heads(hq, hkv, d):
+    check(case(2, [1, 33, 70], [200, 33, 310], hq=hq, hkv=hkv, d=d, dtype=H if hq % 2 else BF), f"{hq}/{hkv}")
+
+
+@pytest.mark.parametrize("i,params", list(enumerate([
+    dict(causal=False), dict(window_left=0), dict(window_left=100), dict(window_left=40, window_right=0, softcap=20.0),
+    dict(causal=False, window_left=30, window_right=90), dict(causal=False, window_right=5), dict(softcap=30.0),
+    dict(scale=0.3), dict(window_left=2**31 - 1, window_right=2**31 - 1)])))
+@pytest.mark.parametrize("d", [64, 128])
+def test_masks(i, params, d):
+    check(case(10 + i, [40, 1, 200, 300], [400, 350, 200, 290], d=d, page=16), str(params), logits=4.0, **params)
+
+
+@pytest.mark.parametrize("params", [{}, dict(softcap=15.0), dict(causal=False, window_right=20), dict(window_left=150)])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, H)])
+def test_alibi(params, d, dtype):
+    slopes = torch.tensor([2.0 ** -(h + 1) for h in range(6)])
+    c = case(30, [64, 1, 150], [400, 500, 150], hq=6, hkv=2, d=d, dtype=dtype)
+    out, lse, _ = run(c, alibi_slopes=slopes, **params)
+    assert_close(out, lse, oracle(c, alibi_slopes=slopes, **params), str(params), logits=2.0, n_keys=500)
+
+
+@pytest.mark.parametrize("params", [{}, dict(window_left=100), dict(softcap=30.0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix(params, d):
+    c = case(40, [50, 200, 1, 130, 90, 10], [300, 200, 129, 260, 90, 400], d=d, page=16)
+    pre = torch.tensor([0, 150, 40, 260, 1000, 395], dtype=torch.int32)
+    check(c, str(params), prefix_lens=pre, **params)
+
+
+def test_rows_without_keys():
+    """More rows than keys, and windows that leave some rows nothing: 0 and -inf
+    there, and the other rows of the same tiles right."""
+    c = case(50, [150, 40, 5], [20, 0, 3], d=128)
+    out, lse = check(c)
+    assert (out[:130] == 0).all() and torch.isneginf(lse[:, :130]).all()
+    c = case(51, [30], [300], d=64)
+    out, lse = check(c, causal=False, window_left=-1, window_right=0)
+    c = case(52, [300], [130], d=64)
+    check(c, causal=False, window_left=10)  # the last rows' windows end before the first row's begin
+    check(c, window_left=10)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 1), (64, 1, 1), (64, 12, 12)])
+def test_long_caches_are_split(d, hq, hkv):
+    """Few units over many key tiles: split along the keys and joined; long and
+    short sequences side by side."""
+    c = case(60, [1, 40, 7], [9000, 5000, 100], hq=hq, hkv=hkv, d=d, page=32)
+    out, lse, ws = run(c)
+    assert_close(out, lse, oracle(c), n_keys=9000)
+    counts = ws[256:272].view(torch.int32).tolist()
+    assert counts[2] > 0 and counts[1] >= 2 * counts[2], counts
+    # a row none of whose keys lie in some pieces
+    c = case(61, [3], [7000], hq=hq, hkv=hkv, d=d, page=32)
+    check(c, window_left=300)
+    check(c, causal=False, window_right=10)
+
+
+def test_many_sequences_and_empty_ones():
+    rng = np.random.default_rng(7)
+    q_lens = rng.integers(0, 3, 3000).tolist()
+    kv = rng.integers(0, 60, 3000).tolist()
+    check(case(70, q_lens, kv, hq=2, hkv=1, d=64, page=8))
+
+
+def test_large_logits():
+    """Rows whose maxima grow by far more than 2^8 from tile to tile (the
+    reference is raised and O rescaled), and fall again."""
+    for d, dtype in ((128, BF), (64, H)):
+        c = case(80, [70, 2], [600, 900], d=d, dtype=dtype)
+        ramp = torch.linspace(0.05, 4.0, 16)
+        bt = c["bt"]
+        for s in range(2):
+            for p in range(bt.shape[1]):
+                if bt[s, p] >= 0:
+                    c["kc"][int(bt[s, p])] *= ramp[p % 16].item()
+        # scale 1 and keys up to 4 times as large: a logit is off by up to 128 * 6e-8 * 82 * 4 = 2.5e-3
+        check(c, f"ramp {d}", logits=30.0, scale=1.0)
+
+
+def test_fixed_length_queries_and_padded_cache():
+    check(case(90, [9, 9, 9], [100, 9, 33], page=None, d=64, fixed=True))
+    check(case(91, [130, 130], [300, 130], page=16, d=128, fixed=True))
+
+
+def test_strides_and_untouched_rows():
+    """q, out, LSE and cache as slices of wider tensors; rows of no sequence and
+    the columns between stay as they were."""
+    c = case(100, [5, 60], [80, 61], hq=4, hkv=2, d=64, page=8, extra=(3, 4))
+    out, lse, _ = run(c, fill=7.0)
+    ref = oracle(c)
+    assert_close(out, lse, ref)
+    assert (out[:3] == 7).all() and (out[-4:] == 7).all() and (lse[:, :3] == 7).all() and (lse[:, -4:] == 7).all()
+    m = fa()
+    wide_q = torch.full((72, 4 + 3, 64 + 16), float("nan"), dtype=BF, device=DEV)
+    wide_q[:, :4, :64] = c["q"].to(DEV)
+    wide_o = torch.full((72, 9, 64 + 8), 7.0, dtype=BF, device=DEV)
+    wide_l = torch.full((72, 8), 7.0, device=DEV)
+    n_pages, page = c["kc"].shape[:2]
+    wide_c = torch.full((n_pages, 2, page, 2, 64), float("nan"), dtype=BF, device=DEV)  # k and v pages in one pool
+    wide_c[:, 0], wide_c[:, 1] = c["kc"].to(DEV), c["vc"].to(DEV)
+    o2, l2, ws = m.fa_fwd_chunk(wide_q[:, :4, :64], wide_c[:, 0], wide_c[:, 1], dev(c["lens"]), out=wide_o[:, 2:6, :64],
+                                lse=wide_l[:, 1:5].T, cu_seqlens_q=dev(c["cu"]), block_table=dev(c["bt"]), max_seqlen_q=60,
+                                max_seqlen_k=80)
+    assert m.fa_check_device_error(ws) == (0, 0)
+    assert torch.equal(o2[3:68], out[3:68]) and torch.equal(l2[:, 3:68], lse[:, 3:68])
+    assert (wide_o[:, :2] == 7).all() and (wide_o[:, 6:] == 7).all() and (wide_o[:, :, 64:] == 7).all() and (wide_o[:3] == 7).all()
+    assert (wide_l[:, 0] == 7).all() and (wide_l[:, 5:] == 7).all()
+
+
+def test_heads_major_cache():
+    """A cache [pages, Hkv, page, d] seen as [pages, page, Hkv, d]."""
+    c = case(101, [20, 1], [200, 77], d=128)
+    out, lse, _ = run(c)
+    c2 = dict(c)
+    c2["kc"], c2["vc"] = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in (c["kc"], c["vc"])]
+    m = fa()
+    o2, l2, _ = m.fa_fwd_chunk(dev(c["q"]), c["kc"].transpose(1, 2).contiguous().to(DEV).transpose(1, 2),
+                               c["vc"].transpose(1, 2).contiguous().to(DEV).transpose(1, 2), dev(c["lens"]),
+                               cu_seqlens_q=dev(c["cu"]), block_table=dev(c["bt"]), max_seqlen_q=20, max_seqlen_k=200)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_same_bits_again_and_without_skipping():
+    m = fa()
+    c = case(110, [1, 200, 40], [5000, 900, 1000], d=128)
+    a = run(c)
+    for _ in range(3):
+        b = run(c, workspace=a[2])
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # every tile scheduled as PARTIAL: other splits, the same values
+    out, lse, _ = run(c, debug_flags=m.FA_DEBUG_NO_SKIP, window_left=500)
+    assert_close(out, lse, oracle(c, window_left=500), n_keys=5000)
+
+
+def test_lengths_and_pages_that_do_not_fit():
+    m = fa()
+    BOUNDS = m._lib.FA_ERR_DEVICE_BOUNDS
+    c = case(120, [4, 30, 6], [60, 200, 50], d=128)
+    ref = oracle(c, seqs=[0, 2])
+    for field, value in (("lens", 201), ("lens", -1), ("prefix", -1)):
+        c2 = dict(c, lens=c["lens"].clone())
+        kw = {}
+        if field == "lens":
+            c2["lens"][1] = value
+        else:
+            kw["prefix_lens"] = torch.tensor([0, value, 0], dtype=torch.int32)
+        out, lse, ws = run(c2, check=False, fill=7.0, **kw)
+        assert m.fa_check_device_error(ws) == (BOUNDS, 1)
+        assert m.fa_check_device_error(ws) == (0, 0)
+        assert_close(out, lse, ref)
+        assert (out[4:34] == 7).all() and (lse[:, 4:34] == 7).all()
+    # a chunk longer than max_seqlen_q; prefix sums that run backwards or past the rows
+    out, lse, ws = run(dict(c, max_q=20), check=False, fill=7.0)
+    assert m.fa_check_device_error(ws) == (BOUNDS, 1)
+    assert_close(out, lse, ref)
+    for cu in ([0, 4, 2, 40], [0, 4, 4, 41], [-1, 4, 4, 10]):
+        out, lse, ws = run(dict(c, cu=torch.tensor(cu, dtype=torch.int32)), check=False, fill=7.0)
+        assert m.fa_check_device_error(ws)[0] == BOUNDS
+    # pages outside the cache: recorded, the other sequences right
+    for page in (-1, c["kc"].shape[0], 2**31 - 1):
+        c2 = dict(c, bt=c["bt"].clone())
+        c2["bt"][1, 3] = page
+        out, lse, ws = run(c2, check=False)
+        rc, info = m.fa_check_device_error(ws)
+        assert rc == BOUNDS and info == page % 2**32
+        assert_close(out, lse, ref)
+
+
+def test_small_workspace_and_misaligned_arguments():
+    m = fa()
+    c = case(125, [4], [60])
+    with pytest.raises(m.FaError) as e:
+        run(c, workspace=torch.zeros(512, dtype=torch.uint8, device=DEV))
+    assert e.value.status == m._lib.FA_ERR_WORKSPACE
+    with pytest.raises(m.FaError) as e:
+        run(c, alibi_slopes=torch.zeros(3))
+    assert e.value.status == m._lib.FA_ERR_INVALID_ARG
+
+
+def test_wait_that_runs_out_is_reported():
+    """The first key tile is never sent (FA_DEBUG_WITHHOLD): the bounded waits
+    give up, the status is reported, and the next call on the workspace is right."""
+    m = fa()
+    c = case(126, [4, 30], [60, 200])
+    _, _, ws = run(c, check=False, debug_flags=m.FA_DEBUG_WITHHOLD)
+    assert m.fa_check_device_error(ws)[0] == m._lib.FA_ERR_DEVICE_TIMEOUT
+    out, lse, _ = run(c, workspace=ws)
+    assert_close(out, lse, oracle(c))
+
+
+def test_far_pages():
+    """Pages beyond 2^31 elements of the cache: the append writes them, the attention reads them."""
+    m = fa()
+    hkv, d, page = 8, 128, 64
+    n_pages = 2**31 // (page * hkv * d) + 4
+    kc = torch.empty(n_pages, page, hkv, d, dtype=BF, device=DEV)
+    vc = torch.empty(n_pages, page, hkv, d, dtype=BF, device=DEV)
+    g = torch.Generator().manual_seed(130)
+    n = 150
+    bt = torch.tensor([[n_pages - 1, 1, n_pages - 3]], dtype=torch.int32)
+    q, k, v = rnd(g, n, 8, d), rnd(g, n, hkv, d), rnd(g, n, hkv, d)
+    cu = torch.tensor([0, n], dtype=torch.int32)
+    _, lens, _ = m.fa_kvcache_append(k.to(DEV), v.to(DEV), kc, vc, torch.zeros(1, dtype=torch.int32, device=DEV),
+                                     cu_seqlens_q=cu.to(DEV), block_table=bt.to(DEV))
+    out, lse, _ = m.fa_fwd_chunk(q.to(DEV), kc, vc, lens, cu_seqlens_q=cu.to(DEV), block_table=bt.to(DEV), max_seqlen_q=n,
+                                 max_seqlen_k=n)
+    small = torch.zeros(3, page, hkv, d, dtype=BF)
+    small_v = torch.zeros(3, page, hkv, d, dtype=BF)
+    for p in range(3):
+        part = k[p * page:(p + 1) * page]
+        small[p, :len(part)], small_v[p, :len(part)] = part, v[p * page:(p + 1) * page]
+    c = dict(q=q, kc=small, vc=small_v, lens=torch.tensor([n]), cu=cu, bt=torch.tensor([[0, 1, 2]]), params={})
+    assert_close(out, lse, oracle(c))
+
+
+def test_serving_steps():
+    """A prompt in pieces and then tokens, two sequences side by side, with
+    rotation: fa_kvcache_append and fa_fwd_chunk step by step against attention
+    over the whole rotated sequences."""
+    from oracle import attention as A
+    from oracle import rotary as R
+    m = fa()
+    for dtype, d, hq, hkv, page in ((BF, 128, 8, 2, 16), (H, 64, 6, 6, 24)):
+        g = torch.Generator().manual_seed(140)
+        total = [230, 61]
+        q, k, v = ([rnd(g, n, h, d, dtype=dtype) for n in total] for h in (hq, hkv, hkv))
+        f, _ = m.fa_rope_inv_freq(d // 2, 10000.0)
+        fd = f.to(DEV)
+        n_pages = sum(-(-n // page) for n in total) + 1
+        perm = torch.randperm(n_pages, generator=g).to(torch.int32)
+        bt = torch.full((2, -(-max(total) // page)), -1, dtype=torch.int32)
+        at = 0
+        for s, n in enumerate(total):
+            bt[s, :-(-n // page)] = perm[at:at - (-n // page)]
+            at += -(-n // page)
+        kc = torch.full((n_pages, page, hkv, d), float("nan"), dtype=dtype, device=DEV)
+        vc = kc.clone()
+        lens = [torch.zeros(2, dtype=torch.int32, device=DEV), torch.empty(2, dtype=torch.int32, device=DEV)]
+        ws = None
+        got = [[], []]
+        done = [0, 0]
+        for step in ([100, 0], [129, 60], [1, 1]):
+            rows = [x[s][done[s]:done[s] + step[s]] for x in (q, k, v) for s in (0, 1)]
+            qs, ks, vs = torch.cat(rows[:2]).to(DEV), torch.cat(rows[2:4]).to(DEV), torch.cat(rows[4:]).to(DEV)
+            cu = torch.tensor([0, step[0], sum(step)], dtype=torch.int32, device=DEV)
+            done = [a + b for a, b in zip(done, step)]
+            if ws is None:
+                _, plan = m.fa_fwd_chunk_plan(qs, kc, vc, lens[0], cu_seqlens_q=cu, block_table=bt.to(DEV), max_seqlen_q=200,
+                                              max_seqlen_k=max(total))
+                ws = m.alloc_workspace(2 * plan["workspace_bytes"], DEV)
+            qr, _, _ = m.fa_kvcache_append(ks, vs, kc, vc, lens[0], q=qs, cu_seqlens_q=cu, block_table=bt.to(DEV), inv_freq=fd,
+                                           seqlens_out=lens[1], workspace=ws)
+            out, _, _ = m.fa_fwd_chunk(qr, kc, vc, lens[1], cu_seqlens_q=cu, block_table=bt.to(DEV), max_seqlen_q=200,
+                                       max_seqlen_k=max(total), workspace=ws)
+            lens.reverse()
+            got[0].append(out[:step[0]])
+            got[1].append(out[step[0]:])
+        assert m.fa_check_device_error(ws) == (0, 0)
+        h = torch.finfo(dtype).eps / 2
+        for s, n in enumerate(total):
+            pos = np.arange(n)
+            qr, kr = R.rope(q[s], pos, f), R.rope(k[s], pos, f)
+            ref, _ = A.attention(qr[None], kr[None], v[s].double().numpy()[None], causal=True)
+            mass, _ = A.attention(qr[None], kr[None], v[s].double().abs().numpy()[None], causal=True)
+            o = torch.cat(got[s]).double().cpu().numpy()
+            # q and k are each rounded once more after the rotation: a logit moves by at most
+            # 2 h (1 + h) scale sum |q k| <= 2 h * |q| |k| / sqrt(d) (Cauchy-Schwarz), p by that share
+            norm = np.linalg.norm(qr, axis=-1).max(axis=1)[:, None] * np.linalg.norm(kr, axis=-1).max() / np.sqrt(d)
+            dx = np.exp(2 * 2 * h * (1 + h) * norm)[..., None] - 1  # numerator and denominator
+            tol = (h * (mass[0] + np.abs(ref[0])) * (1 + h) + 2e-4 * mass[0] + dx * mass[0]) * (1 + h) + n * 2.0 ** -25 * 6
+            assert (np.abs(o - ref[0]) <= tol).all(), np.abs(o - ref[0]).max()
+
+
+def test_capture_streams_and_changed_lengths():
+    """Captured once and replayed with other lengths; two calls at once on two
+    streams, each with its own workspace."""
+    m = fa()
+    c = case(150, [1, 1, 1], [4000, 300, 10], hq=8, hkv=2)
+    st = {k: dev(c[k]) for k in ("q", "kc", "vc", "lens", "cu", "bt")}
+    out, lse, ws = run(c)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+
+    def call(o, l, w, stream=None):
+        m.fa_fwd_chunk(st["q"], st["kc"], st["vc"], st["lens"], out=o, lse=l, cu_seqlens_q=st["cu"], block_table=st["bt"],
+                       max_seqlen_q=1, max_seqlen_k=4000, workspace=w, stream=stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(o2, l2, ws)
+    for lens in ([4000, 300, 10], [129, 300, 1], [3999, 0, 10]):
+        st["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_close(o2, l2, oracle(dict(c, lens=torch.tensor(lens))), n_keys=4000)
+    assert m.fa_check_device_error(ws) == (0, 0)
+    st["lens"].copy_(c["lens"])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for i in range(8):
+        s = streams[i % 2]
+        with torch.cuda.stream(s):
+            w = torch.zeros(ws.numel(), dtype=torch.uint8, device=DEV) if i < 2 else outs[i - 2][2]
+            o, l = torch.empty_like(out), torch.empty_like(lse)
+            call(o, l, w)
+            outs.append((o, l, w))
+    torch.cuda.synchronize()
+    for o, l, _ in outs:
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    # a stream's handle that is not the current one; buffers allocated by the call
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, l, _ = m.fa_fwd_chunk(st["q"], st["kc"], st["vc"], st["lens"], cu_seqlens_q=st["cu"], block_table=st["bt"], max_seqlen_q=1,
+                             max_seqlen_k=4000, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(o, out) and torch.equal(l, lse)
