@@ -31,29 +31,26 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
-constexpr int kSeqSmem = 2048;  // sequences whose row-tile offsets are kept in shared memory
-// Cost model, in key tiles: what a piece costs beside its tiles (its start, Q,
-// the epilogue), what leaving a partial and joining it costs more, and the
-// join's launch.
-constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 4.f;
+constexpr int kSeqSmem = 1024, kTileSmem = 1280;  // sequences and row tiles kept in shared memory, more in the workspace
+constexpr int kTailFlag = 1 << 30;                // in a row tile's second word: its units are cut as tail
+// Cost model, in key tiles (about 0.8 us of a CTA): what a piece costs beside
+// its tiles (its start, Q, the epilogue), what leaving a partial and joining it
+// costs more, and what there being any to join does.
+constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 2.f;
+constexpr int kMaxTailCut = 8;
 
 __device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
   if (atomicCAS(&p.ws->error, 0u, code) == 0u) atomicExch(&p.ws->error_info, info);
 }
 
-// Key tiles of row tile rt of sequence b (kt0, count) and the range [fl, fh]
-// of them, relative to kt0, whose every pair is kept.
-__device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int b, int rt, int& kt0, int& count, int& fl,
-                                              int& fh) {
-  const int q_len = chunk_qlen(p, b), kv = p.kv_len[b], off = kv - q_len;
-  const int pre = p.prefix ? p.prefix[b] : 0;
+// Key tiles that some row of row tile rt of a sequence sees: kt0 .. kt0 + count - 1.
+__device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int4 seq, int rt, int& kt0, int& count) {
+  const int q_len = seq.y, kv = seq.z, pre = seq.w, off = kv - q_len;
   const int i0 = rt * p.rt_tokens, i1 = min(i0 + p.rt_tokens, q_len) - 1;
   int lo0, hi0, lo1, hi1;  // both ends move right with the row
   chunk_row_keys(p, i0, off, kv, pre, lo0, hi0);
   chunk_row_keys(p, i1, off, kv, pre, lo1, hi1);
   kt0 = count = 0;
-  fl = 1;
-  fh = 0;
   if (p.debug_flags & FA_DEBUG_NO_SKIP) {
     count = (kv + kKeysPerTile - 1) / kKeysPerTile;
     return;
@@ -61,9 +58,6 @@ __device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int b, int r
   if (lo0 > hi1) return;
   kt0 = lo0 / kKeysPerTile;
   count = hi1 / kKeysPerTile - kt0 + 1;
-  // FULL: first key at least lo1, last key at most hi0 (which may be negative)
-  fl = (lo1 + kKeysPerTile - 1) / kKeysPerTile - kt0;
-  fh = (hi0 + 1) / kKeysPerTile - 1 - kt0;
 }
 
 // Block-wide exclusive prefix sum; `total` gets the sum.
@@ -93,127 +87,183 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
   return r;
 }
 
-// Number of pieces of a unit of n key tiles cut at T.
-__device__ __forceinline__ int pieces_of(int n, int T) { return n <= T ? 1 : (n + T - 1) / T; }
-
+// One CTA cuts the step into pieces (see the head of this file).
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
-  __shared__ int s_off[kSeqSmem + 1];
+  __shared__ int4 s_seq[kSeqSmem];
+  __shared__ int4 s_tile[kTileSmem];
   __shared__ int s_hist[kBins];
   __shared__ int s_warp[64];
   __shared__ float s_cost[32];
   __shared__ int s_T[32];
-  __shared__ int s_nmax, s_slots, s_splits;
-  __shared__ unsigned long long s_work;
+  __shared__ int s_nmax, s_slots, s_splits, s_bin, s_before;
+  __shared__ unsigned int s_work;
+  let_dependents_start();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool in_smem = p.n_seq <= kSeqSmem;
+  int4* const seqs = p.n_seq <= kSeqSmem ? s_seq : p.seqs;
   if (tid == 0) {
     s_nmax = s_slots = s_splits = 0;
     s_work = 0;
   }
-  s_hist[tid] = 0;
 
   // ---- row tiles per sequence; sequences whose lengths do not fit get none
-  int base = 0;
+  int R = 0;
   for (int s0 = 0; s0 < p.n_seq; s0 += kPlanThreads) {
     const int s = s0 + tid;
     int nt = 0;
+    int4 q = make_int4(0, 0, 0, 0);
     if (s < p.n_seq) {
       const int64_t c0 = p.cu_q ? p.cu_q[s] : 0, c1 = p.cu_q ? p.cu_q[s + 1] : p.Sq;
-      const int64_t q_len = c1 - c0, kv = p.kv_len[s];
-      if (c0 < 0 || q_len < 0 || q_len > p.Sq || (p.cu_q && c1 > p.tot_q) || kv < 0 || kv > p.Sk ||
-          (p.prefix && p.prefix[s] < 0))
+      const int64_t q_len = c1 - c0;
+      q.z = p.kv_len[s];
+      q.w = p.prefix ? p.prefix[s] : 0;
+      if (c0 < 0 || q_len < 0 || q_len > p.Sq || (p.cu_q && c1 > p.tot_q) || q.z < 0 || q.z > p.Sk || q.w < 0) {
         chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)s);
-      else
-        nt = (int)((q_len + p.rt_tokens - 1) / p.rt_tokens);
+      } else {
+        q.y = (int)q_len;
+        nt = (q.y + p.rt_tokens - 1) / p.rt_tokens;
+      }
     }
     int total;
-    const int at = base + block_scan(nt, s_warp, total);
-    if (s < p.n_seq) {
-      p.rt_off[s] = at;
-      if (in_smem) s_off[s] = at;
-    }
-    base += total;
+    q.x = R + block_scan(nt, s_warp, total);
+    if (s < p.n_seq) seqs[s] = q;
+    R += total;
   }
-  // (overlapping cu_seqlens_q could list more tiles than the workspace holds)
-  const int R = min(base, p.max_rtiles);
-  if (base > R && tid == 0) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)p.n_seq);
+  if (R > p.max_rtiles) {  // overlapping cu_seqlens_q: more tiles than the workspace lists
+    if (tid == 0) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)p.n_seq);
+    R = p.max_rtiles;
+  }
+  int4* const tiles = R <= kTileSmem ? s_tile : p.rtiles;
   __syncthreads();
 
   // ---- key tiles of each row tile
   int nmax = 0;
-  unsigned long long work = 0;
+  unsigned int work = 0;
   for (int r = tid; r < R; r += kPlanThreads) {
     int lo = 0, hi = p.n_seq;  // the last sequence whose first tile is at or before r
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((in_smem ? s_off[mid] : p.rt_off[mid]) <= r) lo = mid;
+      if (seqs[mid].x <= r) lo = mid;
       else hi = mid;
     }
-    const int rt = r - (in_smem ? s_off[lo] : p.rt_off[lo]);
-    int kt0, n, fl, fh;
-    row_tile_keys(p, lo, rt, kt0, n, fl, fh);
-    p.rtiles[r] = make_int4(lo, rt, kt0, n);
+    const int4 q = seqs[lo];
+    int kt0, n;
+    row_tile_keys(p, q, r - q.x, kt0, n);
+    tiles[r] = make_int4(lo, r - q.x, kt0, n);
     nmax = max(nmax, n);
     work += n;
   }
-  atomicMax(&s_nmax, nmax);
-  atomicAdd(&s_work, work);
+  nmax = __reduce_max_sync(0xffffffffu, nmax);
+  work = __reduce_add_sync(0xffffffffu, work);
+  if (lane == 0) {
+    atomicMax(&s_nmax, nmax);
+    atomicAdd(&s_work, work);
+  }
+  s_hist[tid] = 0;
   __syncthreads();
   nmax = s_nmax;
-  work = s_work * p.n_hg;
+  const float fwork = (float)s_work * p.n_hg, P = (float)p.grid;
+  const int units = R * p.n_hg;
 
-  // ---- the length T: one candidate per warp.  A round of the grid takes as
-  // long as its longest piece; t0 tiles each would fill one round evenly, so
-  // the candidates are whole units, t0 up to twice as much (one round with room
-  // for the units' odd lengths), and the same for two, three and four rounds.
-  {
-    const float P = (float)p.grid;
-    const int t0 = (int)((work + p.grid - 1) / p.grid);
+  // ---- the length T, one candidate per warp: whole units; t0 tiles, which would
+  // fill one round of the grid evenly, up to twice as many (room for the units'
+  // odd lengths), and the same for two, three and four rounds
+  int T = max(nmax, 1);
+  if (p.max_slots > 0 && nmax > 1) {
+    const float t0 = fwork / P;
     float f = 0.f;
-    if (warp >= 1 && warp <= 16) f = 1.f + (warp - 1) / 16.f;
+    if (warp <= 16) f = 1.f + (warp - 1) / 16.f;
     else if (warp <= 24) f = (1.f + (warp - 17) / 8.f) / 2.f;
     else if (warp <= 28) f = (1.f + (warp - 25) / 4.f) / 3.f;
     else f = (1.f + (warp - 29) / 4.f) / 4.f;
-    int T = warp == 0 ? nmax : (int)ceilf(f * t0);
-    T = max(1, min(T, nmax));
+    const int t = warp == 0 ? nmax : min(max(1, (int)ceilf(f * t0)), nmax);
     float cost = 3e38f;
-    if (warp == 0 || (T < nmax && p.max_slots > 0)) {
+    if (warp == 0 || t < nmax) {
       int m = 0, part = 0, longest = 0;
       for (int r = lane; r < R; r += 32) {
-        const int n = p.rtiles[r].w, k = pieces_of(n, T);
+        const int n = tiles[r].w, k = n <= t ? 1 : (n + t - 1) / t;
         m += k;
         if (k > 1) part += k;
-        longest = max(longest, (n + k - 1) / k);
+        longest = max(longest, k > 1 ? (n + k - 1) / k : n);
       }
       m = __reduce_add_sync(0xffffffffu, m) * p.n_hg;
       part = __reduce_add_sync(0xffffffffu, part) * p.n_hg;
       longest = __reduce_max_sync(0xffffffffu, longest);
-      const float total = (float)work + kPieceCost * m + kPartialCost * part;
-      const float rounds = ceilf(m / P);
-      if (m > 0)
-        cost = fmaxf(longest + kPieceCost, total / P) + (rounds - m / P) * total / m + (part ? kJoinCost : 0.f);
+      const float total = fwork + kPieceCost * m + kPartialCost * part;
+      cost = fmaxf(longest + kPieceCost + (part ? kPartialCost : 0.f), (total + (ceilf(m / P) * P - m) * total / m) / P) +
+             (part ? kJoinCost : 0.f);
       if (part > p.max_slots) cost = 3e38f;
     }
     if (lane == 0) {
       s_cost[warp] = cost;
-      s_T[warp] = T;
+      s_T[warp] = t;
     }
+    __syncthreads();
+    float best = s_cost[lane];
+    int at = lane;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float c = __shfl_xor_sync(0xffffffffu, best, o);
+      const int w = __shfl_xor_sync(0xffffffffu, at, o);
+      if (c < best || (c == best && w < at)) {
+        best = c;
+        at = w;
+      }
+    }
+    T = s_T[at];
   }
-  __syncthreads();
-  int T = s_T[0];
-  float best = s_cost[0];
-  for (int w = 1; w < 32; ++w)
-    if (s_cost[w] < best) {
-      best = s_cost[w];
-      T = s_T[w];
-    }
-
-  // ---- list the pieces, longest first (a counting sort by length)
   int shift = 0;
   while ((T >> shift) >= kBins) ++shift;
   auto bin_of = [&](int len) { return kBins - 1 - (len >> shift); };
+
+  // ---- whole units that leave a last round mostly empty: as many row tiles as
+  // that round holds, the shortest ones (in their order where they are equally
+  // long), are cut in `cut` and fill it
+  int cut = 1;
+  const int last = units % p.grid;  // units of the last round
+  if (T >= nmax && nmax > 1 && units > p.grid && last > 0 && 2 * last <= p.grid) {
+    const int tails = (last + p.n_hg - 1) / p.n_hg;  // row tiles
+    cut = min(min(p.grid / (tails * p.n_hg), kMaxTailCut), p.max_slots / (tails * p.n_hg));
+    if (cut >= 2) {
+      for (int r = tid; r < R; r += kPlanThreads) atomicAdd(&s_hist[bin_of(tiles[r].w)], 1);
+      __syncthreads();
+      const int mine = s_hist[tid];
+      int total;
+      const int before = block_scan(mine, s_warp, total);
+      if (before < R - tails + 1 && before + mine >= R - tails + 1) {  // holds the first tail tile
+        s_bin = tid;
+        s_before = before;
+      }
+      s_hist[tid] = 0;
+      __syncthreads();
+      // of that bin's tiles, in their order, the first `whole` stay
+      const int bin = s_bin, whole = R - tails - s_before;
+      int seen = 0;
+      bool worth = false;
+      for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
+        const int r = r0 + tid;
+        const int b = r < R ? bin_of(tiles[r].w) : -1;
+        const int rank = seen + block_scan(b == bin ? 1 : 0, s_warp, total);
+        if (r < R && (b > bin || (b == bin && rank >= whole))) {
+          tiles[r].y |= kTailFlag;
+          // (the round ends with its longest piece)
+          worth |= tiles[r].w * (1.f - 1.f / cut) > kPartialCost + kJoinCost;
+        }
+        seen += total;
+      }
+      if (!__syncthreads_or(worth)) cut = 1;
+    } else {
+      cut = 1;
+    }
+  }
+  auto pieces_of = [&](int4 t) {
+    if (t.w > T) return (t.w + T - 1) / T;
+    return (cut > 1 && (t.y & kTailFlag)) ? max(1, min(cut, t.w)) : 1;
+  };
+
+  // ---- list the pieces, longest first (a counting sort by length)
   for (int r = tid; r < R; r += kPlanThreads) {
-    const int n = p.rtiles[r].w, k = pieces_of(n, T), len = n / k, more = n - len * k;
+    const int4 t = tiles[r];
+    const int k = pieces_of(t), len = t.w / k, more = t.w - len * k;
     if (more) atomicAdd(&s_hist[bin_of(len + 1)], more * p.n_hg);
     atomicAdd(&s_hist[bin_of(len)], (k - more) * p.n_hg);
   }
@@ -222,30 +272,25 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   const int start = block_scan(s_hist[tid], s_warp, total);
   s_hist[tid] = start;
   __syncthreads();
-  const int64_t units = (int64_t)R * p.n_hg;
-  for (int64_t u = tid; u < units; u += kPlanThreads) {
-    const int r = (int)(u / p.n_hg), hg = (int)(u - (int64_t)r * p.n_hg);
-    const int4 t = p.rtiles[r];
-    int kt0, n, fl, fh;
-    row_tile_keys(p, t.x, t.y, kt0, n, fl, fh);
-    const int k = pieces_of(n, T), len = n / k, more = n - len * k;
+  for (int u = tid; u < units; u += kPlanThreads) {
+    const int r = fast_div(u, p.div_hg), hg = u - r * p.n_hg;
+    const int4 t = tiles[r];
+    const int k = pieces_of(t), len = t.w / k, more = t.w - len * k, rt = t.y & ~kTailFlag;
     int slot0 = -1;
     if (k > 1) {
       slot0 = atomicAdd(&s_slots, k);
       ChunkSplit sp;
-      sp.b = t.x; sp.rt = t.y; sp.hg = hg; sp.slot0 = slot0; sp.n = k;
+      sp.b = t.x; sp.rt = rt; sp.hg = hg; sp.slot0 = slot0; sp.n = k;
       sp.pad[0] = sp.pad[1] = sp.pad[2] = 0;
       p.splits[atomicAdd(&s_splits, 1)] = sp;
     }
-    int done = 0;
+    int at = t.z;
     for (int i = 0; i < k; ++i) {
       const int c = len + (i < more ? 1 : 0);
-      ChunkPiece pc;
-      pc.b = t.x; pc.rt = t.y; pc.hg = hg; pc.kt0 = kt0 + done; pc.count = c;
-      pc.slot = k > 1 ? slot0 + i : -1;
-      pc.fl = fl - done; pc.fh = fh - done;
-      p.pieces[atomicAdd(&s_hist[bin_of(c)], 1)] = pc;
-      done += c;
+      int4* dst = reinterpret_cast<int4*>(p.pieces + atomicAdd(&s_hist[bin_of(c)], 1));
+      dst[0] = make_int4(t.x, rt, hg, at);
+      dst[1] = make_int4(c, k > 1 ? slot0 + i : -1, 0, 0);
+      at += c;
     }
   }
   __syncthreads();
@@ -275,6 +320,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31;
   const int n_warps = gridDim.x * 8;
+  wait_for_previous();
   const int n_rows = p.counts->n_splits * kChunkRows;
   for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < n_rows; w += n_warps) {
     const ChunkSplit sp = p.splits[w / kChunkRows];
@@ -409,6 +455,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
     p.num_pages = (int32_t)n_seq;
     p.box_rows = kKeysPerTile;
   }
+  while ((1 << p.box_shift) < p.box_rows) ++p.box_shift;
   p.div_page = make_fastdiv((uint32_t)p.page_size);
   p.cache_rows = k->shape[1];
   p.cache_outer = k->shape[0];
@@ -455,6 +502,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   p.rt_tokens = kChunkRows / p.gp;
   p.n_hg = p.Hq / p.gp;
   p.div_gp = make_fastdiv((uint32_t)p.gp);
+  p.div_hg = make_fastdiv((uint32_t)p.n_hg);
 
   // ---- bounds of the work, workspace
   int64_t rtiles = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens);
@@ -462,8 +510,11 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   if (rtiles * p.n_hg > (1 << 27)) return FA_ERR_INVALID_ARG;
   const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
   const int64_t ctas = (int64_t)sm_count() * chunk_ctas_per_sm(p.d);
-  // partials: at most two rounds of the grid, and no more than all tiles alone
-  const int64_t slots = n_kt > 1 ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
+  // partials: at most two rounds of the grid, and no more than all tiles alone;
+  // none where no sequence has more than 8 key tiles: cutting and joining such
+  // units gains nothing for the launch it costs (one token over 700 keys, 6
+  // tiles: 13.3 us cut in six and joined, 14.0 us whole, both in a graph)
+  const int64_t slots = n_kt > 8 ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
   const int64_t pieces = units + slots;
   p.max_rtiles = (int32_t)rtiles;
   p.max_slots = (int32_t)slots;
@@ -477,7 +528,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   };
   p.ws = reinterpret_cast<WsHeader*>(base);
   p.counts = reinterpret_cast<ChunkCounts*>(take(sizeof(ChunkCounts)));
-  p.rt_off = reinterpret_cast<int32_t*>(take((size_t)(n_seq + 1) * 4));
+  p.seqs = reinterpret_cast<int4*>(take((size_t)n_seq * sizeof(int4)));
   p.rtiles = reinterpret_cast<int4*>(take((size_t)rtiles * sizeof(int4)));
   p.pieces = reinterpret_cast<ChunkPiece*>(take((size_t)pieces * sizeof(ChunkPiece)));
   p.splits = reinterpret_cast<ChunkSplit*>(take((size_t)(slots / 2) * sizeof(ChunkSplit)));
@@ -499,10 +550,10 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
 }
 
 template <int D, bool F16>
-void launch_join(const ChunkParams& p, cudaStream_t st) {
+cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
   const int64_t warps = (int64_t)p.max_slots / 2 * kChunkRows;
   const int blocks = (int)std::min<int64_t>((warps + 7) / 8, 152 * 4);
-  chunk_join_kernel<D, F16><<<blocks, 256, 0, st>>>(p);
+  return launch_overlapped(chunk_join_kernel<D, F16>, blocks, 256, 0, overlap, st, p);
 }
 
 }  // namespace
@@ -532,17 +583,18 @@ int fa_fwd_chunk(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* 
     if (e == cudaSuccess && ev) e = cudaEventRecord(static_cast<cudaEvent_t>(ev), st);
   };
   const bool any = pub.n_items > 0;
+  // (events between the kernels would be recorded late if these overlapped)
+  const bool overlap = !opts->event_begin && !opts->event_attn_end;
   if (any) {
     chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
     e = cudaGetLastError();
   }
   record(opts->event_begin);
-  if (any && e == cudaSuccess) e = p.f16 ? launch_chunk_attn_f16(p, st) : launch_chunk_attn(p, st);
+  if (any && e == cudaSuccess) e = p.f16 ? launch_chunk_attn_f16(p, overlap, st) : launch_chunk_attn(p, overlap, st);
   record(opts->event_attn_end);
   if (any && e == cudaSuccess && p.max_slots > 0) {
-    if (p.d == 64) p.f16 ? launch_join<64, true>(p, st) : launch_join<64, false>(p, st);
-    else p.f16 ? launch_join<128, true>(p, st) : launch_join<128, false>(p, st);
-    e = cudaGetLastError();
+    if (p.d == 64) e = p.f16 ? launch_join<64, true>(p, overlap, st) : launch_join<64, false>(p, overlap, st);
+    else e = p.f16 ? launch_join<128, true>(p, overlap, st) : launch_join<128, false>(p, overlap, st);
   }
   record(opts->event_end);
   if (e != cudaSuccess) {

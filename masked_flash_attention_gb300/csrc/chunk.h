@@ -16,7 +16,7 @@ struct ChunkPiece {
   int32_t b, rt, hg;   // sequence, row tile, head group
   int32_t kt0, count;  // key tiles kt0 .. kt0 + count - 1
   int32_t slot;        // where its partial rows go; -1: it holds all the unit's keys
-  int32_t fl, fh;      // tiles kt0 + fl .. kt0 + fh are FULL, the others PARTIAL
+  int32_t pad[2];
 };
 static_assert(sizeof(ChunkPiece) == 32, "two 16-byte loads");
 
@@ -41,12 +41,12 @@ struct ChunkParams {
   const int32_t* prefix;       // nullable [n_seq]
   const int32_t* block_table;  // nullable: padded cache
   int64_t bt_stride;
-  int32_t page_size, num_pages, box_rows;
+  int32_t page_size, num_pages, box_rows, box_shift;  // rows per TMA box = 2^box_shift
   FastDiv div_page;
   int32_t n_seq, Sq, Sk;  // Sq/Sk: fixed or maximum lengths
   int64_t tot_q;
   int32_t Hq, G, gp, rt_tokens, n_hg;  // G = Hq / Hkv; n_hg = Hq / gp
-  FastDiv div_gp;
+  FastDiv div_gp, div_hg;
   int32_t d, f16;
   float scale, scale_log2, softcap, inv_softcap;
   const float* alibi;
@@ -55,8 +55,8 @@ struct ChunkParams {
   // workspace
   WsHeader* ws;
   ChunkCounts* counts;
-  int32_t* rt_off;    // [n_seq + 1] first row tile of each sequence
-  int4* rtiles;       // [max_rtiles] {sequence, row tile, first key tile, key tiles}
+  int4* seqs;         // [n_seq] {first row tile, q_len, kv_len, prefix} (many sequences)
+  int4* rtiles;       // [max_rtiles] {sequence, row tile, first key tile, key tiles} (many row tiles)
   ChunkPiece* pieces;
   ChunkSplit* splits;
   float* part_o;      // [max_slots][128][d]
@@ -68,9 +68,35 @@ struct ChunkParams {
   int64_t cache_rows, cache_outer;  // page_size x num_pages, or cap x n_seq
 };
 
-cudaError_t launch_chunk_attn(const ChunkParams& p, cudaStream_t st);      // bf16
-cudaError_t launch_chunk_attn_f16(const ChunkParams& p, cudaStream_t st);  // fp16
+// `overlap`: the kernel may start while the one before it on the stream runs
+// (programmatic dependent launch; it waits for that one's results itself).
+cudaError_t launch_chunk_attn(const ChunkParams& p, bool overlap, cudaStream_t st);      // bf16
+cudaError_t launch_chunk_attn_f16(const ChunkParams& p, bool overlap, cudaStream_t st);  // fp16
 int chunk_ctas_per_sm(int d);
+
+#ifdef __CUDACC__
+// Launch with or without overlap of the preceding kernel's end.
+template <typename... Args>
+inline cudaError_t launch_overlapped(void (*kern)(Args...), unsigned grid, unsigned block, size_t smem, bool overlap,
+                                     cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, args...);
+}
+
+// Lets a dependent kernel that may overlap start; waits for the kernel before
+// (at once when it did not overlap).
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
 
 #ifdef __CUDACC__
 __device__ __forceinline__ int chunk_qlen(const ChunkParams& p, int b) {

@@ -22,10 +22,10 @@
 //    one per CTA, longest first; a piece of a split unit leaves its normalised
 //    rows and log-sum-exp in fp32 for the join.
 //
-// Warp roles (12 warps; 8 at d = 64, two CTAs per SM): 0 K producer, 1 QK
+// Warp roles (12 or 16 warps; 8 at d = 64, two CTAs per SM): 0 K producer, 1 QK
 // issuer and Q producer, 2 V producer, 3 PV issuer, 4.. one or two softmax
 // warpgroups, which at d = 128 take alternate key tiles of a piece and hand the
-// row references from tile to tile through shared memory.  A warp none of whose
+// row references from tile to tile through shared memory, 12.. more producers.  A warp none of whose
 // rows exists keeps step on the barriers and computes nothing.
 //
 // Every mbarrier wait is bounded (1 s); on a time-out the kernel records
@@ -49,18 +49,27 @@ namespace mfa {
 
 namespace {
 
-// Register split: d = 128 launches 384 threads at 168 registers, of which the
-// producers and issuers keep 72 and the softmax warpgroups take 216; d = 64
-// 256 threads at 128, split 40 / 216.
-template <int D>
+// NP producer warps per operand.  A warp issues a TMA copy only every 65 to 90
+// cycles while the SM's TMA unit takes one in about 28: at d = 128 a page of 16
+// rows makes 32 copies per K/V tile, and with boxes that small a fourth
+// warpgroup shares them, three warps per operand (2048 tokens over 32768 keys,
+// page 16: 1113 us with one warp, 966 us with three; page 64: 822 and 882 us,
+// the registers it takes slowing the others).  At d = 64 a box is one copy and
+// the two CTAs of an SM issue side by side: one warp.
+// Register split: with one producer warp per operand 384 threads launch at 168
+// registers, of which the softmax warpgroups take 216 and the others keep 72; the
+// blocks of 512 threads, and d = 64, launch at 128 and are split 40 / 216.
+template <int D, int NP_>
 struct CCfg {
+  static constexpr int NP = NP_;
   static constexpr int NW = D == 64 ? 1 : 2;  // softmax warpgroups
-  static constexpr int kThreads = 128 + 128 * NW;
+  static constexpr int kThreads = 128 + 128 * NW + (NP > 1 ? 128 : 0);
   static constexpr int kCtas = D == 64 ? 2 : 1;  // per SM
-  static constexpr int kLaunchRegs = D == 64 ? 128 : 168;
-  static constexpr int kIssueRegs = D == 64 ? 40 : 72;
+  static constexpr int kLaunchRegs = (D == 64 || NP > 1) ? 128 : 168;
+  static constexpr int kIssueRegs = (D == 64 || NP > 1) ? 40 : 72;
   static constexpr int kSoftmaxRegs = 216;
-  static_assert(128 * kIssueRegs + 128 * NW * kSoftmaxRegs <= kThreads * kLaunchRegs,
+  static_assert(NP == 1 || (NP == 3 && D == 128), "the role table has one or three warps per operand");
+  static_assert((kThreads - 128 * NW) * kIssueRegs + 128 * NW * kSoftmaxRegs <= kThreads * kLaunchRegs,
                 "the register split must fit the block's launch allocation");
   static constexpr uint32_t kCols = NW == 2 ? 512 : 256;  // TMEM: S and P buffers, O
   static constexpr uint32_t kSCol = 0;
@@ -70,6 +79,8 @@ struct CCfg {
   static constexpr int NSK = D == 128 ? 3 : 2;
   static constexpr int NSV = 2;
   static constexpr int kTileBytes = 128 * D * 2;
+  // K/V tiles: D / 64 halves of 128 rows by 64 columns (128 bytes)
+  static constexpr int kHalfStep = 16384;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = NQ * kTileBytes;
   static constexpr int kVOff = kKOff + NSK * kTileBytes;
@@ -108,6 +119,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=l"(d)
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
@@ -151,7 +167,7 @@ __device__ __forceinline__ ChunkPiece piece_at(const ChunkParams& p, int i) {
   const int4 a = src[0], b = src[1];
   ChunkPiece w;
   w.b = a.x; w.rt = a.y; w.hg = a.z; w.kt0 = a.w;
-  w.count = b.x; w.slot = b.y; w.fl = b.z; w.fh = b.w;
+  w.count = b.x; w.slot = b.y;
   return w;
 }
 // Next round at or after r whose piece has key tiles, or -1.
@@ -164,12 +180,135 @@ __device__ __forceinline__ int next_busy(const ChunkParams& p, int n, int r, Chu
   }
 }
 
+// Output of a row that keeps no key of its sequence.
+template <int D>
+__device__ __forceinline__ void write_empty_row(const ChunkParams& p, int b, int h, int i) {
+  const int64_t qrow = (p.cu_q ? p.cu_q[b] : 0) + i, ob = p.cu_q ? 0 : b;
+  uint16_t* o = p.o + ob * p.o_sb + qrow * p.o_ss + (int64_t)h * p.o_sh;
+#pragma unroll
+  for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(o + c) = make_uint4(0, 0, 0, 0);
+  p.lse[ob * p.lse_sb + (int64_t)h * p.lse_sh + qrow * p.lse_ss] = -INFINITY;
+}
+
+// One producer warp: K or V tiles of every piece, in order, through a ring of
+// n_stages stages.  Box x of a tile (its rows x * box_rows ..) is sent by lane
+// x / NP of the operand's warp x % NP; each warp waits for the stage itself and
+// arrives on its full barrier (NP arrivals) with the bytes it sends.  Written for
+// few registers, and one copy of the code for both operands: with two, the
+// softmax loop beside them ran a fifth slower.
+template <int D, int NP>
+__device__ __forceinline__ void produce(const ChunkParams& p, const bool is_k, const int n_stages,
+                                        const CUtensorMap* map, int n_pieces, int part, int lane, uint64_t* full,
+                                        uint64_t* empty, uint64_t* v_tail, unsigned char* ring,
+                                        volatile int* abort_flag) {
+  constexpr int kTileBytes = 128 * D * 2, kHalfStep = 16384;
+  if (lane == 0) tc::tma_prefetch_desc(map);
+  int s = 0;             // stage of the next tile
+  uint32_t phase = 1;    // parity its empty barrier has to have completed (a fresh barrier passes for 1)
+  uint32_t tails = 0;
+  bool ok = true;
+  // test only: the first key tile is never sent (FA_DEBUG_WITHHOLD)
+  bool withhold = is_k && (p.debug_flags & FA_DEBUG_WITHHOLD);
+  ChunkPiece w;
+  for (int r = next_busy(p, n_pieces, 0, w); ok && r >= 0; r = next_busy(p, n_pieces, r + 1, w)) {
+    const int head = w.hg * p.gp / p.G;
+    const int32_t* table = p.block_table ? p.block_table + (int64_t)w.b * p.bt_stride : nullptr;
+    const int seq = w.b;
+    int key = w.kt0 * kKeysPerTile;             // the tile's first key
+    int left = p.kv_len[w.b] - key;             // keys from there to the sequence's end
+    for (int i = w.count; i > 0; --i, key += kKeysPerTile, left -= kKeysPerTile) {
+      const int rows = min(kKeysPerTile, left);
+      const int nb = (rows + p.box_rows - 1) >> p.box_shift;
+      // this lane's first page, read before the wait
+      int x = part + NP * lane, row = 0, page = -1;
+      auto look_up = [&] {
+        const int at = key + (x << p.box_shift), pi = fast_div(at, p.div_page);
+        row = at - pi * p.page_size;
+        page = table ? table[pi] : seq;
+      };
+      if (x < nb) look_up();
+      const bool tail = !is_k && rows < kKeysPerTile;
+      bool go = true;
+      if (lane == 0) {
+        go = tc::mbar_wait(empty + s, phase, abort_flag);
+        // the last tail's barrier phase ends before an arrival for the next
+        if (!is_k && go && tail && tails > 0) go = tc::mbar_wait_drain(v_tail, (tails - 1) & 1, 1000000000ull);
+      }
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (!go) {
+        if (lane == 0) fail(p, abort_flag, is_k ? 1 : 7);
+        ok = false;
+        break;
+      }
+      uint64_t* bar = tail ? v_tail : full + s;
+      for (int x0 = 0; !withhold; ) {
+        const bool good = x < nb && page >= 0 && page < p.num_pages;
+        if (x < nb && !good) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)page);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, good)) * p.box_rows * (uint32_t)(D * 2);
+        const bool last = x0 + 32 * NP >= nb;
+        if (lane == 0) {
+          // the warp's one arrival comes with its last group of boxes
+          if (last) tc::mbar_arrive_expect_tx(bar, bytes);
+          else mbar_expect_tx(bar, bytes);
+        }
+        __syncwarp();
+        if (good) {
+          unsigned char* dst = ring + s * kTileBytes + x * p.box_rows * 128;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) tc::tma_load_4d(dst + c * kHalfStep, map, bar, c * 64, head, row, page);
+        }
+        __syncwarp();
+        if (last) break;
+        x0 += 32 * NP;
+        x += 32 * NP;
+        if (x < nb) look_up();
+      }
+      withhold = false;
+      if (tail) {
+        if (part == 0) {
+          // rows past the last key in its 16-key step: zero once the copies have landed
+          if (!tc::mbar_wait_drain(v_tail, tails & 1, 1000000000ull)) {
+            if (lane == 0) fail(p, abort_flag, 8);
+            ok = false;
+            break;
+          }
+          const int end = (rows + 15) & ~15;
+          for (int e = lane; e < (end - rows) * (D / 8); e += 32) {
+            const int rr = rows + e / (D / 8), ch = e % (D / 8);
+            *reinterpret_cast<uint4*>(ring + s * kTileBytes + (ch >> 3) * kHalfStep + rr * 128 + (ch & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ++tails;
+        if (lane == 0) tc::mbar_arrive(full + s);
+      }
+      if (++s == n_stages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  if (lane == 0 && *abort_flag) {
+    // let the copies already issued land before the CTA can exit: wait, up to a
+    // limit, for each stage's next full phase (a stage without copies in flight
+    // runs into the limit)
+    for (int k = 0; k < n_stages; ++k) {
+      // stages before s were last filled in this pass of the ring, the others in the pass before
+      const uint32_t ph = k < s ? phase ^ 1 : phase;
+      tc::mbar_wait_drain(full + k, ph, 100000000ull);
+    }
+  }
+  __syncwarp();
+}
+
 // GEN: soft-cap and / or ALiBi (the plain logits fold the scale into the exponent).
-template <int D, bool GEN, bool F16>
-__global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
+template <int D, int NP, bool GEN, bool F16>
+__global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
     chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tmq,
                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-  using C = CCfg<D>;
+  using C = CCfg<D, NP>;
   constexpr int NSK = C::NSK, NSV = C::NSV, NQ = C::NQ, NW = C::NW;
   constexpr uint32_t kSCol = C::kSCol, kPCol = C::kPCol, kOCol = C::kOCol;
   extern __shared__ unsigned char smem_raw[];
@@ -208,14 +347,14 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
       tc::mbar_init(refb + k, 128);
     }
     for (int s = 0; s < NSK; ++s) {
-      tc::mbar_init(k_full + s, 1);
+      tc::mbar_init(k_full + s, NP);
       tc::mbar_init(k_empty + s, 1);
     }
     for (int s = 0; s < NSV; ++s) {
-      tc::mbar_init(v_full + s, 1);
+      tc::mbar_init(v_full + s, NP);
       tc::mbar_init(v_empty + s, 1);
     }
-    tc::mbar_init(v_tail, 1);
+    tc::mbar_init(v_tail, NP);
     tc::mbar_init(sumx, 256);
     tc::mbar_init(o_full, 1);
     *abort_flag = 0;
@@ -229,102 +368,17 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = *tmem_slot;
+  wait_for_previous();
   const int n_pieces = p.counts->n_pieces;
 
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
-  if (warp == 0 || warp == 2) {
+  if (warp < 4 || warp >= 4 + 4 * NW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+  if (warp == 0 || warp == 2 || warp >= 4 + 4 * NW) {
     // ------------------------------------------------------------ producers
-    // K (warp 0) and V (warp 2) tiles of every piece, in order, through their
-    // rings.  Box r of a tile (its rows r * box_rows ..) is sent by lane r % 32.
-    const bool is_k = (warp == 0);
-    const CUtensorMap* map = is_k ? &tmk : &tmv;
-    uint64_t* full = is_k ? k_full : v_full;
-    uint64_t* empty = is_k ? k_empty : v_empty;
-    unsigned char* ring = smem + (is_k ? C::kKOff : C::kVOff);
-    const int NS = is_k ? NSK : NSV;
-    const int br = p.box_rows;
-    const uint32_t box_bytes = (uint32_t)br * D * 2;
-    // test only: the first key tile is never sent (FA_DEBUG_WITHHOLD)
-    const bool withhold = is_k && (p.debug_flags & FA_DEBUG_WITHHOLD);
-    if (lane == 0) tc::tma_prefetch_desc(map);
-    int j = 0, tails = 0;
-    bool ok = true;
-    ChunkPiece w;
-    for (int r = next_busy(p, n_pieces, 0, w); ok && r >= 0; r = next_busy(p, n_pieces, r + 1, w)) {
-      const int kv = p.kv_len[w.b];
-      const int head = w.hg * p.gp / p.G;
-      const int32_t* table = p.block_table ? p.block_table + (int64_t)w.b * p.bt_stride : nullptr;
-      for (int i = 0; i < w.count; ++i, ++j) {
-        if (withhold && j == 0) continue;
-        const int j0 = (w.kt0 + i) * kKeysPerTile;
-        const int rows = min(kKeysPerTile, kv - j0);
-        const int nb = (rows + br - 1) / br;
-        const int s = j % NS;
-        // this lane's page, read before the wait
-        auto page_of = [&](int box, int& row) {
-          const int key = j0 + box * br, pi = fast_div(key, p.div_page);
-          row = key - pi * p.page_size;
-          return table ? table[pi] : w.b;
-        };
-        int row = 0, page = -1;
-        if (lane < nb) page = page_of(lane, row);
-        bool go = true;
-        if (lane == 0 && j >= NS) go = tc::mbar_wait(empty + s, ((j / NS) - 1) & 1, abort_flag);
-        go = __shfl_sync(0xffffffffu, go, 0);
-        if (!go) {
-          if (lane == 0) fail(p, abort_flag, is_k ? 1 : 7);
-          ok = false;
-          break;
-        }
-        const bool tail = !is_k && rows < kKeysPerTile;
-        uint64_t* bar = tail ? v_tail : full + s;
-        for (int b0 = 0; b0 < nb; b0 += 32) {
-          if (b0 && b0 + lane < nb) page = page_of(b0 + lane, row);
-          const bool mine = b0 + lane < nb;
-          const bool good = mine && page >= 0 && page < p.num_pages;
-          if (mine && !good) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)page);
-          const int n = __popc(__ballot_sync(0xffffffffu, good));
-          if (lane == 0) {
-            // the barrier's one arrival comes with the last group of boxes
-            if (b0 + 32 < nb) mbar_expect_tx(bar, n * box_bytes);
-            else tc::mbar_arrive_expect_tx(bar, n * box_bytes);
-          }
-          __syncwarp();
-          if (good) {
-            unsigned char* dst = ring + s * C::kTileBytes + (b0 + lane) * br * 128;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tc::tma_load_4d(dst + c * 16384, map, bar, c * 64, head, row, page);
-          }
-          __syncwarp();
-        }
-        if (tail) {
-          // rows past the last key in its 16-key step: zero once the copies have landed
-          if (!tc::mbar_wait_drain(v_tail, tails & 1, 1000000000ull)) {
-            if (lane == 0) fail(p, abort_flag, 8);
-            ok = false;
-            break;
-          }
-          ++tails;
-          const int end = (rows + 15) & ~15;
-          for (int e = lane; e < (end - rows) * (D / 8); e += 32) {
-            const int rr = rows + e / (D / 8), ch = e % (D / 8);
-            *reinterpret_cast<uint4*>(ring + s * C::kTileBytes + (ch >> 3) * 16384 + rr * 128 + (ch & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(full + s);
-        }
-      }
-    }
-    if (lane == 0 && *abort_flag) {
-      // let the copies already issued land before the CTA can exit
-      const int first = j > NS ? j - NS : 0;
-      for (int jj = first; jj < j; ++jj)
-        if (!(withhold && jj == 0)) tc::mbar_wait_drain(full + jj % NS, (jj / NS) & 1, 100000000ull);
-    }
-    __syncwarp();
+    // NP warps per operand: K warps 0, 12, 13, V warps 2, 14, 15
+    const int part = warp < 4 ? 0 : 1 + (warp & 1);
+    const bool is_k = warp < 4 ? warp == 0 : warp < 6 + 4 * NW;
+    produce<D, NP>(p, is_k, is_k ? NSK : NSV, is_k ? &tmk : &tmv, n_pieces, part, lane, is_k ? k_full : v_full,
+                   is_k ? k_empty : v_empty, v_tail, smem + (is_k ? C::kKOff : C::kVOff), abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issuer
     // S[g % NW] = Q K_g^T for the g-th tile of this CTA, as soon as the softmax
@@ -360,12 +414,14 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
           if (!tc::mbar_wait(k_full + s, (g / NSK) & 1, abort_flag)) { ok = false; break; }
           if (g >= NW && !tc::mbar_wait(s_free + sb, ((g - NW) / NW) & 1, abort_flag)) { ok = false; break; }
           tc::fence_after_sync();
-          const uint32_t qa = sQ + qb * C::kTileBytes, ka = sK + s * C::kTileBytes;
+          // (an operand's later steps: its descriptor plus a constant, the
+          // address field does not overflow)
+          const uint64_t qd = tc::sdesc_sw128(sQ + qb * C::kTileBytes, 16, 1024);
+          const uint64_t kd = tc::sdesc_sw128(sK + s * C::kTileBytes, 16, 1024);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
-            tc::mma_ss(tbase + kSCol + sb * 128, tc::sdesc_sw128(qa + o, 16, 1024),
-                       tc::sdesc_sw128(ka + o, 16, 1024), idS, ks > 0 ? 1u : 0u);
+            const uint32_t o = ((ks >> 2) * C::kHalfStep + (ks & 3) * 32) >> 4;
+            tc::mma_ss(tbase + kSCol + sb * 128, qd + o, kd + o, idS, ks > 0 ? 1u : 0u);
           }
           tc::mma_commit(s_full + sb);
           tc::mma_commit(k_empty + s);
@@ -420,12 +476,20 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
             break;
           }
           tc::fence_after_sync();
-          const uint32_t va = sV + s * C::kTileBytes;
+          const uint64_t vd = tc::sdesc_sw128(sV + s * C::kTileBytes, C::kHalfStep, 1024);
+          // (whole tiles apart: the queue of MMAs is shallow, and whatever the
+          // issuing thread does between two of them idles the tensor cores)
+          if (steps == 8) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            if (ks < steps)
+            for (int ks = 0; ks < 8; ++ks)
               tc::mma_ts(tbase + kOCol, tbase + kPCol + pb * 64 + ks * 8,
-                         tc::sdesc_sw128(va + ks * 2048, 16384, 1024), idO, (i > 0 || ks > 0) ? 1u : 0u);
+                         vd + (uint32_t)(ks * 2048 >> 4), idO, (i > 0 || ks > 0) ? 1u : 0u);
+          } else {
+#pragma unroll 1
+            for (int ks = 0; ks < steps; ++ks)
+              tc::mma_ts(tbase + kOCol, tbase + kPCol + pb * 64 + ks * 8,
+                         vd + (uint32_t)(ks * 2048 >> 4), idO, (i > 0 || ks > 0) ? 1u : 0u);
+          }
           tc::mma_commit(p_free + pb);
           tc::mma_commit(v_empty + s);
           if (i == w.count - 1) tc::mma_commit(o_full);
@@ -446,50 +510,64 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
     float* refv = reinterpret_cast<float*>(smem + C::kRefOff);  // [2 tile parity][128]
     float* rsum = reinterpret_cast<float*>(smem + C::kSumOff);  // [2 warpgroups][128]
     constexpr int kHalfD = D / NW;  // O columns each warpgroup stores
-    const int tok = fast_div(row, p.div_gp), hd = row - tok * p.gp;  // this row's token and head in the tile
-    const bool in_tile = tok < p.rt_tokens;
     bool ok = true;
     int g = 0, kk = 0;  // tiles and busy pieces so far
     for (int r = 0; ok; ++r) {
       const int pi = round_piece(r);
       if (pi >= n_pieces) break;
-      const ChunkPiece un = piece_at(p, pi);
-      const int b = un.b;
-      const int q_len = chunk_qlen(p, b), kv_len = p.kv_len[b];
-      const int off = kv_len - q_len;
-      const int i = un.rt * p.rt_tokens + tok;
-      const bool exists = in_tile && i < q_len;
-      const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[b] : 0, ob = p.cu_q ? 0 : b;
-      uint16_t* obase = p.o + ob * p.o_sb + (int64_t)un.hg * p.gp * p.o_sh;
-      float* lptr = p.lse + ob * p.lse_sb + (int64_t)(un.hg * p.gp + hd) * p.lse_sh + (qbase + i) * p.lse_ss;
-      if (un.count == 0) {
-        if (w == 0 && exists) {
-          uint16_t* optr = obase + (qbase + i) * p.o_ss + (int64_t)hd * p.o_sh;
-#pragma unroll
-          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(optr + c) = make_uint4(0, 0, 0, 0);
-          *lptr = -INFINITY;
+      // what the tile loop keeps live is little: the piece's tiles, this row's
+      // keys, and (GEN) its place and slope; the rest is read again after it
+      int kt0, count, jlo_r, jhi_r, place = 0;
+      float alibi_l2 = 0.f;
+      bool active;
+      {
+        const ChunkPiece un = piece_at(p, pi);
+        kt0 = un.kt0;
+        count = un.count;
+        const int q_len = chunk_qlen(p, un.b), kv_len = p.kv_len[un.b];
+        const int tok = fast_div(row, p.div_gp), i = un.rt * p.rt_tokens + tok;
+        const bool exists = tok < p.rt_tokens && i < q_len;
+        if (count == 0) {
+          if (w == 0 && exists) write_empty_row<D>(p, un.b, un.hg * p.gp + row - tok * p.gp, i);
+          continue;
         }
-        continue;
+        chunk_row_keys(p, i, kv_len - q_len, kv_len, p.prefix ? p.prefix[un.b] : 0, jlo_r, jhi_r);
+        if (!exists) { jlo_r = 0; jhi_r = INT_MAX; }  // whatever it computes is not stored
+        active = __any_sync(0xffffffffu, exists);
+        if (GEN) {
+          place = i + kv_len - q_len;
+          if (p.alibi && exists) alibi_l2 = __ldg(p.alibi + un.hg * p.gp + row - tok * p.gp) * kLog2e;
+        }
       }
-      int jlo_r, jhi_r;
-      chunk_row_keys(p, i, off, kv_len, p.prefix ? p.prefix[b] : 0, jlo_r, jhi_r);
-      if (!exists) { jlo_r = 1; jhi_r = 0; }
-      const bool active = __any_sync(0xffffffffu, exists);
-      const float alibi_l2 = (GEN && p.alibi && exists) ? __ldg(p.alibi + un.hg * p.gp + hd) * kLog2e : 0.f;
       float m_ref = -INFINITY;  // reference after the last tile seen
       float r_own = -INFINITY;  // reference this warpgroup's row sum is against
       float l = 0.f;
       const int it0 = (NW == 1 || (g & 1) == w) ? 0 : 1;
-      for (int it = it0; it < un.count; it += NW) {
+      if (!active) {
+        // no row of this warp exists: keep step on the barriers
+        for (int it = it0; ok && it < count; it += NW) {
+          const int gt = g + it;
+          ok = tc::mbar_wait(s_full + w, (gt / NW) & 1, abort_flag);
+          tc::mbar_arrive_relaxed(s_free + w);
+          if (NW == 2) {
+            ok = ok && (gt < 1 || tc::mbar_wait(refb + (w ^ 1), ((gt - 1) >> 1) & 1, abort_flag));
+            tc::mbar_arrive(refb + w);
+          }
+          ok = ok && (gt < NW || tc::mbar_wait(p_free + w, ((gt - NW) / NW) & 1, abort_flag));
+          tc::mbar_arrive_relaxed(p_full + w);
+        }
+      } else
+      for (int it = it0; it < count; it += NW) {
         const int gt = g + it;
         const int par = w;  // == gt % NW
-        const int j0 = (un.kt0 + it) * kKeysPerTile;
-        const bool part = it < un.fl || it > un.fh;
+        const int j0 = (kt0 + it) * kKeysPerTile;
+        // some row of the warp does not keep the whole tile
+        const bool part = __any_sync(0xffffffffu, jlo_r > j0 || jhi_r < j0 + kKeysPerTile - 1);
         if (!tc::mbar_wait(s_full + par, (gt / NW) & 1, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
         float2 x[64];
-        float mx = -INFINITY;
-        if (active) {
+        float mx;
+        {
           uint32_t t[4][32];
           const uint32_t sa = lane_base + kSCol + par * 128;
 #pragma unroll
@@ -503,20 +581,23 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
         }
         tc::fence_before_sync();
         tc::mbar_arrive_relaxed(s_free + par);  // the QK NW tiles on may overwrite this S buffer
-        if (active) {
+        {
           if constexpr (GEN) {
             // logits in log2 units: soft-cap or scale, then the distance penalty
             if (p.softcap > 0.f) {
+              // cap tanh(y) = cap - 2 cap / (1 + e^(2 y)); the rounding near 1 leaves
+              // about cap 2^-23 in the logit (5e-6 at cap 30)
+              const float k = 2.f * p.scale_log2 * p.inv_softcap, c1 = p.softcap * kLog2e;
 #pragma unroll
               for (int e = 0; e < 64; ++e)
-                x[e] = make_float2(softcap_log2(x[e].x * p.scale, p.softcap, p.inv_softcap),
-                                   softcap_log2(x[e].y * p.scale, p.softcap, p.inv_softcap));
+                x[e] = make_float2(fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x[e].x * k)), c1),
+                                   fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x[e].y * k)), c1));
             } else {
 #pragma unroll
               for (int e = 0; e < 64; ++e) x[e] = make_float2(x[e].x * p.scale_log2, x[e].y * p.scale_log2);
             }
             if (p.alibi) {
-              const float dist = (float)(i + off - j0);  // to the tile's first key
+              const float dist = (float)(place - j0);  // to the tile's first key
 #pragma unroll
               for (int e = 0; e < 64; ++e) {
                 x[e].x -= alibi_l2 * fabsf(dist - (float)(2 * e));
@@ -573,7 +654,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
           r_own = m_ref;
         }
         uint32_t pk[4][16];
-        if (active) {
+        {
           const float eref = (m_ref == -INFINITY) ? 0.f : m_ref;
           const float2 ner = make_float2(-eref, -eref);
           float2 acc[4];
@@ -594,7 +675,7 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
         }
         // this P buffer is free once the PV NW tiles back is done
         if (gt >= NW && !tc::mbar_wait(p_free + par, ((gt - NW) / NW) & 1, abort_flag)) { ok = false; break; }
-        if (active) {
+        {
           const uint32_t pa = lane_base + kPCol + par * 64;
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::tmem_st16(pa + c * 16, pk[c]);
@@ -605,12 +686,13 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
       }
       if (!ok) break;
       // ---- epilogue: both warpgroups' row sums against the final reference
-      const int gl = g + un.count - 1;  // the piece's last tile
-      g += un.count;
+      const int gl = g + count - 1;  // the piece's last tile
+      g += count;
       if (NW == 2 && (gl & 1) != w) {
         if (!tc::mbar_wait(refb + (gl & 1), (gl >> 1) & 1, abort_flag)) { ok = false; break; }
         m_ref = refv[(gl & 1) * 128 + row];
       }
+      const ChunkPiece un = piece_at(p, pi);
       // O is read out of TMEM before this warpgroup's row sum is posted: the
       // next piece's first PV overwrites O, and its P comes from a warpgroup
       // that has passed the row-sum barrier (with one warpgroup: from this
@@ -637,6 +719,9 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
       const bool empty = !(lt > 0.f);
       const float inv = empty ? 0.f : 1.f / lt;
       const float lse2 = empty ? -INFINITY : m_ref + __log2f(lt);
+      const int q_len = chunk_qlen(p, un.b);
+      const int tok = fast_div(row, p.div_gp), i = un.rt * p.rt_tokens + tok;
+      const bool exists = tok < p.rt_tokens && i < q_len;
       if (un.slot >= 0) {
         if (exists) {
           float* dst = p.part_o + ((int64_t)un.slot * kChunkRows + row) * D + w * kHalfD;
@@ -653,6 +738,8 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
         // through a warp-private staging tile: a thread packs its own row, then
         // each store instruction writes 64 contiguous bytes of 8 rows
         uint4* stg = reinterpret_cast<uint4*>(smem + C::kStageOff + (warp - 4) * 2048);  // [32 rows][4]
+        const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[un.b] : 0, ob = p.cu_q ? 0 : un.b;
+        uint16_t* obase = p.o + ob * p.o_sb + (int64_t)un.hg * p.gp * p.o_sh;
         uint16_t* orow[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -683,7 +770,8 @@ __global__ void __launch_bounds__(CCfg<D>::kThreads, CCfg<D>::kCtas)
           }
           __syncwarp();
         }
-        if (w == 0 && exists) *lptr = lse2 * kLn2;
+        if (w == 0 && exists)
+          p.lse[ob * p.lse_sb + (int64_t)(un.hg * p.gp + row - tok * p.gp) * p.lse_sh + (qbase + i) * p.lse_ss] = lse2 * kLn2;
       }
       ++kk;
     }
@@ -718,9 +806,9 @@ bool encode_map(CUtensorMap* m, const void* base, int d, int heads, int64_t rows
   return r == CUDA_SUCCESS;
 }
 
-template <int D, bool GEN, bool F16>
-cudaError_t launch_v(const ChunkParams& p, cudaStream_t st) {
-  using C = CCfg<D>;
+template <int D, int NP, bool GEN, bool F16>
+cudaError_t launch_v(const ChunkParams& p, bool overlap, cudaStream_t st) {
+  using C = CCfg<D, NP>;
   // setmaxnreg.inc would wait forever if the block were launched with fewer
   // registers than the split assumes: launch only when the build matches.
   static std::atomic<int> launch_regs{-1};
@@ -728,12 +816,12 @@ cudaError_t launch_v(const ChunkParams& p, cudaStream_t st) {
   cudaError_t e;
   if (regs < 0) {
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, chunk_kernel<D, GEN, F16>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, chunk_kernel<D, NP, GEN, F16>)) != cudaSuccess) return e;
     regs = fa.numRegs;
     launch_regs.store(regs, std::memory_order_relaxed);
   }
   if (regs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  if ((e = ensure_smem_attr<chunk_kernel<D, GEN, F16>>(C::kSmem)) != cudaSuccess) return e;
+  if ((e = ensure_smem_attr<chunk_kernel<D, NP, GEN, F16>>(C::kSmem)) != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   const bool packed = p.cu_q != nullptr;
   const int heads_kv = p.Hq / p.G;
@@ -742,15 +830,15 @@ cudaError_t launch_v(const ChunkParams& p, cudaStream_t st) {
       !encode_map(&mk, p.k, D, heads_kv, p.cache_rows, p.cache_outer, p.k_sh, p.k_ss, p.k_sb, 1, p.box_rows, F16) ||
       !encode_map(&mv, p.v, D, heads_kv, p.cache_rows, p.cache_outer, p.v_sh, p.v_ss, p.v_sb, 1, p.box_rows, F16))
     return cudaErrorInvalidValue;
-  chunk_kernel<D, GEN, F16><<<(unsigned)p.grid, C::kThreads, C::kSmem, st>>>(p, mq, mk, mv);
-  return cudaGetLastError();
+  return launch_overlapped(chunk_kernel<D, NP, GEN, F16>, (unsigned)p.grid, C::kThreads, C::kSmem, overlap, st, p, mq, mk, mv);
 }
 
 template <bool F16>
-cudaError_t launch_t(const ChunkParams& p, cudaStream_t st) {
+cudaError_t launch_t(const ChunkParams& p, bool overlap, cudaStream_t st) {
   const bool gen = p.softcap > 0.f || p.alibi;
-  if (p.d == 64) return gen ? launch_v<64, true, F16>(p, st) : launch_v<64, false, F16>(p, st);
-  return gen ? launch_v<128, true, F16>(p, st) : launch_v<128, false, F16>(p, st);
+  if (p.d == 64) return gen ? launch_v<64, 1, true, F16>(p, overlap, st) : launch_v<64, 1, false, F16>(p, overlap, st);
+  if (p.box_rows <= 16) return gen ? launch_v<128, 3, true, F16>(p, overlap, st) : launch_v<128, 3, false, F16>(p, overlap, st);
+  return gen ? launch_v<128, 1, true, F16>(p, overlap, st) : launch_v<128, 1, false, F16>(p, overlap, st);
 }
 
 }  // namespace
@@ -758,10 +846,12 @@ cudaError_t launch_t(const ChunkParams& p, cudaStream_t st) {
 // The fp16 instantiations build in their own translation unit (chunk_f16.cu
 // includes this file with MFA_CHUNK_F16_UNIT defined), in parallel.
 #ifndef MFA_CHUNK_F16_UNIT
-int chunk_ctas_per_sm(int d) { return d == 64 ? CCfg<64>::kCtas : CCfg<128>::kCtas; }
-cudaError_t launch_chunk_attn(const ChunkParams& p, cudaStream_t st) { return launch_t<false>(p, st); }
+int chunk_ctas_per_sm(int d) { return d == 64 ? CCfg<64, 1>::kCtas : CCfg<128, 1>::kCtas; }
+cudaError_t launch_chunk_attn(const ChunkParams& p, bool overlap, cudaStream_t st) { return launch_t<false>(p, overlap, st); }
 #else
-cudaError_t launch_chunk_attn_f16(const ChunkParams& p, cudaStream_t st) { return launch_t<true>(p, st); }
+cudaError_t launch_chunk_attn_f16(const ChunkParams& p, bool overlap, cudaStream_t st) {
+  return launch_t<true>(p, overlap, st);
+}
 #endif
 
 }  // namespace mfa
