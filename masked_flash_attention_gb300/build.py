@@ -1,20 +1,24 @@
-"""Build libmfa_gb300.so in-tree with nvcc for sm_103a (GB300).
+"""Build libmfa_gb300.so in-tree with nvcc for sm_103a (GB300), and _binding.so,
+the CPython module of the short calls, against it and torch's headers.
 
-Each CUDA translation unit is compiled in parallel, then linked into one
-shared library next to this file.  Nothing is installed anywhere.
+Each translation unit is compiled in parallel, then linked into one shared
+library and one module next to this file.  Nothing is installed anywhere.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmfa_gb300.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["api.cu", "sched.cu", "topk.cu", "decode.cu", "prefill_sm103.cu", "prefill_f16.cu", "backward.cu", "backward_sm103.cu", "noalloc.cu", "rope.cu", "chunk.cu", "chunk_sm103.cu",
            "chunk_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,6 +33,13 @@ def nvcc() -> str:
     return cand
 
 
+def torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")  # found, not imported
+    if spec is None:
+        raise RuntimeError("torch not found: the binding is compiled against its headers")
+    return os.path.dirname(spec.origin)
+
+
 def _deps_mtime() -> float:
     m = 0.0
     for d in (CSRC, os.path.join(ROOT, "include")):
@@ -39,7 +50,8 @@ def _deps_mtime() -> float:
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile (if stale) and return the path of the shared library."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    outputs = (LIB, BINDING)
+    if not force and all(os.path.exists(f) for f in outputs) and min(map(os.path.getmtime, outputs)) >= _deps_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -55,14 +67,33 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        obj = os.path.join(BUILD, "binding.o")
+        include = [os.path.join(ROOT, "include"), os.path.join(torch_dir(), "include"),
+                   os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"),
+                   sysconfig.get_paths()["include"]]
+        run(["g++", "-O2", "-std=c++17", "-fPIC", *("-I" + d for d in include), "-c",
+             os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ failed for binding.cpp")
+        return obj
+
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    run([cc, *ARCH, "-shared", "-o", tmp, *objs], "link failed")
     os.replace(tmp, LIB)
+    # torch's libraries are those that `import torch` has loaded, the kernels' library is the one beside the module
+    tmp = BINDING + ".tmp"
+    run(["g++", "-shared", "-o", tmp, binding_obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+         "-L" + os.path.join(torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"],
+        "link of the binding failed")
+    os.replace(tmp, BINDING)
     return LIB
 
 
