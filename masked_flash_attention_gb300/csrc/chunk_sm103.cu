@@ -25,7 +25,7 @@
 // Warp roles (12 or 16 warps; 8 at d = 64, two CTAs per SM): 0 K producer, 1 QK
 // issuer and Q producer, 2 V producer, 3 PV issuer, 4.. one or two softmax
 // warpgroups, which at d = 128 take alternate key tiles of a piece and hand the
-// row references from tile to tile through shared memory, 12.. more producers.  A warp none of whose
+// row references from tile to tile through shared memory, 12 and 13 more producers.  A warp none of whose
 // rows exists keeps step on the barriers and computes nothing.
 //
 // Every mbarrier wait is bounded (1 s); on a time-out the kernel records
@@ -50,15 +50,16 @@ namespace mfa {
 namespace {
 
 // NP producer warps per operand.  A warp issues a TMA copy only every 65 to 90
-// cycles while the SM's TMA unit takes one in about 28: at d = 128 a page of 16
-// rows makes 32 copies per K/V tile, and with boxes that small a fourth
-// warpgroup shares them, three warps per operand (2048 tokens over 32768 keys,
-// page 16: 1113 us with one warp, 966 us with three; page 64: 822 and 882 us,
-// the registers it takes slowing the others).  At d = 64 a box is one copy and
-// the two CTAs of an SM issue side by side: one warp.
+// cycles, and at d = 128 a page of 16 rows makes 32 copies per K/V tile: with
+// boxes that small and many query rows, two warps of a fourth warpgroup share
+// them.  Otherwise one warp is better: more warps cost the others instruction
+// issue.  Measured, one and two warps (three were slower than two): 4 x 512
+// tokens over 4096 keys, page 16: 139 and 120 us (page 64: 111 with one); 64
+// single tokens over up to 8192 keys, page 16: 164 and 175 us.
 // Register split: with one producer warp per operand 384 threads launch at 168
-// registers, of which the softmax warpgroups take 216 and the others keep 72; the
-// blocks of 512 threads, and d = 64, launch at 128 and are split 40 / 216.
+// registers, of which the softmax warpgroups take 216 and the others keep 72;
+// with two, 512 threads launch at 128, split 72 / 184; d = 64 launches 256
+// threads at 128, split 40 / 216.
 template <int D, int NP_>
 struct CCfg {
   static constexpr int NP = NP_;
@@ -66,15 +67,17 @@ struct CCfg {
   static constexpr int kThreads = 128 + 128 * NW + (NP > 1 ? 128 : 0);
   static constexpr int kCtas = D == 64 ? 2 : 1;  // per SM
   static constexpr int kLaunchRegs = (D == 64 || NP > 1) ? 128 : 168;
-  static constexpr int kIssueRegs = (D == 64 || NP > 1) ? 40 : 72;
-  static constexpr int kSoftmaxRegs = 216;
-  static_assert(NP == 1 || (NP == 3 && D == 128), "the role table has one or three warps per operand");
+  static constexpr int kIssueRegs = D == 64 ? 40 : 72;
+  static constexpr int kSoftmaxRegs = NP > 1 ? 184 : 216;
+  static_assert(NP == 1 || (NP == 2 && NW == 2), "the role table has one or two warps per operand");
   static_assert((kThreads - 128 * NW) * kIssueRegs + 128 * NW * kSoftmaxRegs <= kThreads * kLaunchRegs,
                 "the register split must fit the block's launch allocation");
-  static constexpr uint32_t kCols = NW == 2 ? 512 : 256;  // TMEM: S and P buffers, O
-  static constexpr uint32_t kSCol = 0;
-  static constexpr uint32_t kPCol = 128 * NW;
-  static constexpr uint32_t kOCol = kPCol + 64 * NW;
+  // TMEM.  Two warpgroups: three S buffers, each overwritten by its P, and O;
+  // one: S, P and O.
+  static constexpr uint32_t kCols = NW == 2 ? 512 : 256;
+  static constexpr int NB = NW == 2 ? 3 : 1;            // S / P buffers, 128 columns of S each
+  static constexpr uint32_t kPCol = NW == 2 ? 0 : 128;  // P of buffer b: kPCol + 128 b
+  static constexpr uint32_t kOCol = NW == 2 ? 384 : 192;
   static constexpr int NQ = D == 128 ? 1 : 2;
   static constexpr int NSK = D == 128 ? 3 : 2;
   static constexpr int NSV = 2;
@@ -86,8 +89,8 @@ struct CCfg {
   static constexpr int kVOff = kKOff + NSK * kTileBytes;
   static constexpr int kAuxOff = kVOff + NSV * kTileBytes;  // barriers and flags
   static constexpr int kRefOff = kAuxOff + 512;             // row references [2][128]
-  static constexpr int kSumOff = kRefOff + 2 * 128 * 4;     // row sums [2][128]
-  static constexpr int kStageOff = kSumOff + 2 * 128 * 4;   // output staging, 2 KB per softmax warp
+  static constexpr int kSumOff = kRefOff + 2 * 128 * 4;     // row sums [2][2][128]
+  static constexpr int kStageOff = kSumOff + 2 * 2 * 128 * 4;   // output staging, 2 KB per softmax warp
   static constexpr int kSmem = kStageOff + 4 * NW * 2048 + 1024;
   static_assert(kSmem <= (kCtas == 1 ? 227 * 1024 : 113 * 1024), "shared memory budget");
   static_assert(kOCol + D <= kCols, "TMEM budget");
@@ -130,13 +133,15 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float row_max(const float2 (&x)[64]) {
-  float m[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m[k] = fmaxf(x[k].x, x[k].y);
-#pragma unroll
-  for (int i = 8; i < 64; ++i) m[i & 7] = max3f(m[i & 7], x[i].x, x[i].y);
-  return fmaxf(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], max3f(m[5], m[6], m[7])));
+// Waits for this thread's TMEM loads; the registers pass through, so that no use
+// of theirs moves before the wait.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 __device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
@@ -310,7 +315,8 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using C = CCfg<D, NP>;
   constexpr int NSK = C::NSK, NSV = C::NSV, NQ = C::NQ, NW = C::NW;
-  constexpr uint32_t kSCol = C::kSCol, kPCol = C::kPCol, kOCol = C::kOCol;
+  constexpr uint32_t kPCol = C::kPCol, kOCol = C::kOCol;
+  constexpr int NB = C::NB;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -324,13 +330,13 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
   uint64_t* v_full = k_empty + NSK;  // [NSV]
   uint64_t* v_empty = v_full + NSV;  // [NSV]
   uint64_t* v_tail = v_empty + NSV;  // [1] copies of a V tile whose end is zeroed
-  uint64_t* s_full = v_tail + 1;     // [2] S buffer written by QK
-  uint64_t* s_free = s_full + 2;     // [2] S buffer read by the softmax (128 arrivals)
-  uint64_t* p_full = s_free + 2;     // [2] P buffer written, O rescaled (128 arrivals)
-  uint64_t* p_free = p_full + 2;     // [2] PV reading a P buffer done
-  uint64_t* o_full = p_free + 2;     // [1] last PV of a piece done
+  uint64_t* s_full = v_tail + 1;     // [NB] S buffer written by QK
+  uint64_t* p_full = s_full + NB;    // [NB] P buffer written, O rescaled (128 arrivals)
+  uint64_t* p_free = p_full + NB;    // [NB] PV reading a P buffer done
+  uint64_t* s_free = p_free + NB;    // [1] one warpgroup: S read by the softmax (128 arrivals)
+  uint64_t* o_full = s_free + 1;     // [1] last PV of a piece done
   uint64_t* drained = o_full + 1;    // [2] all MMAs of an issuer done (teardown)
-  uint64_t* sumx = drained + 2;      // [1] row sums of both warpgroups posted (256 arrivals)
+  uint64_t* sumx = drained + 2;      // [1] row sums of all warpgroups posted (128 NW arrivals)
   uint64_t* refb = sumx + 1;         // [2 tile parity] row references posted (128 arrivals)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(refb + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -339,10 +345,6 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
     for (int k = 0; k < 2; ++k) {
       tc::mbar_init(q_full + k, 1);
       tc::mbar_init(q_empty + k, 1);
-      tc::mbar_init(s_full + k, 1);
-      tc::mbar_init(s_free + k, 128);
-      tc::mbar_init(p_full + k, 128);
-      tc::mbar_init(p_free + k, 1);
       tc::mbar_init(drained + k, 1);
       tc::mbar_init(refb + k, 128);
     }
@@ -355,7 +357,13 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       tc::mbar_init(v_empty + s, 1);
     }
     tc::mbar_init(v_tail, NP);
-    tc::mbar_init(sumx, 256);
+    for (int k = 0; k < NB; ++k) {
+      tc::mbar_init(s_full + k, 1);
+      tc::mbar_init(p_full + k, 128);
+      tc::mbar_init(p_free + k, 1);
+    }
+    tc::mbar_init(s_free, 128);
+    tc::mbar_init(sumx, 128 * NW);
     tc::mbar_init(o_full, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -372,17 +380,17 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
   const int n_pieces = p.counts->n_pieces;
 
   if (warp < 4 || warp >= 4 + 4 * NW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
-  if (warp == 0 || warp == 2 || warp >= 4 + 4 * NW) {
+  if (warp == 0 || warp == 2 || (NP == 2 && (warp == 12 || warp == 13))) {
     // ------------------------------------------------------------ producers
-    // NP warps per operand: K warps 0, 12, 13, V warps 2, 14, 15
-    const int part = warp < 4 ? 0 : 1 + (warp & 1);
-    const bool is_k = warp < 4 ? warp == 0 : warp < 6 + 4 * NW;
+    // K: warp 0 (and 12), V: warp 2 (and 13)
+    const int part = warp < 4 ? 0 : 1;
+    const bool is_k = warp == 0 || warp == 12;
     produce<D, NP>(p, is_k, is_k ? NSK : NSV, is_k ? &tmk : &tmv, n_pieces, part, lane, is_k ? k_full : v_full,
                    is_k ? k_empty : v_empty, v_tail, smem + (is_k ? C::kKOff : C::kVOff), abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issuer
-    // S[g % NW] = Q K_g^T for the g-th tile of this CTA, as soon as the softmax
-    // has read that S buffer NW tiles back; and Q: with two buffers the next
+    // S[g % NB] = Q K_g^T for the g-th tile of this CTA, as soon as that buffer is
+    // free: the PV of its P done (one warpgroup: S read by the softmax); and Q: with two buffers the next
     // piece's while the current one runs, with one once its QKs are done.
     if (lane == 0) {
       constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128, false, false, F16);
@@ -410,9 +418,12 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
         const int un = next_busy(p, n_pieces, u + 1, wn);
         if (!tc::mbar_wait(q_full + qb, (kk / NQ) & 1, abort_flag)) { ok = false; break; }
         for (int i = 0; i < w.count; ++i, ++g) {
-          const int s = g % NSK, sb = g % NW;
+          const int s = g % NSK, sb = g % NB;
           if (!tc::mbar_wait(k_full + s, (g / NSK) & 1, abort_flag)) { ok = false; break; }
-          if (g >= NW && !tc::mbar_wait(s_free + sb, ((g - NW) / NW) & 1, abort_flag)) { ok = false; break; }
+          if (g >= NB && !tc::mbar_wait(NW == 2 ? p_free + sb : s_free, ((g - NB) / NB) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
           tc::fence_after_sync();
           // (an operand's later steps: its descriptor plus a constant, the
           // address field does not overflow)
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = ((ks >> 2) * C::kHalfStep + (ks & 3) * 32) >> 4;
-            tc::mma_ss(tbase + kSCol + sb * 128, qd + o, kd + o, idS, ks > 0 ? 1u : 0u);
+            tc::mma_ss(tbase + sb * 128, qd + o, kd + o, idS, ks > 0 ? 1u : 0u);
           }
           tc::mma_commit(s_full + sb);
           tc::mma_commit(k_empty + s);
@@ -457,7 +468,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------------ PV issuer
-    // O (+)= P[g % NW] V_g once the softmax of tile g has written P (and
+    // O (+)= P[g % NB] V_g once the softmax of tile g has written P (and
     // rescaled O), over the 16-key steps that hold keys.
     if (lane == 0) {
       constexpr uint32_t idO = tc::idesc_bf16_f32(128, D, false, true, F16);
@@ -468,9 +479,9 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       for (int r = next_busy(p, n_pieces, 0, w); ok && r >= 0; r = next_busy(p, n_pieces, r + 1, w)) {
         const int kv = p.kv_len[w.b];
         for (int i = 0; i < w.count; ++i, ++g) {
-          const int s = g % NSV, pb = g % NW;
+          const int s = g % NSV, pb = g % NB;
           const int steps = min(8, (kv - (w.kt0 + i) * kKeysPerTile + 15) / 16);
-          if (!tc::mbar_wait(p_full + pb, (g / NW) & 1, abort_flag) ||
+          if (!tc::mbar_wait(p_full + pb, (g / NB) & 1, abort_flag) ||
               !tc::mbar_wait(v_full + s, (g / NSV) & 1, abort_flag)) {
             ok = false;
             break;
@@ -482,12 +493,12 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
           if (steps == 8) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              tc::mma_ts(tbase + kOCol, tbase + kPCol + pb * 64 + ks * 8,
+              tc::mma_ts(tbase + kOCol, tbase + kPCol + pb * 128 + ks * 8,
                          vd + (uint32_t)(ks * 2048 >> 4), idO, (i > 0 || ks > 0) ? 1u : 0u);
           } else {
 #pragma unroll 1
             for (int ks = 0; ks < steps; ++ks)
-              tc::mma_ts(tbase + kOCol, tbase + kPCol + pb * 64 + ks * 8,
+              tc::mma_ts(tbase + kOCol, tbase + kPCol + pb * 128 + ks * 8,
                          vd + (uint32_t)(ks * 2048 >> 4), idO, (i > 0 || ks > 0) ? 1u : 0u);
           }
           tc::mma_commit(p_free + pb);
@@ -500,7 +511,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       tc::mbar_wait_drain(drained + 1, 0, 200000000ull);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 4 + 4 * NW) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------ softmax
     const int w = NW == 2 ? (warp - 4) >> 2 : 0;
@@ -508,10 +519,21 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
     const int row = 32 * wq + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(32 * wq) << 16);
     float* refv = reinterpret_cast<float*>(smem + C::kRefOff);  // [2 tile parity][128]
-    float* rsum = reinterpret_cast<float*>(smem + C::kSumOff);  // [2 warpgroups][128]
+    float* rsum = reinterpret_cast<float*>(smem + C::kSumOff);  // [2][2 warpgroups][128]
     constexpr int kHalfD = D / NW;  // O columns each warpgroup stores
     bool ok = true;
     int g = 0, kk = 0;  // tiles and busy pieces so far
+    // buffer of this warpgroup's next tile and the parity of its use; tiles come
+    // NW apart whatever the pieces' lengths
+    int sb = NW == 2 ? w : 0;
+    uint32_t use = 0;
+    auto advance = [&] {
+      sb += NW;
+      if (sb >= NB) {
+        sb -= NB;
+        use ^= 1;
+      }
+    };
     for (int r = 0; ok; ++r) {
       const int pi = round_piece(r);
       if (pi >= n_pieces) break;
@@ -542,46 +564,38 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       float m_ref = -INFINITY;  // reference after the last tile seen
       float r_own = -INFINITY;  // reference this warpgroup's row sum is against
       float l = 0.f;
-      const int it0 = (NW == 1 || (g & 1) == w) ? 0 : 1;
+      const int it0 = (NW == 1 || (g & 1) == w) ? 0 : 1;  // the piece's first tile that is this warpgroup's
       if (!active) {
         // no row of this warp exists: keep step on the barriers
         for (int it = it0; ok && it < count; it += NW) {
           const int gt = g + it;
-          ok = tc::mbar_wait(s_full + w, (gt / NW) & 1, abort_flag);
-          tc::mbar_arrive_relaxed(s_free + w);
+          ok = tc::mbar_wait(s_full + sb, use, abort_flag);
+          if (NW == 1) tc::mbar_arrive_relaxed(s_free);
           if (NW == 2) {
-            ok = ok && (gt < 1 || tc::mbar_wait(refb + (w ^ 1), ((gt - 1) >> 1) & 1, abort_flag));
-            tc::mbar_arrive(refb + w);
+            ok = ok && (gt < 1 || tc::mbar_wait(refb + ((gt - 1) & 1), ((gt - 1) >> 1) & 1, abort_flag));
+            tc::mbar_arrive(refb + (gt & 1));
           }
-          ok = ok && (gt < NW || tc::mbar_wait(p_free + w, ((gt - NW) / NW) & 1, abort_flag));
-          tc::mbar_arrive_relaxed(p_full + w);
+          if (NW == 1) ok = ok && (gt < 1 || tc::mbar_wait(p_free, (gt - 1) & 1, abort_flag));
+          tc::mbar_arrive_relaxed(p_full + sb);
+          advance();
         }
       } else
       for (int it = it0; it < count; it += NW) {
         const int gt = g + it;
-        const int par = w;  // == gt % NW
         const int j0 = (kt0 + it) * kKeysPerTile;
         // some row of the warp does not keep the whole tile
         const bool part = __any_sync(0xffffffffu, jlo_r > j0 || jhi_r < j0 + kKeysPerTile - 1);
-        if (!tc::mbar_wait(s_full + par, (gt / NW) & 1, abort_flag)) { ok = false; break; }
+        if (!tc::mbar_wait(s_full + sb, use, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
-        float2 x[64];
-        float mx;
-        {
-          uint32_t t[4][32];
-          const uint32_t sa = lane_base + kSCol + par * 128;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::tmem_ld32(sa + c * 32, t[c]);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[c * 16 + e] = make_float2(__uint_as_float(t[c][2 * e]), __uint_as_float(t[c][2 * e + 1]));
-        }
-        tc::fence_before_sync();
-        tc::mbar_arrive_relaxed(s_free + par);  // the QK NW tiles on may overwrite this S buffer
-        {
+        // The row is taken in four runs of 32 columns, twice: from the last to the
+        // first for the maximum (with the logits' transforms, which are left in
+        // TMEM), and back for the exponentials, each run loaded while the one
+        // before it is worked on.  The loops are not unrolled further: four warps
+        // of instruction stream share a fetch path that this code is bound by.
+        const uint32_t sa = lane_base + sb * 128, pa = lane_base + kPCol + sb * 128;
+        uint32_t xa[32], xb[32];
+        float mx = -INFINITY;
+        auto first_pass = [&](uint32_t (&x)[32], int c) {
           if constexpr (GEN) {
             // logits in log2 units: soft-cap or scale, then the distance penalty
             if (p.softcap > 0.f) {
@@ -589,100 +603,119 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
               // about cap 2^-23 in the logit (5e-6 at cap 30)
               const float k = 2.f * p.scale_log2 * p.inv_softcap, c1 = p.softcap * kLog2e;
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                x[e] = make_float2(fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x[e].x * k)), c1),
-                                   fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x[e].y * k)), c1));
+              for (int e = 0; e < 32; ++e)
+                x[e] = __float_as_uint(fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(__uint_as_float(x[e]) * k)), c1));
             } else {
 #pragma unroll
-              for (int e = 0; e < 64; ++e) x[e] = make_float2(x[e].x * p.scale_log2, x[e].y * p.scale_log2);
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.scale_log2);
             }
             if (p.alibi) {
-              const float dist = (float)(place - j0);  // to the tile's first key
+              const float dist = (float)(place - j0 - 32 * c);  // to the run's first key
 #pragma unroll
-              for (int e = 0; e < 64; ++e) {
-                x[e].x -= alibi_l2 * fabsf(dist - (float)(2 * e));
-                x[e].y -= alibi_l2 * fabsf(dist - (float)(2 * e + 1));
-              }
+              for (int e = 0; e < 32; ++e)
+                x[e] = __float_as_uint(__uint_as_float(x[e]) - alibi_l2 * fabsf(dist - (float)e));
             }
           }
           if (part) {
-            // the row keeps keys clo .. clo + span of the tile; a row that keeps
+            // the row keeps keys clo .. clo + span of the run; a row that keeps
             // none gets a start no key reaches.  (The scale is positive, so
             // a raw -inf stays -inf through it.)
             const bool none = jhi_r < jlo_r;
-            const int clo = none ? (1 << 20) : jlo_r - j0;
+            const int clo = none ? (1 << 20) : jlo_r - j0 - 32 * c;
             const unsigned span = none ? 0u : (unsigned)(jhi_r - jlo_r);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              x[e].x = (unsigned)(2 * e - clo) <= span ? x[e].x : -INFINITY;
-              x[e].y = (unsigned)(2 * e + 1 - clo) <= span ? x[e].y : -INFINITY;
-            }
+            for (int e = 0; e < 32; ++e) x[e] = (unsigned)(e - clo) <= span ? x[e] : __float_as_uint(-INFINITY);
           }
-          mx = row_max(x);
-          if constexpr (!GEN) mx *= p.scale_log2;
+          if ((GEN || part) && c > 0) tc::tmem_st32(sa + c * 32, x);
+          float m[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[k] = __uint_as_float(x[k]);
+#pragma unroll
+          for (int e = 4; e < 32; e += 2)
+            m[(e >> 1) & 3] = max3f(m[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          mx = max3f(mx, max3f(m[0], m[1], m[2]), m[3]);
+        };
+        tc::tmem_ld32(sa + 96, xa);
+        tmem_loaded(xa);
+#pragma unroll 1
+        for (int c = 3; c > 0; c -= 2) {
+          tc::tmem_ld32(sa + (c - 1) * 32, xb);
+          first_pass(xa, c);
+          tmem_loaded(xb);
+          if (c > 1) tc::tmem_ld32(sa + (c - 2) * 32, xa);
+          first_pass(xb, c - 1);
+          if (c > 1) tmem_loaded(xa);
         }
+        if constexpr (!GEN) mx *= p.scale_log2;
+        if (GEN || part) tc::tmem_wait_st();
         // the reference after tile gt - 1
-        if (NW == 2 && gt >= 1 && !tc::mbar_wait(refb + (par ^ 1), ((gt - 1) >> 1) & 1, abort_flag)) {
+        if (NW == 2 && gt >= 1 && !tc::mbar_wait(refb + ((gt - 1) & 1), ((gt - 1) >> 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
-        const float m_prev = (it == 0) ? -INFINITY : (NW == 2 ? refv[(par ^ 1) * 128 + row] : m_ref);
+        const float m_prev = (it == 0) ? -INFINITY : (NW == 2 ? refv[((gt - 1) & 1) * 128 + row] : m_ref);
         const bool upd = mx > m_prev + 8.f;  // raise the reference only when outgrown by 2^8
         m_ref = upd ? mx : m_prev;
         if (NW == 2) {
-          refv[par * 128 + row] = m_ref;
-          tc::mbar_arrive(refb + par);
+          refv[(gt & 1) * 128 + row] = m_ref;
+          tc::mbar_arrive(refb + (gt & 1));
         }
         if (it != 0 && __any_sync(0xffffffffu, upd && m_prev != -INFINITY)) {
           // O holds the PV of tile gt - 1 (against m_prev) once that PV is done
-          if (!tc::mbar_wait(p_free + (gt - 1) % NW, ((gt - 1) / NW) & 1, abort_flag)) { ok = false; break; }
+          const int pb = sb > 0 ? sb - 1 : NB - 1;
+          if (!tc::mbar_wait(p_free + pb, sb > 0 ? use : use ^ 1, abort_flag)) { ok = false; break; }
           tc::fence_after_sync();
           const float f = (upd && m_prev != -INFINITY) ? fast_exp2(m_prev - m_ref) : 1.f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t t[32];
             const uint32_t a = lane_base + kOCol + c * 32;
-            tc::tmem_ld32(a, t);
-            tc::tmem_wait_ld();
+            tc::tmem_ld32(a, xa);
+            tmem_loaded(xa);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * f);
-            tc::tmem_st32(a, t);
+            for (int e = 0; e < 32; ++e) xa[e] = __float_as_uint(__uint_as_float(xa[e]) * f);
+            tc::tmem_st32(a, xa);
           }
         }
         if (r_own != m_ref) {
           l = (r_own == -INFINITY) ? 0.f : l * fast_exp2(r_own - m_ref);
           r_own = m_ref;
         }
-        uint32_t pk[4][16];
-        {
-          const float eref = (m_ref == -INFINITY) ? 0.f : m_ref;
-          const float2 ner = make_float2(-eref, -eref);
-          float2 acc[4];
+        // one warpgroup: the P buffer is free once the PV before is done (with
+        // two, the QK into this S buffer has waited for it)
+        if (NW == 1 && gt >= 1 && !tc::mbar_wait(p_free, (gt - 1) & 1, abort_flag)) { ok = false; break; }
+        const float eref = (m_ref == -INFINITY) ? 0.f : m_ref;
+        const float2 ner = make_float2(-eref, -eref), sl2 = make_float2(p.scale_log2, p.scale_log2);
+        float2 acc[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q] = make_float2(0.f, 0.f);
-          const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+        for (int q = 0; q < 4; ++q) acc[q] = make_float2(0.f, 0.f);
+        auto second_pass = [&](const uint32_t (&x)[32], int c) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 v = GEN ? add2(x[c * 16 + e], ner) : fma2(x[c * 16 + e], sl2, ner);
-              const float2 pe = make_float2(fast_exp2(v.x), fast_exp2(v.y));
-              acc[e & 3] = add2(acc[e & 3], pe);
-              pk[c][e] = pack2<F16>(pe.x, pe.y);
-            }
-          acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-          l += acc[0].x + acc[0].y;
+          for (int e = 0; e < 16; ++e) {
+            const float2 xe = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            const float2 v = GEN ? add2(xe, ner) : fma2(xe, sl2, ner);
+            const float2 pe = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+            acc[e & 3] = add2(acc[e & 3], pe);
+            pk[e] = pack2<F16>(pe.x, pe.y);
+          }
+          tc::tmem_st16(pa + c * 16, pk);
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tc::tmem_ld32(sa + (c + 1) * 32, xa);
+          second_pass(xb, c);
+          tmem_loaded(xa);
+          if (c < 2) tc::tmem_ld32(sa + (c + 2) * 32, xb);
+          second_pass(xa, c + 1);
+          if (c < 2) tmem_loaded(xb);
         }
-        // this P buffer is free once the PV NW tiles back is done
-        if (gt >= NW && !tc::mbar_wait(p_free + par, ((gt - NW) / NW) & 1, abort_flag)) { ok = false; break; }
-        {
-          const uint32_t pa = lane_base + kPCol + par * 64;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::tmem_st16(pa + c * 16, pk[c]);
-          tc::tmem_wait_st();
-        }
+        acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+        l += acc[0].x + acc[0].y;
+        tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive_relaxed(p_full + par);
+        if (NW == 1) tc::mbar_arrive_relaxed(s_free);  // the next QK may overwrite S
+        tc::mbar_arrive_relaxed(p_full + sb);
+        advance();
       }
       if (!ok) break;
       // ---- epilogue: both warpgroups' row sums against the final reference
@@ -704,13 +737,16 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       for (int c = 0; c < kHalfD / 32; ++c) tc::tmem_ld32(lane_base + kOCol + w * kHalfD + c * 32, ro[c]);
       float lt;
       if constexpr (NW == 2) {
-        rsum[w * 128 + row] = (r_own == m_ref || r_own == -INFINITY) ? l : l * fast_exp2(r_own - m_ref);
+        // (two sets of sums: a warpgroup may write the next piece's while another
+        // still reads these)
+        float* rs = rsum + (kk & 1) * 256;
+        rs[w * 128 + row] = (r_own == m_ref || r_own == -INFINITY) ? l : l * fast_exp2(r_own - m_ref);
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         tc::mbar_arrive(sumx);
         if (!tc::mbar_wait(sumx, kk & 1, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
-        lt = rsum[row] + rsum[128 + row];
+        lt = rs[row] + rs[128 + row];
       } else {
         tc::tmem_wait_ld();
         tc::fence_before_sync();
@@ -836,8 +872,10 @@ cudaError_t launch_v(const ChunkParams& p, bool overlap, cudaStream_t st) {
 template <bool F16>
 cudaError_t launch_t(const ChunkParams& p, bool overlap, cudaStream_t st) {
   const bool gen = p.softcap > 0.f || p.alibi;
-  if (p.d == 64) return gen ? launch_v<64, 1, true, F16>(p, overlap, st) : launch_v<64, 1, false, F16>(p, overlap, st);
-  if (p.box_rows <= 16) return gen ? launch_v<128, 3, true, F16>(p, overlap, st) : launch_v<128, 3, false, F16>(p, overlap, st);
+  if (p.d == 64)
+    return gen ? launch_v<64, 1, true, F16>(p, overlap, st) : launch_v<64, 1, false, F16>(p, overlap, st);
+  if (p.box_rows <= 16 && (int64_t)p.Sq * p.gp > 32)  // (CCfg)
+    return gen ? launch_v<128, 2, true, F16>(p, overlap, st) : launch_v<128, 2, false, F16>(p, overlap, st);
   return gen ? launch_v<128, 1, true, F16>(p, overlap, st) : launch_v<128, 1, false, F16>(p, overlap, st);
 }
 
