@@ -36,7 +36,7 @@ constexpr int kTailFlag = 1 << 30;                // in a row tile's second word
 // Cost model, in key tiles (about 0.8 us of a CTA): what a piece costs beside
 // its tiles (its start, Q, the epilogue), what leaving a partial and joining it
 // costs more, and what there being any to join does.
-constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 2.f;
+constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 4.f;
 constexpr int kMaxTailCut = 8;
 
 __device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
@@ -312,52 +312,54 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// One warp per row of a split unit: the weights of its pieces from their
-// log-sum-exps, then the weighted sum of their rows (a lane holds D / 32
-// columns).  Bound by L2 reads of the partials, 4 D bytes per row and piece.
+// A group of D / 4 threads per row of a split unit: the weights of its pieces
+// from their log-sum-exps, then the weighted sum of their rows, four columns per
+// thread.  Bound by the latency of its loads (a few L2 reads one behind the
+// other), so the rows get as many threads as there are and the first pieces'
+// rows are asked for before the weights are known.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int n_warps = gridDim.x * 8;
+  constexpr int kLanes = D / 4, kRows = 256 / kLanes;  // threads per row, rows per block
+  constexpr int kAhead = 4;
+  const int c = threadIdx.x % kLanes;
   wait_for_previous();
   const int n_rows = p.counts->n_splits * kChunkRows;
-  for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < n_rows; w += n_warps) {
+  for (int w = blockIdx.x * kRows + threadIdx.x / kLanes; w < n_rows; w += gridDim.x * kRows) {
     const ChunkSplit sp = p.splits[w / kChunkRows];
     const int row = w % kChunkRows;
     const int tok = fast_div(row, p.div_gp), i = sp.rt * p.rt_tokens + tok;
     if (tok >= p.rt_tokens || i >= chunk_qlen(p, sp.b)) continue;
-    const int h = sp.hg * p.gp + row - tok * p.gp;
-    float mx = -INFINITY;
-    for (int k = lane; k < sp.n; k += 32) mx = fmaxf(mx, p.part_lse[(int64_t)(sp.slot0 + k) * kChunkRows + row]);
+    const float* po = p.part_o + ((int64_t)sp.slot0 * kChunkRows + row) * D + 4 * c;
+    const float* pl = p.part_lse + (int64_t)sp.slot0 * kChunkRows + row;
+    float4 v[kAhead];
+    float ls[kAhead];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float acc[kPer], sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    if (mx != -INFINITY) {
-      const float* po = p.part_o + ((int64_t)sp.slot0 * kChunkRows + row) * D + lane * kPer;
-      const float* pl = p.part_lse + (int64_t)sp.slot0 * kChunkRows + row;
-#pragma unroll 4
-      for (int k = 0; k < sp.n; ++k) {
-        const float f = fast_exp2(pl[(int64_t)k * kChunkRows] - mx);
-        sum += f;
-        const float* src = po + (int64_t)k * kChunkRows * D;
-        if constexpr (kPer == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          acc[0] += f * v.x; acc[1] += f * v.y; acc[2] += f * v.z; acc[3] += f * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] += f * v.x; acc[1] += f * v.y;
-        }
-      }
+    for (int k = 0; k < kAhead; ++k) {
+      const bool have = k < sp.n;
+      v[k] = have ? *reinterpret_cast<const float4*>(po + (int64_t)k * kChunkRows * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+      ls[k] = have ? pl[k * kChunkRows] : -INFINITY;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t qrow = (p.cu_q ? p.cu_q[sp.b] : 0) + i, ob = p.cu_q ? 0 : sp.b;
-    uint16_t* o = p.o + ob * p.o_sb + qrow * p.o_ss + (int64_t)h * p.o_sh + lane * kPer;
+    float mx = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
+    for (int k = kAhead; k < sp.n; ++k) mx = fmaxf(mx, pl[k * kChunkRows]);
+    const float ref = mx == -INFINITY ? 0.f : mx;  // no piece has a key of the row: all weights 0
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float l, float4 x) {
+      const float f = fast_exp2(l - ref);
+      sum += f;
+      o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+    };
 #pragma unroll
-    for (int c = 0; c < kPer; c += 2) reinterpret_cast<uint32_t*>(o)[c / 2] = pack2<F16>(acc[c] * inv, acc[c + 1] * inv);
-    if (lane == 0)
+    for (int k = 0; k < kAhead; ++k) add(ls[k], v[k]);
+#pragma unroll 4
+    for (int k = kAhead; k < sp.n; ++k)
+      add(pl[k * kChunkRows], *reinterpret_cast<const float4*>(po + (int64_t)k * kChunkRows * D));
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int h = sp.hg * p.gp + row - tok * p.gp;
+    const int64_t qrow = (p.cu_q ? p.cu_q[sp.b] : 0) + i, ob = p.cu_q ? 0 : sp.b;
+    *reinterpret_cast<uint2*>(p.o + ob * p.o_sb + qrow * p.o_ss + (int64_t)h * p.o_sh + 4 * c) =
+        make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
+    if (c == 0)
       p.lse[ob * p.lse_sb + (int64_t)h * p.lse_sh + qrow * p.lse_ss] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
   }
 }
@@ -501,6 +503,15 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
     if (p.G % g == 0 && g * (kChunkRows / g) >= 112) p.gp = g;
   p.rt_tokens = kChunkRows / p.gp;
   p.n_hg = p.Hq / p.gp;
+  // few rows in every sequence: query tiles of at most 32 rows, and the kernel
+  // form that deals each key tile's keys to the tile's four quarters
+  p.narrow = Sq > 0 && Sq * p.gp <= 32;
+  if (p.narrow) p.rt_tokens = 32 / p.gp;
+  // d = 64: two CTAs per SM overlap their units' ends, which short units need;
+  // one CTA with two softmax warpgroups keeps the tensor cores fed better along
+  // long ones (two and one: 8 x 512 tokens, 12 heads, over 512 keys 24.0 and 26.6
+  // us, over 4096 keys 95 and 87; 64 single tokens over up to 1500 keys 44 and 48)
+  p.pair = d == 64 && Sk <= (p.narrow ? 2048 : 1024);
   p.div_gp = make_fastdiv((uint32_t)p.gp);
   p.div_hg = make_fastdiv((uint32_t)p.n_hg);
 
@@ -509,7 +520,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   if (cu_q) rtiles = std::min(rtiles, p.tot_q / p.rt_tokens + n_seq);
   if (rtiles * p.n_hg > (1 << 27)) return FA_ERR_INVALID_ARG;
   const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
-  const int64_t ctas = (int64_t)sm_count() * chunk_ctas_per_sm(p.d);
+  const int64_t ctas = (int64_t)sm_count() * (p.pair ? 2 : 1);
   // partials: at most two rounds of the grid, and no more than all tiles alone;
   // none where no sequence has more than 8 key tiles: cutting and joining such
   // units gains nothing for the launch it costs (one token over 700 keys, 6
@@ -551,8 +562,8 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
 
 template <int D, bool F16>
 cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  const int64_t warps = (int64_t)p.max_slots / 2 * kChunkRows;
-  const int blocks = (int)std::min<int64_t>((warps + 7) / 8, 152 * 4);
+  const int64_t rows = (int64_t)p.max_slots / 2 * kChunkRows;
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(rows / (1024 / D), 152 * 8));
   return launch_overlapped(chunk_join_kernel<D, F16>, blocks, 256, 0, overlap, st, p);
 }
 

@@ -47,6 +47,8 @@ struct ChunkParams {
   int64_t tot_q;
   int32_t Hq, G, gp, rt_tokens, n_hg;  // G = Hq / Hkv; n_hg = Hq / gp
   FastDiv div_gp, div_hg;
+  int32_t narrow;  // no unit has more than 32 rows
+  int32_t pair;    // d = 64: two CTAs with one softmax warpgroup each per SM
   int32_t d, f16;
   float scale, scale_log2, softcap, inv_softcap;
   const float* alibi;
@@ -72,7 +74,6 @@ struct ChunkParams {
 // (programmatic dependent launch; it waits for that one's results itself).
 cudaError_t launch_chunk_attn(const ChunkParams& p, bool overlap, cudaStream_t st);      // bf16
 cudaError_t launch_chunk_attn_f16(const ChunkParams& p, bool overlap, cudaStream_t st);  // fp16
-int chunk_ctas_per_sm(int d);
 
 #ifdef __CUDACC__
 // Launch with or without overlap of the preceding kernel's end.

@@ -18,6 +18,10 @@
 //    ones of V that the last 16-key MMA step still reads are zeroed (a page's
 //    unused rows may hold anything, and 0 times NaN is NaN), and the steps past
 //    them are not issued;
+//  - a narrow piece, of at most 32 rows (single tokens, a few speculated ones),
+//    would leave its exponentials to one warp of four: its rows stand in all
+//    four quarters of the tile, warp q takes keys 32 q .. 32 q + 31 of each
+//    key tile for them, and the quarters are joined by log-sum-exp at the end;
 //  - work comes as pieces from the planner's list (chunk.cu), taken in rounds of
 //    one per CTA, longest first; a piece of a split unit leaves its normalised
 //    rows and log-sum-exp in fp32 for the join.
@@ -60,14 +64,14 @@ namespace {
 // registers, of which the softmax warpgroups take 216 and the others keep 72;
 // with two, 512 threads launch at 128, split 72 / 184; d = 64 launches 256
 // threads at 128, split 40 / 216.
-template <int D, int NP_>
+template <int D, int NW_, int NP_>
 struct CCfg {
+  static constexpr int NW = NW_;  // softmax warpgroups
   static constexpr int NP = NP_;
-  static constexpr int NW = D == 64 ? 1 : 2;  // softmax warpgroups
   static constexpr int kThreads = 128 + 128 * NW + (NP > 1 ? 128 : 0);
-  static constexpr int kCtas = D == 64 ? 2 : 1;  // per SM
-  static constexpr int kLaunchRegs = (D == 64 || NP > 1) ? 128 : 168;
-  static constexpr int kIssueRegs = D == 64 ? 40 : 72;
+  static constexpr int kCtas = NW == 1 ? 2 : 1;  // per SM
+  static constexpr int kLaunchRegs = (NW == 1 || NP > 1) ? 128 : 168;
+  static constexpr int kIssueRegs = NW == 1 ? 40 : 72;
   static constexpr int kSoftmaxRegs = NP > 1 ? 184 : 216;
   static_assert(NP == 1 || (NP == 2 && NW == 2), "the role table has one or two warps per operand");
   static_assert((kThreads - 128 * NW) * kIssueRegs + 128 * NW * kSoftmaxRegs <= kThreads * kLaunchRegs,
@@ -79,8 +83,8 @@ struct CCfg {
   static constexpr uint32_t kPCol = NW == 2 ? 0 : 128;  // P of buffer b: kPCol + 128 b
   static constexpr uint32_t kOCol = NW == 2 ? 384 : 192;
   static constexpr int NQ = D == 128 ? 1 : 2;
-  static constexpr int NSK = D == 128 ? 3 : 2;
-  static constexpr int NSV = 2;
+  static constexpr int NSK = D == 128 ? 3 : 2 * NW;
+  static constexpr int NSV = D == 128 ? 2 : 2 * NW;
   static constexpr int kTileBytes = 128 * D * 2;
   // K/V tiles: D / 64 halves of 128 rows by 64 columns (128 bytes)
   static constexpr int kHalfStep = 16384;
@@ -90,7 +94,8 @@ struct CCfg {
   static constexpr int kAuxOff = kVOff + NSV * kTileBytes;  // barriers and flags
   static constexpr int kRefOff = kAuxOff + 512;             // row references [2][128]
   static constexpr int kSumOff = kRefOff + 2 * 128 * 4;     // row sums [2][2][128]
-  static constexpr int kStageOff = kSumOff + 2 * 2 * 128 * 4;   // output staging, 2 KB per softmax warp
+  static constexpr int kNarOff = kSumOff + 2 * 2 * 128 * 4;  // narrow pieces: LSE of the quarters' rows [2][4][32]
+  static constexpr int kStageOff = kNarOff + 2 * 4 * 32 * 4;   // output staging, 2 KB per softmax warp
   static constexpr int kSmem = kStageOff + 4 * NW * 2048 + 1024;
   static_assert(kSmem <= (kCtas == 1 ? 227 * 1024 : 113 * 1024), "shared memory budget");
   static_assert(kOCol + D <= kCols, "TMEM budget");
@@ -309,12 +314,12 @@ __device__ __forceinline__ void produce(const ChunkParams& p, const bool is_k, c
 }
 
 // GEN: soft-cap and / or ALiBi (the plain logits fold the scale into the exponent).
-template <int D, int NP, bool GEN, bool F16>
-__global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
+template <int D, int NW, int NP, bool NARROW, bool GEN, bool F16>
+__global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kCtas)
     chunk_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tmq,
                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-  using C = CCfg<D, NP>;
-  constexpr int NSK = C::NSK, NSV = C::NSV, NQ = C::NQ, NW = C::NW;
+  using C = CCfg<D, NW, NP>;
+  constexpr int NSK = C::NSK, NSV = C::NSV, NQ = C::NQ;
   constexpr uint32_t kPCol = C::kPCol, kOCol = C::kOCol;
   constexpr int NB = C::NB;
   extern __shared__ unsigned char smem_raw[];
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
   uint64_t* drained = o_full + 1;    // [2] all MMAs of an issuer done (teardown)
   uint64_t* sumx = drained + 2;      // [1] row sums of all warpgroups posted (128 NW arrivals)
   uint64_t* refb = sumx + 1;         // [2 tile parity] row references posted (128 arrivals)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(refb + 2);
+  uint64_t* narb = refb + 2;         // [2 warpgroups] steps of a narrow piece's merge (128 arrivals)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(narb + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (tid == 0) {
@@ -347,6 +353,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       tc::mbar_init(q_empty + k, 1);
       tc::mbar_init(drained + k, 1);
       tc::mbar_init(refb + k, 128);
+      tc::mbar_init(narb + k, 128);
     }
     for (int s = 0; s < NSK; ++s) {
       tc::mbar_init(k_full + s, NP);
@@ -404,9 +411,12 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
         const int q_row0 = p.cu_q ? p.cu_q[w.b] : 0;
         const int q_b = p.cu_q ? 0 : w.b;
         unsigned char* dst = smem + C::kQOff + qb * C::kTileBytes;
-        tc::mbar_arrive_expect_tx(q_full + qb, q_bytes);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_4d(dst + c * 16384, &tmq, q_full + qb, c * 64, w.hg * p.gp, q_row0 + w.rt * p.rt_tokens, q_b);
+        // narrow: the same rows in each quarter of the tile
+        constexpr int kCopies = NARROW ? 4 : 1;
+        tc::mbar_arrive_expect_tx(q_full + qb, kCopies * q_bytes);
+        for (int e = 0; e < kCopies * (D / 64); ++e)
+          tc::tma_load_4d(dst + (e / kCopies) * 16384 + (e % kCopies) * 4096, &tmq, q_full + qb, (e / kCopies) * 64,
+                          w.hg * p.gp, q_row0 + w.rt * p.rt_tokens, q_b);
       };
       bool ok = true;
       int g = 0, kk = 0;  // tiles and busy pieces so far
@@ -523,6 +533,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
     constexpr int kHalfD = D / NW;  // O columns each warpgroup stores
     bool ok = true;
     int g = 0, kk = 0;  // tiles and busy pieces so far
+    uint32_t nsteps = 0;  // steps of narrow pieces' merges so far
     // buffer of this warpgroup's next tile and the parity of its use; tiles come
     // NW apart whatever the pieces' lengths
     int sb = NW == 2 ? w : 0;
@@ -547,10 +558,10 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
         kt0 = un.kt0;
         count = un.count;
         const int q_len = chunk_qlen(p, un.b), kv_len = p.kv_len[un.b];
-        const int tok = fast_div(row, p.div_gp), i = un.rt * p.rt_tokens + tok;
+        const int rl = NARROW ? lane : row, tok = fast_div(rl, p.div_gp), i = un.rt * p.rt_tokens + tok;
         const bool exists = tok < p.rt_tokens && i < q_len;
         if (count == 0) {
-          if (w == 0 && exists) write_empty_row<D>(p, un.b, un.hg * p.gp + row - tok * p.gp, i);
+          if (w == 0 && exists && (!NARROW || wq == 0)) write_empty_row<D>(p, un.b, un.hg * p.gp + rl - tok * p.gp, i);
           continue;
         }
         chunk_row_keys(p, i, kv_len - q_len, kv_len, p.prefix ? p.prefix[un.b] : 0, jlo_r, jhi_r);
@@ -558,7 +569,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
         active = __any_sync(0xffffffffu, exists);
         if (GEN) {
           place = i + kv_len - q_len;
-          if (p.alibi && exists) alibi_l2 = __ldg(p.alibi + un.hg * p.gp + row - tok * p.gp) * kLog2e;
+          if (p.alibi && exists) alibi_l2 = __ldg(p.alibi + un.hg * p.gp + rl - tok * p.gp) * kLog2e;
         }
       }
       float m_ref = -INFINITY;  // reference after the last tile seen
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
         const uint32_t sa = lane_base + sb * 128, pa = lane_base + kPCol + sb * 128;
         uint32_t xa[32], xb[32];
         float mx = -INFINITY;
-        auto first_pass = [&](uint32_t (&x)[32], int c) {
+        auto first_pass = [&](uint32_t (&x)[32], int c, bool keep) {
           if constexpr (GEN) {
             // logits in log2 units: soft-cap or scale, then the distance penalty
             if (p.softcap > 0.f) {
@@ -626,7 +637,7 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = (unsigned)(e - clo) <= span ? x[e] : __float_as_uint(-INFINITY);
           }
-          if ((GEN || part) && c > 0) tc::tmem_st32(sa + c * 32, x);
+          if ((GEN || part) && keep) tc::tmem_st32(sa + c * 32, x);
           float m[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) m[k] = __uint_as_float(x[k]);
@@ -635,16 +646,23 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
             m[(e >> 1) & 3] = max3f(m[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           mx = max3f(mx, max3f(m[0], m[1], m[2]), m[3]);
         };
-        tc::tmem_ld32(sa + 96, xa);
-        tmem_loaded(xa);
-#pragma unroll 1
-        for (int c = 3; c > 0; c -= 2) {
-          tc::tmem_ld32(sa + (c - 1) * 32, xb);
-          first_pass(xa, c);
+        if constexpr (NARROW) {
+          // the warp's quarter of the tile's keys
+          tc::tmem_ld32(sa + wq * 32, xb);
           tmem_loaded(xb);
-          if (c > 1) tc::tmem_ld32(sa + (c - 2) * 32, xa);
-          first_pass(xb, c - 1);
-          if (c > 1) tmem_loaded(xa);
+          first_pass(xb, wq, false);
+        } else {
+          tc::tmem_ld32(sa + 96, xa);
+          tmem_loaded(xa);
+#pragma unroll 1
+          for (int c = 3; c > 0; c -= 2) {
+            tc::tmem_ld32(sa + (c - 1) * 32, xb);
+            first_pass(xa, c, true);
+            tmem_loaded(xb);
+            if (c > 1) tc::tmem_ld32(sa + (c - 2) * 32, xa);
+            first_pass(xb, c - 1, c > 1);
+            if (c > 1) tmem_loaded(xa);
+          }
         }
         if constexpr (!GEN) mx *= p.scale_log2;
         if (GEN || part) tc::tmem_wait_st();
@@ -700,14 +718,23 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
           }
           tc::tmem_st16(pa + c * 16, pk);
         };
+        if constexpr (NARROW) {
+          uint32_t zero[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) zero[e] = 0;
 #pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tc::tmem_ld32(sa + (c + 1) * 32, xa);
-          second_pass(xb, c);
-          tmem_loaded(xa);
-          if (c < 2) tc::tmem_ld32(sa + (c + 2) * 32, xb);
-          second_pass(xa, c + 1);
-          if (c < 2) tmem_loaded(xb);
+          for (int c = 1; c < 4; ++c) tc::tmem_st16(pa + ((wq + c) & 3) * 16, zero);
+          second_pass(xb, wq);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tc::tmem_ld32(sa + (c + 1) * 32, xa);
+            second_pass(xb, c);
+            tmem_loaded(xa);
+            if (c < 2) tc::tmem_ld32(sa + (c + 2) * 32, xb);
+            second_pass(xa, c + 1);
+            if (c < 2) tmem_loaded(xb);
+          }
         }
         acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
         l += acc[0].x + acc[0].y;
@@ -756,58 +783,123 @@ __global__ void __launch_bounds__(CCfg<D, NP>::kThreads, CCfg<D, NP>::kCtas)
       const float inv = empty ? 0.f : 1.f / lt;
       const float lse2 = empty ? -INFINITY : m_ref + __log2f(lt);
       const int q_len = chunk_qlen(p, un.b);
-      const int tok = fast_div(row, p.div_gp), i = un.rt * p.rt_tokens + tok;
-      const bool exists = tok < p.rt_tokens && i < q_len;
-      if (un.slot >= 0) {
-        if (exists) {
-          float* dst = p.part_o + ((int64_t)un.slot * kChunkRows + row) * D + w * kHalfD;
+      const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[un.b] : 0, ob = p.cu_q ? 0 : un.b;
+      if constexpr (NARROW) {
+        // The four quarters' rows, each over its quarter of every tile's keys, are
+        // joined by their log-sum-exp, 8 rows at a time through the
+        // warpgroup's staging memory.
+        float* so = reinterpret_cast<float*>(smem + C::kStageOff + w * 8192);  // [4 quarters][8 rows][kHalfD]
+        float* sl = reinterpret_cast<float*>(smem + C::kNarOff) + w * 128;     // [4 quarters][32 rows]
+        const int n_rows = min(p.rt_tokens, q_len - un.rt * p.rt_tokens) * p.gp;
+        const int wtid = 32 * wq + lane, c4 = 4 * (wtid % (kHalfD / 4)), rr = wtid / (kHalfD / 4);
+        auto step = [&] {
+          tc::mbar_arrive(narb + w);
+          const bool go = tc::mbar_wait(narb + w, nsteps & 1, abort_flag);
+          ++nsteps;
+          return go;
+        };
+        for (int r0 = 0; r0 < n_rows && ok; r0 += 8) {
+          if (!(ok = step())) break;  // the staging memory is free
+          if (r0 == 0) sl[wq * 32 + lane] = lse2;
+          if (lane >= r0 && lane < r0 + 8) {
+            float* dst = so + (wq * 8 + lane - r0) * kHalfD;
 #pragma unroll
-          for (int c = 0; c < kHalfD / 32; ++c)
+            for (int c = 0; c < kHalfD / 32; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + c * 32 + e) =
-                  make_float4(__uint_as_float(ro[c][e]) * inv, __uint_as_float(ro[c][e + 1]) * inv,
-                              __uint_as_float(ro[c][e + 2]) * inv, __uint_as_float(ro[c][e + 3]) * inv);
-          if (w == 0) p.part_lse[(int64_t)un.slot * kChunkRows + row] = lse2;
-        }
-      } else if (active) {
-        // through a warp-private staging tile: a thread packs its own row, then
-        // each store instruction writes 64 contiguous bytes of 8 rows
-        uint4* stg = reinterpret_cast<uint4*>(smem + C::kStageOff + (warp - 4) * 2048);  // [32 rows][4]
-        const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[un.b] : 0, ob = p.cu_q ? 0 : un.b;
-        uint16_t* obase = p.o + ob * p.o_sb + (int64_t)un.hg * p.gp * p.o_sh;
-        uint16_t* orow[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = 32 * wq + 8 * k + (lane >> 2), t = fast_div(rr, p.div_gp);
-          const int ti = un.rt * p.rt_tokens + t;
-          orow[k] = (t < p.rt_tokens && ti < q_len)
-                        ? obase + (qbase + ti) * p.o_ss + (int64_t)(rr - t * p.gp) * p.o_sh + w * kHalfD + 8 * (lane & 3)
-                        : nullptr;
-        }
-#pragma unroll
-        for (int c = 0; c < kHalfD / 32; ++c) {
-          const uint32_t* t = ro[c];
-#pragma unroll
-          for (int v4 = 0; v4 < 4; ++v4) {
-            uint4 o4;
-            o4.x = pack2<F16>(__uint_as_float(t[8 * v4 + 0]) * inv, __uint_as_float(t[8 * v4 + 1]) * inv);
-            o4.y = pack2<F16>(__uint_as_float(t[8 * v4 + 2]) * inv, __uint_as_float(t[8 * v4 + 3]) * inv);
-            o4.z = pack2<F16>(__uint_as_float(t[8 * v4 + 4]) * inv, __uint_as_float(t[8 * v4 + 5]) * inv);
-            o4.w = pack2<F16>(__uint_as_float(t[8 * v4 + 6]) * inv, __uint_as_float(t[8 * v4 + 7]) * inv);
-            stg[lane * 4 + (v4 ^ ((lane >> 1) & 3))] = o4;
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(dst + c * 32 + e) =
+                    make_float4(__uint_as_float(ro[c][e]) * inv, __uint_as_float(ro[c][e + 1]) * inv,
+                                __uint_as_float(ro[c][e + 2]) * inv, __uint_as_float(ro[c][e + 3]) * inv);
           }
-          __syncwarp();
+          if (!(ok = step())) break;
+          const int r1 = r0 + rr;
+          if (rr < 8 && r1 < n_rows) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = fmaxf(top, sl[q * 32 + r1]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (top != -INFINITY) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float f = fast_exp2(sl[q * 32 + r1] - top);
+                const float4 v = *reinterpret_cast<const float4*>(so + (q * 8 + rr) * kHalfD + c4);
+                sum += f;
+                o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+              }
+            }
+            const float f = sum > 0.f ? 1.f / sum : 0.f;
+            const float ls = sum > 0.f ? top + __log2f(sum) : -INFINITY;
+            o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+            if (un.slot >= 0) {
+              const int64_t at = (int64_t)un.slot * kChunkRows + r1;
+              *reinterpret_cast<float4*>(p.part_o + at * D + w * kHalfD + c4) = o;
+              if (w == 0 && c4 == 0) p.part_lse[at] = ls;
+            } else {
+              const int t1 = fast_div(r1, p.div_gp), h1 = un.hg * p.gp + r1 - t1 * p.gp;
+              const int64_t qrow = qbase + un.rt * p.rt_tokens + t1;
+              *reinterpret_cast<uint2*>(p.o + ob * p.o_sb + qrow * p.o_ss + (int64_t)h1 * p.o_sh + w * kHalfD + c4) =
+                  make_uint2(pack2<F16>(o.x, o.y), pack2<F16>(o.z, o.w));
+              if (w == 0 && c4 == 0) p.lse[ob * p.lse_sb + (int64_t)h1 * p.lse_sh + qrow * p.lse_ss] = ls * kLn2;
+            }
+          }
+        }
+        // (with two warpgroups the next piece's row-sum barrier keeps its staging
+        // after these reads)
+        if (NW == 1 && ok) ok = step();
+        if (!ok) break;
+      } else {
+        const int tok = fast_div(row, p.div_gp), i = un.rt * p.rt_tokens + tok;
+        const bool exists = tok < p.rt_tokens && i < q_len;
+        if (un.slot >= 0) {
+          if (exists) {
+            float* dst = p.part_o + ((int64_t)un.slot * kChunkRows + row) * D + w * kHalfD;
+#pragma unroll
+            for (int c = 0; c < kHalfD / 32; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(dst + c * 32 + e) =
+                    make_float4(__uint_as_float(ro[c][e]) * inv, __uint_as_float(ro[c][e + 1]) * inv,
+                                __uint_as_float(ro[c][e + 2]) * inv, __uint_as_float(ro[c][e + 3]) * inv);
+            if (w == 0) p.part_lse[(int64_t)un.slot * kChunkRows + row] = lse2;
+          }
+        } else if (active) {
+          // through a warp-private staging tile: a thread packs its own row, then
+          // each store instruction writes 64 contiguous bytes of 8 rows
+          uint4* stg = reinterpret_cast<uint4*>(smem + C::kStageOff + (warp - 4) * 2048);  // [32 rows][4]
+          uint16_t* obase = p.o + ob * p.o_sb + (int64_t)un.hg * p.gp * p.o_sh;
+          uint16_t* orow[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int rr = 8 * k + (lane >> 2), q = lane & 3;
-            const uint4 o4 = stg[rr * 4 + (q ^ ((rr >> 1) & 3))];
-            if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + c * 32) = o4;
+            const int rr = 32 * wq + 8 * k + (lane >> 2), t = fast_div(rr, p.div_gp);
+            const int ti = un.rt * p.rt_tokens + t;
+            orow[k] = (t < p.rt_tokens && ti < q_len)
+                          ? obase + (qbase + ti) * p.o_ss + (int64_t)(rr - t * p.gp) * p.o_sh + w * kHalfD + 8 * (lane & 3)
+                          : nullptr;
           }
-          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kHalfD / 32; ++c) {
+            const uint32_t* t = ro[c];
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+              uint4 o4;
+              o4.x = pack2<F16>(__uint_as_float(t[8 * v4 + 0]) * inv, __uint_as_float(t[8 * v4 + 1]) * inv);
+              o4.y = pack2<F16>(__uint_as_float(t[8 * v4 + 2]) * inv, __uint_as_float(t[8 * v4 + 3]) * inv);
+              o4.z = pack2<F16>(__uint_as_float(t[8 * v4 + 4]) * inv, __uint_as_float(t[8 * v4 + 5]) * inv);
+              o4.w = pack2<F16>(__uint_as_float(t[8 * v4 + 6]) * inv, __uint_as_float(t[8 * v4 + 7]) * inv);
+              stg[lane * 4 + (v4 ^ ((lane >> 1) & 3))] = o4;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int rr = 8 * k + (lane >> 2), q = lane & 3;
+              const uint4 o4 = stg[rr * 4 + (q ^ ((rr >> 1) & 3))];
+              if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + c * 32) = o4;
+            }
+            __syncwarp();
+          }
+          if (w == 0 && exists)
+            p.lse[ob * p.lse_sb + (int64_t)(un.hg * p.gp + row - tok * p.gp) * p.lse_sh + (qbase + i) * p.lse_ss] = lse2 * kLn2;
         }
-        if (w == 0 && exists)
-          p.lse[ob * p.lse_sb + (int64_t)(un.hg * p.gp + row - tok * p.gp) * p.lse_sh + (qbase + i) * p.lse_ss] = lse2 * kLn2;
       }
       ++kk;
     }
@@ -842,9 +934,9 @@ bool encode_map(CUtensorMap* m, const void* base, int d, int heads, int64_t rows
   return r == CUDA_SUCCESS;
 }
 
-template <int D, int NP, bool GEN, bool F16>
+template <int D, int NW, int NP, bool NARROW, bool GEN, bool F16>
 cudaError_t launch_v(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  using C = CCfg<D, NP>;
+  using C = CCfg<D, NW, NP>;
   // setmaxnreg.inc would wait forever if the block were launched with fewer
   // registers than the split assumes: launch only when the build matches.
   static std::atomic<int> launch_regs{-1};
@@ -852,12 +944,12 @@ cudaError_t launch_v(const ChunkParams& p, bool overlap, cudaStream_t st) {
   cudaError_t e;
   if (regs < 0) {
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, chunk_kernel<D, NP, GEN, F16>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, chunk_kernel<D, NW, NP, NARROW, GEN, F16>)) != cudaSuccess) return e;
     regs = fa.numRegs;
     launch_regs.store(regs, std::memory_order_relaxed);
   }
   if (regs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  if ((e = ensure_smem_attr<chunk_kernel<D, NP, GEN, F16>>(C::kSmem)) != cudaSuccess) return e;
+  if ((e = ensure_smem_attr<chunk_kernel<D, NW, NP, NARROW, GEN, F16>>(C::kSmem)) != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   const bool packed = p.cu_q != nullptr;
   const int heads_kv = p.Hq / p.G;
@@ -866,17 +958,25 @@ cudaError_t launch_v(const ChunkParams& p, bool overlap, cudaStream_t st) {
       !encode_map(&mk, p.k, D, heads_kv, p.cache_rows, p.cache_outer, p.k_sh, p.k_ss, p.k_sb, 1, p.box_rows, F16) ||
       !encode_map(&mv, p.v, D, heads_kv, p.cache_rows, p.cache_outer, p.v_sh, p.v_ss, p.v_sb, 1, p.box_rows, F16))
     return cudaErrorInvalidValue;
-  return launch_overlapped(chunk_kernel<D, NP, GEN, F16>, (unsigned)p.grid, C::kThreads, C::kSmem, overlap, st, p, mq, mk, mv);
+  return launch_overlapped(chunk_kernel<D, NW, NP, NARROW, GEN, F16>, (unsigned)p.grid, C::kThreads, C::kSmem, overlap, st, p, mq, mk, mv);
 }
 
+template <int D, int NW, int NP, bool NARROW, bool F16>
+cudaError_t launch_g(const ChunkParams& p, bool overlap, cudaStream_t st) {
+  return (p.softcap > 0.f || p.alibi) ? launch_v<D, NW, NP, NARROW, true, F16>(p, overlap, st)
+                                      : launch_v<D, NW, NP, NARROW, false, F16>(p, overlap, st);
+}
+
+// (CCfg, ChunkParams::narrow and ::pair say which form is for what)
 template <bool F16>
 cudaError_t launch_t(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  const bool gen = p.softcap > 0.f || p.alibi;
-  if (p.d == 64)
-    return gen ? launch_v<64, 1, true, F16>(p, overlap, st) : launch_v<64, 1, false, F16>(p, overlap, st);
-  if (p.box_rows <= 16 && (int64_t)p.Sq * p.gp > 32)  // (CCfg)
-    return gen ? launch_v<128, 2, true, F16>(p, overlap, st) : launch_v<128, 2, false, F16>(p, overlap, st);
-  return gen ? launch_v<128, 1, true, F16>(p, overlap, st) : launch_v<128, 1, false, F16>(p, overlap, st);
+  if (p.d == 64) {
+    if (p.narrow) return p.pair ? launch_g<64, 1, 1, true, F16>(p, overlap, st) : launch_g<64, 2, 1, true, F16>(p, overlap, st);
+    return p.pair ? launch_g<64, 1, 1, false, F16>(p, overlap, st) : launch_g<64, 2, 1, false, F16>(p, overlap, st);
+  }
+  if (p.narrow) return launch_g<128, 2, 1, true, F16>(p, overlap, st);
+  return p.box_rows <= 16 ? launch_g<128, 2, 2, false, F16>(p, overlap, st)
+                          : launch_g<128, 2, 1, false, F16>(p, overlap, st);
 }
 
 }  // namespace
@@ -884,7 +984,6 @@ cudaError_t launch_t(const ChunkParams& p, bool overlap, cudaStream_t st) {
 // The fp16 instantiations build in their own translation unit (chunk_f16.cu
 // includes this file with MFA_CHUNK_F16_UNIT defined), in parallel.
 #ifndef MFA_CHUNK_F16_UNIT
-int chunk_ctas_per_sm(int d) { return d == 64 ? CCfg<64, 1>::kCtas : CCfg<128, 1>::kCtas; }
 cudaError_t launch_chunk_attn(const ChunkParams& p, bool overlap, cudaStream_t st) { return launch_t<false>(p, overlap, st); }
 #else
 cudaError_t launch_chunk_attn_f16(const ChunkParams& p, bool overlap, cudaStream_t st) {

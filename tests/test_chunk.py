@@ -60,8 +60,8 @@ def plan(q=None, kc=None, vc=None, lens=None, **kw):
 def test_plan_geometry():
     rc, p = plan()
     assert rc == 0 and p["path"] == _lib.FA_PATH_PREFILL
-    # 4 q-heads share a K/V head: 32 tokens x 4 heads per query tile, 2 head groups
-    assert p["rows_per_tile"] == 32 and p["n_heads_sched"] == 2 and p["n_row_tiles"] == 1 and p["n_k_tiles"] == 1
+    # 4 q-heads share a K/V head, 2 head groups; 5 tokens x 4 heads: a query tile of 32 rows
+    assert p["rows_per_tile"] == 8 and p["n_heads_sched"] == 2 and p["n_row_tiles"] == 1 and p["n_k_tiles"] == 1
     assert p["n_items"] == 2 * 2 and p["n_kernels"] == 2 and p["n_splits"] == 0  # one key tile: nothing to split
     rc, p = plan(block_table=i32(2, 500), max_seqlen_k=8000)
     assert rc == 0 and p["n_k_tiles"] == 63 and p["n_kernels"] == 3 and p["n_splits"] == 4 * 63
@@ -78,7 +78,7 @@ def test_plan_geometry():
 @pytest.mark.parametrize("hq,hkv,gp", [(1, 1, 1), (8, 8, 1), (32, 8, 4), (5, 1, 5), (12, 2, 6), (40, 1, 40), (48, 1, 24),
                                        (128, 1, 128), (256, 1, 128), (33, 1, 11), (11, 1, 11), (62, 2, 31)])
 def test_plan_heads_per_tile(hq, hkv, gp):
-    rc, p = plan(T(7, hq, 64), T(10, 16, hkv, 64))
+    rc, p = plan(T(7, hq, 64), T(10, 16, hkv, 64), max_seqlen_q=40)
     assert rc == 0 and p["n_heads_sched"] == hq // gp and p["rows_per_tile"] == 128 // gp, (p["n_heads_sched"], p["rows_per_tile"])
 
 

@@ -343,3 +343,21 @@ def test_capture_streams_and_changed_lengths():
                              max_seqlen_k=4000, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 1), (8, 1), (5, 1), (32, 1), (12, 4)])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, H)])
+def test_few_rows(hq, hkv, d, dtype):
+    """Units of at most 32 (token, head) rows, whose keys are dealt to the four
+    quarters of a tile, beside larger ones: each number of 8-row steps, quarters
+    without a key, whole and split, every kind of logit."""
+    q_lens, kv = [1, 2, 3, 5, 8, 9, 1, 4, 40], [1, 33, 129, 700, 1000, 2000, 5000, 31, 300]
+    slopes = torch.tensor([2.0 ** -(1 + h % 8) for h in range(hq)])
+    c = case(200 + hq, q_lens, kv, hq=hq, hkv=hkv, d=d, dtype=dtype, page=16)
+    check(c, "plain")
+    check(c, "window", window_left=20)
+    check(c, "gen", logits=2.0, window_left=600, softcap=20.0)
+    pre = torch.tensor([1, 20, 0, 699, 0, 1999, 100, 31, 200], dtype=torch.int32)
+    check(c, "prefix", prefix_lens=pre)
+    out, lse, _ = run(c, alibi_slopes=slopes)
+    assert_close(out, lse, oracle(c, alibi_slopes=slopes), "alibi", logits=2.0, n_keys=5000)
