@@ -13,7 +13,12 @@
 // element), 3 flop each; the angles are made once per (token, pair) in shared
 // memory and serve all heads of the token.  A thread takes 16 elements of one
 // head (two 16-byte loads) of one token, keeps the 8 (cos, sin) of its columns
-// in registers and walks the token's heads, four of them in flight.
+// in registers and walks the token's heads, two of them in flight; four CTAs per
+// SM hide each other's starts (three with four heads in flight were 4 % slower,
+// six spill).  Measured (copy rate 6792 GB/s): q and k of 8192 tokens, 32 / 8
+// heads, d = 128: 29.3 us, 0.84 of the copy rate; of 65536 tokens 195 us, 1.01;
+// 16384 tokens appended with q: 66.6 us, 0.89; one token 3.2 us.  Pairs whose
+// columns no 16-byte load holds (kHalfOdd) run at 0.45.
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -30,7 +35,8 @@ using namespace mfa;
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens per CTA
+constexpr int kRopeBlocks = 4;  // CTAs per SM
+constexpr int kMaxTokens = 8;   // tokens per CTA
 
 // One of q, k, v: rows of `heads` heads, read at in + b * in_sb + i * in_ss,
 // written at out + b * out_sb + i * out_ss (the cache's page and row strides
@@ -133,7 +139,7 @@ __device__ __forceinline__ float to_float(uint16_t u) {
 enum { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
 
 template <int D, bool F16, int LAYOUT, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 16;  // threads per head
   __shared__ float2 cs[kMaxTokens * D / 2];
   __shared__ int s_pos[kMaxTokens], s_b[kMaxTokens], s_i[kMaxTokens];
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const unsigned group = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
 
   const int step = per * gridDim.y;
-  constexpr int U = LAYOUT == kHalfOdd ? 1 : 4;  // heads in flight
+  constexpr int U = LAYOUT == kHalfOdd ? 1 : 2;  // heads in flight
   for (int h0 = blockIdx.y * per + slot % per; h0 < p.heads; h0 += U * step) {
     uint4 va[U], vb[U];
     uint16_t* dst[U];
@@ -358,12 +364,12 @@ int launch_rope(RopeParams& p, int d, bool f16, bool interleaved, const fa_opts*
   cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
   cudaError_t e = cudaSuccess;
   if (opts->event_begin) e = cudaEventRecord(static_cast<cudaEvent_t>(opts->event_begin), st);
-  // Few tokens: one per CTA and the heads over the grid's second dimension, so
-  // that a thread has one head; many: eight per CTA, whose angles cost an
-  // eighth of the frequency work and whose threads keep four heads in flight.
+  // Tokens per CTA: the fewest that one wave of CTAs takes, at most eight.  With
+  // one, the heads go over the grid's second dimension too, so that a thread has
+  // one head (1050 tokens in two waves of one each took 9.1 us, in one of four 4.7).
   const int slots = kRopeThreads / (d / 16);
   p.tb = 1;
-  while (p.tb < kMaxTokens && p.rows / (2 * p.tb) >= 4 * 152) p.tb *= 2;
+  while (p.tb < kMaxTokens && p.rows > (int64_t)152 * kRopeBlocks * p.tb) p.tb *= 2;
   const int64_t blocks = (p.rows + p.tb - 1) / p.tb;
   int ysplit = 1;
   if (p.tb == 1) {
