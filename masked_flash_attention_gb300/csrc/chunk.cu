@@ -39,27 +39,6 @@ constexpr int kTailFlag = 1 << 30;                // in a row tile's second word
 constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 4.f;
 constexpr int kMaxTailCut = 8;
 
-__device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
-  if (atomicCAS(&p.ws->error, 0u, code) == 0u) atomicExch(&p.ws->error_info, info);
-}
-
-// Key tiles that some row of row tile rt of a sequence sees: kt0 .. kt0 + count - 1.
-__device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int4 seq, int rt, int& kt0, int& count) {
-  const int q_len = seq.y, kv = seq.z, pre = seq.w, off = kv - q_len;
-  const int i0 = rt * p.rt_tokens, i1 = min(i0 + p.rt_tokens, q_len) - 1;
-  int lo0, hi0, lo1, hi1;  // both ends move right with the row
-  chunk_row_keys(p, i0, off, kv, pre, lo0, hi0);
-  chunk_row_keys(p, i1, off, kv, pre, lo1, hi1);
-  kt0 = count = 0;
-  if (p.debug_flags & FA_DEBUG_NO_SKIP) {
-    count = (kv + kKeysPerTile - 1) / kKeysPerTile;
-    return;
-  }
-  if (lo0 > hi1) return;
-  kt0 = lo0 / kKeysPerTile;
-  count = hi1 / kKeysPerTile - kt0 + 1;
-}
-
 // Block-wide exclusive prefix sum; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -112,16 +91,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     int nt = 0;
     int4 q = make_int4(0, 0, 0, 0);
     if (s < p.n_seq) {
-      const int64_t c0 = p.cu_q ? p.cu_q[s] : 0, c1 = p.cu_q ? p.cu_q[s + 1] : p.Sq;
-      const int64_t q_len = c1 - c0;
-      q.z = p.kv_len[s];
-      q.w = p.prefix ? p.prefix[s] : 0;
-      if (c0 < 0 || q_len < 0 || q_len > p.Sq || (p.cu_q && c1 > p.tot_q) || q.z < 0 || q.z > p.Sk || q.w < 0) {
-        chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)s);
-      } else {
-        q.y = (int)q_len;
-        nt = (q.y + p.rt_tokens - 1) / p.rt_tokens;
-      }
+      if (chunk_seq(p, s, q)) nt = (q.y + p.rt_tokens - 1) / p.rt_tokens;
+      else chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)s);
     }
     int total;
     q.x = R + block_scan(nt, s_warp, total);
@@ -530,6 +501,14 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   p.max_rtiles = (int32_t)rtiles;
   p.max_slots = (int32_t)slots;
   p.grid = (int32_t)std::min<int64_t>(ctas, std::max<int64_t>(1, pieces));
+  // Few short units: no planner, each CTA works out its own piece, one per row
+  // tile that a sequence may have and head group (one token that sees 60 keys: 7.2
+  // us in a graph, with the planner 10.8).  More units than CTAs are left to
+  // the planner's order: 8 x 1024 tokens of 12 heads, 768 units of 1 to 8 tiles,
+  // took 42 us in turn, 34 us longest first.
+  const int64_t all = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens) * p.n_hg;
+  p.direct = slots == 0 && all <= ctas ? (int32_t)all : 0;
+  if (p.direct) p.grid = p.direct;
   size_t off = kWsHeadBytes;
   unsigned char* base = static_cast<unsigned char*>(opts->workspace);
   auto take = [&](size_t bytes) {
@@ -555,7 +534,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   pub->n_k_tiles = (int32_t)n_kt;
   pub->n_splits = p.max_slots;
   pub->n_items = units;
-  pub->n_kernels = units > 0 ? 2 + (slots > 0) : 0;
+  pub->n_kernels = units > 0 ? 1 + (p.direct == 0) + (slots > 0) : 0;
   pub->workspace_bytes = off;
   return FA_OK;
 }
@@ -596,12 +575,12 @@ int fa_fwd_chunk(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* 
   const bool any = pub.n_items > 0;
   // (events between the kernels would be recorded late if these overlapped)
   const bool overlap = !opts->event_begin && !opts->event_attn_end;
-  if (any) {
+  if (any && !p.direct) {
     chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
     e = cudaGetLastError();
   }
   record(opts->event_begin);
-  if (any && e == cudaSuccess) e = p.f16 ? launch_chunk_attn_f16(p, overlap, st) : launch_chunk_attn(p, overlap, st);
+  if (any && e == cudaSuccess) e = p.f16 ? launch_chunk_attn_f16(p, overlap && !p.direct, st) : launch_chunk_attn(p, overlap && !p.direct, st);
   record(opts->event_attn_end);
   if (any && e == cudaSuccess && p.max_slots > 0) {
     if (p.d == 64) e = p.f16 ? launch_join<64, true>(p, overlap, st) : launch_join<64, false>(p, overlap, st);

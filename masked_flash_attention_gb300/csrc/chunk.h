@@ -64,6 +64,7 @@ struct ChunkParams {
   float* part_o;      // [max_slots][128][d]
   float* part_lse;    // [max_slots][128] log2 units
   int32_t max_rtiles, max_slots, grid;
+  int32_t direct;  // > 0: this many pieces, one per CTA, which works it out itself (no planner)
   // layouts for the tensor maps (element strides)
   const uint16_t *q, *k, *v;
   int64_t q_sb, q_ss, q_sh, k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;
@@ -113,6 +114,38 @@ __device__ __forceinline__ void chunk_row_keys(const ChunkParams& p, int i, int 
   if (p.causal) hi = min(hi, max(i + off, prefix - 1));
   if (p.wl >= 0) lo = max(lo, i + off - p.wl);
   if (p.wr >= 0) hi = min(hi, i + off + p.wr);
+}
+
+__device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
+  if (atomicCAS(&p.ws->error, 0u, code) == 0u) atomicExch(&p.ws->error_info, info);
+}
+
+// Sequence s's lengths {-, q_len, kv_len, prefix}; false when they do not fit
+// the sizes the host planned for (nothing indexes with them then).
+__device__ __forceinline__ bool chunk_seq(const ChunkParams& p, int s, int4& q) {
+  const int64_t c0 = p.cu_q ? p.cu_q[s] : 0, c1 = p.cu_q ? p.cu_q[s + 1] : p.Sq, q_len = c1 - c0;
+  q.z = p.kv_len[s];
+  q.w = p.prefix ? p.prefix[s] : 0;
+  if (c0 < 0 || q_len < 0 || q_len > p.Sq || (p.cu_q && c1 > p.tot_q) || q.z < 0 || q.z > p.Sk || q.w < 0) return false;
+  q.y = (int)q_len;
+  return true;
+}
+
+// Key tiles that some row of row tile rt of a sequence sees: kt0 .. kt0 + count - 1.
+__device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int4 seq, int rt, int& kt0, int& count) {
+  const int q_len = seq.y, kv = seq.z, pre = seq.w, off = kv - q_len;
+  const int i0 = rt * p.rt_tokens, i1 = min(i0 + p.rt_tokens, q_len) - 1;
+  int lo0, hi0, lo1, hi1;  // both ends move right with the row
+  chunk_row_keys(p, i0, off, kv, pre, lo0, hi0);
+  chunk_row_keys(p, i1, off, kv, pre, lo1, hi1);
+  kt0 = count = 0;
+  if (p.debug_flags & FA_DEBUG_NO_SKIP) {
+    count = (kv + kKeysPerTile - 1) / kKeysPerTile;
+    return;
+  }
+  if (lo0 > hi1) return;
+  kt0 = lo0 / kKeysPerTile;
+  count = hi1 / kKeysPerTile - kt0 + 1;
 }
 #endif
 

@@ -95,7 +95,8 @@ struct CCfg {
   static constexpr int kRefOff = kAuxOff + 512;             // row references [2][128]
   static constexpr int kSumOff = kRefOff + 2 * 128 * 4;     // row sums [2][2][128]
   static constexpr int kNarOff = kSumOff + 2 * 2 * 128 * 4;  // narrow pieces: LSE of the quarters' rows [2][4][32]
-  static constexpr int kStageOff = kNarOff + 2 * 4 * 32 * 4;   // output staging, 2 KB per softmax warp
+  static constexpr int kOwnOff = kNarOff + 2 * 4 * 32 * 4;  // the piece of a CTA that works out its own
+  static constexpr int kStageOff = kOwnOff + 32;   // output staging, 2 KB per softmax warp
   static constexpr int kSmem = kStageOff + 4 * NW * 2048 + 1024;
   static_assert(kSmem <= (kCtas == 1 ? 227 * 1024 : 113 * 1024), "shared memory budget");
   static_assert(kOCol + D <= kCols, "TMEM budget");
@@ -149,9 +150,6 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-__device__ __forceinline__ void chunk_error(const ChunkParams& p, uint32_t code, uint32_t info) {
-  if (atomicCAS(&p.ws->error, 0u, code) == 0u) atomicExch(&p.ws->error_info, info);
-}
 __device__ __forceinline__ void fail(const ChunkParams& p, volatile int* abort_flag, uint32_t where) {
   if (!*abort_flag) {
     *abort_flag = 1;
@@ -165,15 +163,26 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
-// The piece this CTA takes in round r: rounds of one piece per CTA, every other
-// one in reverse CTA order, so that the CTA with a round's longest piece gets
-// the next one's shortest.  At or past n: none, nor in any later round.
-__device__ __forceinline__ int round_piece(int r) {
+// The dynamic shared memory, from its first 1024-byte boundary.
+__device__ __forceinline__ unsigned char* smem_base() {
+  extern __shared__ unsigned char smem_raw[];
+  return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+
+// The index of the piece this CTA takes in round r (at or past n_pieces: none,
+// nor in any later round).  From the planner's list it takes one per round of
+// the grid, every other round in reverse CTA order, so that the CTA with a
+// round's longest piece gets the next one's shortest; without a planner its
+// one piece stands in its shared memory.
+__device__ __forceinline__ int round_piece(const ChunkParams& p, int r) {
+  if (p.direct) return r;
   const int c = (r & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
   return r * (int)gridDim.x + c;
 }
+template <class C>
 __device__ __forceinline__ ChunkPiece piece_at(const ChunkParams& p, int i) {
-  const int4* src = reinterpret_cast<const int4*>(p.pieces + i);
+  const int4* src = p.direct ? reinterpret_cast<const int4*>(smem_base() + C::kOwnOff) + 2 * i
+                             : reinterpret_cast<const int4*>(p.pieces + i);
   const int4 a = src[0], b = src[1];
   ChunkPiece w;
   w.b = a.x; w.rt = a.y; w.hg = a.z; w.kt0 = a.w;
@@ -181,13 +190,35 @@ __device__ __forceinline__ ChunkPiece piece_at(const ChunkParams& p, int i) {
   return w;
 }
 // Next round at or after r whose piece has key tiles, or -1.
-__device__ __forceinline__ int next_busy(const ChunkParams& p, int n, int r, ChunkPiece& w) {
+template <class C>
+__device__ __forceinline__ int next_busy(const ChunkParams& p, int n_pieces, int r, ChunkPiece& w) {
   for (;; ++r) {
-    const int i = round_piece(r);
-    if (i >= n) return -1;
-    w = piece_at(p, i);
+    const int i = round_piece(p, r);
+    if (i >= n_pieces) return -1;
+    w = piece_at<C>(p, i);
     if (w.count > 0) return r;
   }
+}
+
+// No planner: piece i of sequence i / (tiles * heads), row tile, head group
+// (count -1: the sequence has no such tile), and the check of its lengths.
+__device__ __forceinline__ ChunkPiece direct_piece(const ChunkParams& p, int i) {
+  const int n_rt = (p.Sq + p.rt_tokens - 1) / p.rt_tokens;
+  ChunkPiece w;
+  w.hg = i % p.n_hg;
+  w.rt = i / p.n_hg % n_rt;
+  w.b = i / p.n_hg / n_rt;
+  w.kt0 = 0;
+  w.count = -1;
+  w.slot = -1;
+  w.pad[0] = w.pad[1] = 0;
+  int4 q = make_int4(0, 0, 0, 0);
+  if (!chunk_seq(p, w.b, q)) {
+    if (w.rt == 0 && w.hg == 0) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)w.b);
+  } else if (w.rt * p.rt_tokens < q.y) {
+    row_tile_keys(p, q, w.rt, w.kt0, w.count);
+  }
+  return w;
 }
 
 // Output of a row that keeps no key of its sequence.
@@ -206,7 +237,7 @@ __device__ __forceinline__ void write_empty_row(const ChunkParams& p, int b, int
 // arrives on its full barrier (NP arrivals) with the bytes it sends.  Written for
 // few registers, and one copy of the code for both operands: with two, the
 // softmax loop beside them ran a fifth slower.
-template <int D, int NP>
+template <class C, int D, int NP>
 __device__ __forceinline__ void produce(const ChunkParams& p, const bool is_k, const int n_stages,
                                         const CUtensorMap* map, int n_pieces, int part, int lane, uint64_t* full,
                                         uint64_t* empty, uint64_t* v_tail, unsigned char* ring,
@@ -220,7 +251,7 @@ __device__ __forceinline__ void produce(const ChunkParams& p, const bool is_k, c
   // test only: the first key tile is never sent (FA_DEBUG_WITHHOLD)
   bool withhold = is_k && (p.debug_flags & FA_DEBUG_WITHHOLD);
   ChunkPiece w;
-  for (int r = next_busy(p, n_pieces, 0, w); ok && r >= 0; r = next_busy(p, n_pieces, r + 1, w)) {
+  for (int r = next_busy<C>(p, n_pieces, 0, w); ok && r >= 0; r = next_busy<C>(p, n_pieces, r + 1, w)) {
     const int head = w.hg * p.gp / p.G;
     const int32_t* table = p.block_table ? p.block_table + (int64_t)w.b * p.bt_stride : nullptr;
     const int seq = w.b;
@@ -322,9 +353,7 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
   constexpr int NSK = C::NSK, NSV = C::NSV, NQ = C::NQ;
   constexpr uint32_t kPCol = C::kPCol, kOCol = C::kOCol;
   constexpr int NB = C::NB;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* smem = smem_base();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kAuxOff);
@@ -379,12 +408,13 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
     tc::tmem_alloc(tmem_slot, C::kCols);
     tc::tmem_relinquish();
   }
+  if (p.direct && tid == 128) *reinterpret_cast<ChunkPiece*>(smem + C::kOwnOff) = direct_piece(p, blockIdx.x);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = *tmem_slot;
   wait_for_previous();
-  const int n_pieces = p.counts->n_pieces;
+  const int n_pieces = p.direct ? 1 : p.counts->n_pieces;  // of the grid, or (no planner) of this CTA
 
   if (warp < 4 || warp >= 4 + 4 * NW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
   if (warp == 0 || warp == 2 || (NP == 2 && (warp == 12 || warp == 13))) {
@@ -392,7 +422,7 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
     // K: warp 0 (and 12), V: warp 2 (and 13)
     const int part = warp < 4 ? 0 : 1;
     const bool is_k = warp == 0 || warp == 12;
-    produce<D, NP>(p, is_k, is_k ? NSK : NSV, is_k ? &tmk : &tmv, n_pieces, part, lane, is_k ? k_full : v_full,
+    produce<C, D, NP>(p, is_k, is_k ? NSK : NSV, is_k ? &tmk : &tmv, n_pieces, part, lane, is_k ? k_full : v_full,
                    is_k ? k_empty : v_empty, v_tail, smem + (is_k ? C::kKOff : C::kVOff), abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issuer
@@ -421,11 +451,11 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
       bool ok = true;
       int g = 0, kk = 0;  // tiles and busy pieces so far
       ChunkPiece w, wn;
-      int u = next_busy(p, n_pieces, 0, w);
+      int u = next_busy<C>(p, n_pieces, 0, w);
       if (u >= 0) load_q(w, 0);
       for (; ok && u >= 0; ++kk) {
         const int qb = kk % NQ;
-        const int un = next_busy(p, n_pieces, u + 1, wn);
+        const int un = next_busy<C>(p, n_pieces, u + 1, wn);
         if (!tc::mbar_wait(q_full + qb, (kk / NQ) & 1, abort_flag)) { ok = false; break; }
         for (int i = 0; i < w.count; ++i, ++g) {
           const int s = g % NSK, sb = g % NB;
@@ -486,7 +516,7 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
       bool ok = true;
       int g = 0;
       ChunkPiece w;
-      for (int r = next_busy(p, n_pieces, 0, w); ok && r >= 0; r = next_busy(p, n_pieces, r + 1, w)) {
+      for (int r = next_busy<C>(p, n_pieces, 0, w); ok && r >= 0; r = next_busy<C>(p, n_pieces, r + 1, w)) {
         const int kv = p.kv_len[w.b];
         for (int i = 0; i < w.count; ++i, ++g) {
           const int s = g % NSV, pb = g % NB;
@@ -546,7 +576,7 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
       }
     };
     for (int r = 0; ok; ++r) {
-      const int pi = round_piece(r);
+      const int pi = round_piece(p, r);
       if (pi >= n_pieces) break;
       // what the tile loop keeps live is little: the piece's tiles, this row's
       // keys, and (GEN) its place and slope; the rest is read again after it
@@ -554,14 +584,14 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
       float alibi_l2 = 0.f;
       bool active;
       {
-        const ChunkPiece un = piece_at(p, pi);
+        const ChunkPiece un = piece_at<C>(p, pi);
         kt0 = un.kt0;
         count = un.count;
         const int q_len = chunk_qlen(p, un.b), kv_len = p.kv_len[un.b];
         const int rl = NARROW ? lane : row, tok = fast_div(rl, p.div_gp), i = un.rt * p.rt_tokens + tok;
         const bool exists = tok < p.rt_tokens && i < q_len;
-        if (count == 0) {
-          if (w == 0 && exists && (!NARROW || wq == 0)) write_empty_row<D>(p, un.b, un.hg * p.gp + rl - tok * p.gp, i);
+        if (count <= 0) {
+          if (count == 0 && w == 0 && exists && (!NARROW || wq == 0)) write_empty_row<D>(p, un.b, un.hg * p.gp + rl - tok * p.gp, i);
           continue;
         }
         chunk_row_keys(p, i, kv_len - q_len, kv_len, p.prefix ? p.prefix[un.b] : 0, jlo_r, jhi_r);
@@ -752,7 +782,7 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
         if (!tc::mbar_wait(refb + (gl & 1), (gl >> 1) & 1, abort_flag)) { ok = false; break; }
         m_ref = refv[(gl & 1) * 128 + row];
       }
-      const ChunkPiece un = piece_at(p, pi);
+      const ChunkPiece un = piece_at<C>(p, pi);
       // O is read out of TMEM before this warpgroup's row sum is posted: the
       // next piece's first PV overwrites O, and its P comes from a warpgroup
       // that has passed the row-sum barrier (with one warpgroup: from this

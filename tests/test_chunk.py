@@ -62,7 +62,7 @@ def test_plan_geometry():
     assert rc == 0 and p["path"] == _lib.FA_PATH_PREFILL
     # 4 q-heads share a K/V head, 2 head groups; 5 tokens x 4 heads: a query tile of 32 rows
     assert p["rows_per_tile"] == 8 and p["n_heads_sched"] == 2 and p["n_row_tiles"] == 1 and p["n_k_tiles"] == 1
-    assert p["n_items"] == 2 * 2 and p["n_kernels"] == 2 and p["n_splits"] == 0  # one key tile: nothing to split
+    assert p["n_items"] == 2 * 2 and p["n_kernels"] == 1 and p["n_splits"] == 0  # few, one key tile: nothing to plan or split
     rc, p = plan(block_table=i32(2, 500), max_seqlen_k=8000)
     assert rc == 0 and p["n_k_tiles"] == 63 and p["n_kernels"] == 3 and p["n_splits"] == 4 * 63
     assert p["workspace_bytes"] >= p["n_splits"] * 128 * 129 * 4
@@ -106,3 +106,11 @@ def test_plan_refusals():
 def test_binding_refuses_host_tensors():
     with pytest.raises(fa.FaError):
         fa.fa_fwd_chunk(T(2, 3, 8, 64), T(2, 40, 2, 64), T(2, 40, 2, 64), i32(2), max_seqlen_k=40)
+
+
+def test_plan_without_planner_only_for_few_short_units():
+    kernels = lambda n, q, k: plan(T(n * q, 8, 128), cu_seqlens_q=i32(n + 1), lens=i32(n), block_table=i32(n, 600),  # noqa: E731
+                                   max_seqlen_q=q, max_seqlen_k=k)[1]["n_kernels"]
+    assert kernels(4, 1, 1024) == 1 and kernels(4, 300, 1024) == 1
+    assert kernels(4, 1, 1025) == 3       # more than 8 key tiles: split and joined
+    assert kernels(1000, 1, 1024) == 2    # many units: listed by the planner
