@@ -445,7 +445,8 @@ int fa_kvcache_append(const fa_tensor* q, const fa_tensor* q_out, const fa_tenso
  * above its maximum or below zero is recorded as FA_ERR_DEVICE_BOUNDS and the
  * sequence's rows are not computed; a page index outside the cache likewise,
  * and the outputs that would have read it are not valid.  Entries of the block
- * table past a sequence's keys, and cache rows past them, are never read.
+ * table past a sequence's keys, and cache rows past them, are never read; its
+ * keys that a window hides may be, so their pages have to be in the cache too.
  * Any page size is taken; a multiple of 16 is copied fastest (the copies are
  * as high as the largest power of two that divides it).
  * FA_ERR_UNSUPPORTED: a stride of 0 along more than one element of q, k_cache

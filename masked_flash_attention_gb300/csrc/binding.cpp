@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -56,16 +57,16 @@ struct Call {
     if (!t) throw Refused();
     return *t;
   }
-  int32_t i32(int i) const {
-    if (args[i] == Py_None) return 0;
+  int32_t i32(int i, bool optional = false) const {
+    if (optional && args[i] == Py_None) return 0;
     int over = 0;
     const long long v = PyLong_AsLongLongAndOverflow(args[i], &over);
     if (v == -1 && PyErr_Occurred()) throw Raised();
     if (over || v < INT32_MIN || v > INT32_MAX) throw Refused();
     return (int32_t)v;
   }
-  float f32(int i) const {
-    if (args[i] == Py_None) return 0.f;
+  float f32(int i, bool optional = false) const {
+    if (optional && args[i] == Py_None) return 0.f;
     const double v = PyFloat_AsDouble(args[i]);
     if (v == -1.0 && PyErr_Occurred()) throw Raised();
     return (float)v;
@@ -163,8 +164,8 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F f) {
     return PyLong_FromLong(FA_ERR_INVALID_ARG);
   } catch (const Raised&) {
     return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
@@ -233,10 +234,10 @@ struct ChunkArgs {
     wl = c.i32(9);
     wr = c.i32(10);
     softcap = c.f32(11);
-    scale = c.f32(12);
+    scale = c.f32(12, true);
     causal = c.truth(13);
-    c.opts.max_seqlen_q = c.i32(14);
-    c.opts.max_seqlen_k = c.i32(15);
+    c.opts.max_seqlen_q = c.i32(14, true);
+    c.opts.max_seqlen_k = c.i32(15, true);
     c.opts.debug_flags = (uint32_t)c.i32(16);
   }
   int plan(const Call& c, fa_plan* pl) const {

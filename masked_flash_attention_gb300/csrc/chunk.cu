@@ -325,13 +325,13 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 #pragma unroll 4
     for (int k = kAhead; k < sp.n; ++k)
       add(pl[k * kChunkRows], *reinterpret_cast<const float4*>(po + (int64_t)k * kChunkRows * D));
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int h = sp.hg * p.gp + row - tok * p.gp;
     const int64_t qrow = (p.cu_q ? p.cu_q[sp.b] : 0) + i, ob = p.cu_q ? 0 : sp.b;
     *reinterpret_cast<uint2*>(p.o + ob * p.o_sb + qrow * p.o_ss + (int64_t)h * p.o_sh + 4 * c) =
         make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
     if (c == 0)
-      p.lse[ob * p.lse_sb + (int64_t)h * p.lse_sh + qrow * p.lse_ss] = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+      p.lse[ob * p.lse_sb + (int64_t)h * p.lse_sh + qrow * p.lse_ss] = sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
   }
 }
 

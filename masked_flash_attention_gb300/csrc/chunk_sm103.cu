@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
         tc::fence_before_sync();
         lt = l;
       }
-      const bool empty = !(lt > 0.f);
+      const bool empty = lt == 0.f;  // (a row with a NaN stays NaN)
       const float inv = empty ? 0.f : 1.f / lt;
       const float lse2 = empty ? -INFINITY : m_ref + __log2f(lt);
       const int q_len = chunk_qlen(p, un.b);
@@ -848,17 +848,16 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
 #pragma unroll
             for (int q = 0; q < 4; ++q) top = fmaxf(top, sl[q * 32 + r1]);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (top != -INFINITY) {
+            if (top == -INFINITY) top = 0.f;  // no quarter keeps a key: all weights 0
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float f = fast_exp2(sl[q * 32 + r1] - top);
-                const float4 v = *reinterpret_cast<const float4*>(so + (q * 8 + rr) * kHalfD + c4);
-                sum += f;
-                o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
-              }
+            for (int q = 0; q < 4; ++q) {
+              const float f = fast_exp2(sl[q * 32 + r1] - top);
+              const float4 v = *reinterpret_cast<const float4*>(so + (q * 8 + rr) * kHalfD + c4);
+              sum += f;
+              o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
             }
-            const float f = sum > 0.f ? 1.f / sum : 0.f;
-            const float ls = sum > 0.f ? top + __log2f(sum) : -INFINITY;
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+            const float ls = sum == 0.f ? -INFINITY : top + __log2f(sum);
             o.x *= f; o.y *= f; o.z *= f; o.w *= f;
             if (un.slot >= 0) {
               const int64_t at = (int64_t)un.slot * kChunkRows + r1;

@@ -114,3 +114,11 @@ def test_plan_without_planner_only_for_few_short_units():
     assert kernels(4, 1, 1024) == 1 and kernels(4, 300, 1024) == 1
     assert kernels(4, 1, 1025) == 3       # more than 8 key tiles: split and joined
     assert kernels(1000, 1, 1024) == 2    # many units: listed by the planner
+
+
+def test_binding_refuses_none_for_numbers():
+    with pytest.raises(TypeError):
+        plan(window_left=None)
+    with pytest.raises(TypeError):
+        plan(softcap=None)
+    assert plan(window_left=2**40)[0] == E

@@ -361,3 +361,39 @@ def test_few_rows(hq, hkv, d, dtype):
     check(c, "prefix", prefix_lens=pre)
     out, lse, _ = run(c, alibi_slopes=slopes)
     assert_close(out, lse, oracle(c, alibi_slopes=slopes), "alibi", logits=2.0, n_keys=5000)
+
+
+def test_nothing_to_do_and_no_keys():
+    m = fa()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    z = lambda *s: torch.zeros(*s, dtype=BF, device=DEV)  # noqa: E731
+    # no sequence; sequences without rows (with and without room for some); rows without keys, in an empty cache too
+    out, lse, ws = m.fa_fwd_chunk(z(3, 4, 64), z(2, 16, 2, 64), z(2, 16, 2, 64), i32(), cu_seqlens_q=i32(0),
+                                  block_table=torch.zeros(0, 1, dtype=torch.int32, device=DEV), max_seqlen_q=4, max_seqlen_k=16)
+    assert out.shape == (3, 4, 64) and m.fa_check_device_error(ws) == (0, 0)
+    for max_q in (0, 4):
+        out, _, ws = m.fa_fwd_chunk(z(0, 4, 64), z(2, 16, 2, 64), z(2, 16, 2, 64), i32(5, 0), cu_seqlens_q=i32(0, 0, 0),
+                                    block_table=torch.zeros(2, 1, dtype=torch.int32, device=DEV), max_seqlen_q=max_q, max_seqlen_k=16)
+        torch.cuda.synchronize()
+        assert out.numel() == 0 and m.fa_check_device_error(ws) == (0, 0)
+    for pages in (0, 2):
+        for max_k in (0, 16) if pages else (0,):
+            out, lse, ws = m.fa_fwd_chunk(z(5, 4, 128) + 1, z(pages, 16, 2, 128), z(pages, 16, 2, 128), i32(0, 0),
+                                          cu_seqlens_q=i32(0, 2, 5), block_table=torch.full((2, 1), -1, dtype=torch.int32, device=DEV),
+                                          max_seqlen_q=3, max_seqlen_k=max_k)
+            assert (out == 0).all() and torch.isneginf(lse).all() and m.fa_check_device_error(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_stays_in_its_row(d):
+    """A NaN in one query row makes that row NaN, whole, split or narrow, and no other."""
+    for q_lens, kv in (([40, 3], [300, 200]), ([1, 2], [300, 5000]), ([40, 2], [9000, 400])):
+        c = case(300, q_lens, kv, d=d, page=16)
+        ref = run(c)
+        bad = dict(c, q=c["q"].clone())
+        bad["q"][1, 2, 5] = float("nan")
+        out, lse, _ = run(bad)
+        assert torch.isnan(out[1, 2]).all() and torch.isnan(lse[2, 1])
+        keep = torch.ones(out.shape[:2], dtype=torch.bool, device=DEV)
+        keep[1, 2] = False
+        assert torch.equal(out[keep], ref[0][keep]) and torch.equal(lse.T[keep], ref[1].T[keep])
