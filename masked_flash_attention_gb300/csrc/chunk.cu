@@ -29,8 +29,9 @@
 namespace mfa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kBins = 1024;
+constexpr int kPlanThreads = 256;  // (512 and 1024 took longer, over their barriers)
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kBins = 256;
 constexpr int kSeqSmem = 1024, kTileSmem = 1280;  // sequences and row tiles kept in shared memory, more in the workspace
 constexpr int kTailFlag = 1 << 30;                // in a row tile's second word: its units are cut as tail
 // Cost model, in key tiles (about 0.8 us of a CTA): what a piece costs beside
@@ -50,42 +51,42 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = s_warp[lane];
+  int before = 0;
+  total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    s_warp[32 + lane] = w;
+  for (int w = 0; w < kPlanWarps; ++w) {
+    const int y = s_warp[w];
+    if (w < warp) before += y;
+    total += y;
   }
   __syncthreads();
-  total = s_warp[32 + 31];
-  const int r = x - v + (warp ? s_warp[32 + warp - 1] : 0);
-  __syncthreads();
-  return r;
+  return x - v + before;
 }
 
-// One CTA cuts the step into pieces (see the head of this file).
+// One CTA cuts the step into pieces (see the head of this file).  It runs before
+// everything else and its code once, from a cold instruction cache, so it is kept
+// short: loops not unrolled, one warp-wide step where one will do (64 single
+// tokens: 5.7 us, of which 1.2 the first loads; unrolled, with 1024 threads, 7.6).
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ int4 s_seq[kSeqSmem];
   __shared__ int4 s_tile[kTileSmem];
   __shared__ int s_hist[kBins];
-  __shared__ int s_warp[64];
+  __shared__ int s_warp[kPlanWarps];
   __shared__ float s_cost[32];
   __shared__ int s_T[32];
-  __shared__ int s_nmax, s_slots, s_splits, s_bin, s_before;
-  __shared__ unsigned int s_work;
+  __shared__ int s_nmax[kPlanWarps];
+  __shared__ unsigned int s_work[kPlanWarps];
+  __shared__ int s_slots, s_splits, s_bin, s_before;
   let_dependents_start();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int4* const seqs = p.n_seq <= kSeqSmem ? s_seq : p.seqs;
   if (tid == 0) {
-    s_nmax = s_slots = s_splits = 0;
-    s_work = 0;
+    s_slots = s_splits = 0;
   }
 
   // ---- row tiles per sequence; sequences whose lengths do not fit get none
   int R = 0;
+#pragma unroll 1
   for (int s0 = 0; s0 < p.n_seq; s0 += kPlanThreads) {
     const int s = s0 + tid;
     int nt = 0;
@@ -109,8 +110,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   // ---- key tiles of each row tile
   int nmax = 0;
   unsigned int work = 0;
+#pragma unroll 1
   for (int r = tid; r < R; r += kPlanThreads) {
     int lo = 0, hi = p.n_seq;  // the last sequence whose first tile is at or before r
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (seqs[mid].x <= r) lo = mid;
@@ -126,52 +129,65 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   nmax = __reduce_max_sync(0xffffffffu, nmax);
   work = __reduce_add_sync(0xffffffffu, work);
   if (lane == 0) {
-    atomicMax(&s_nmax, nmax);
-    atomicAdd(&s_work, work);
+    s_nmax[warp] = nmax;
+    s_work[warp] = work;
   }
   s_hist[tid] = 0;
   __syncthreads();
-  nmax = s_nmax;
-  const float fwork = (float)s_work * p.n_hg, P = (float)p.grid;
+  float fwork = 0.f;
+#pragma unroll 1
+  for (int w = 0; w < kPlanWarps; ++w) {
+    nmax = max(nmax, s_nmax[w]);
+    fwork += (float)s_work[w];
+  }
+  fwork *= p.n_hg;
+  const float P = (float)p.grid;
   const int units = R * p.n_hg;
 
-  // ---- the length T, one candidate per warp: whole units; t0 tiles, which would
-  // fill one round of the grid evenly, up to twice as many (room for the units'
-  // odd lengths), and the same for two, three and four rounds
+  // ---- the length T, of 32 candidates: whole units; t0 tiles, which would fill
+  // one round of the grid evenly, up to twice as many (room for the units' odd
+  // lengths), and the same for two, three and four rounds
   int T = max(nmax, 1);
   if (p.max_slots > 0 && nmax > 1) {
     const float t0 = fwork / P;
-    float f = 0.f;
-    if (warp <= 16) f = 1.f + (warp - 1) / 16.f;
-    else if (warp <= 24) f = (1.f + (warp - 17) / 8.f) / 2.f;
-    else if (warp <= 28) f = (1.f + (warp - 25) / 4.f) / 3.f;
-    else f = (1.f + (warp - 29) / 4.f) / 4.f;
-    const int t = warp == 0 ? nmax : min(max(1, (int)ceilf(f * t0)), nmax);
-    float cost = 3e38f;
-    if (warp == 0 || t < nmax) {
-      int m = 0, part = 0, longest = 0;
-      for (int r = lane; r < R; r += 32) {
-        const int n = tiles[r].w, k = n <= t ? 1 : (n + t - 1) / t;
-        m += k;
-        if (k > 1) part += k;
-        longest = max(longest, k > 1 ? (n + k - 1) / k : n);
+#pragma unroll 1
+    for (int j = warp; j < 32; j += kPlanWarps) {
+      float f;
+      if (j <= 16) f = 1.f + (j - 1) / 16.f;
+      else if (j <= 24) f = (1.f + (j - 17) / 8.f) / 2.f;
+      else if (j <= 28) f = (1.f + (j - 25) / 4.f) / 3.f;
+      else f = (1.f + (j - 29) / 4.f) / 4.f;
+      const int t = j == 0 ? nmax : min(max(1, (int)ceilf(f * t0)), nmax);
+      float cost = 3e38f;
+      if (j == 0 || t < nmax) {
+        int m = 0, part = 0, longest = 0;
+        const float per_t = 1.f / t;
+#pragma unroll 1
+        for (int r = lane; r < R; r += 32) {
+          // (quotients rounded up as floats: a cost may be off by a piece)
+          const float n = (float)tiles[r].w;
+          const int k = n <= t ? 1 : (int)ceilf(n * per_t);
+          m += k;
+          if (k > 1) part += k;
+          longest = max(longest, (int)ceilf(__fdividef(n, (float)k)));
+        }
+        m = __reduce_add_sync(0xffffffffu, m) * p.n_hg;
+        part = __reduce_add_sync(0xffffffffu, part) * p.n_hg;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        const float total = fwork + kPieceCost * m + kPartialCost * part;
+        cost = fmaxf(longest + kPieceCost + (part ? kPartialCost : 0.f),
+                     (total + (ceilf(m / P) * P - m) * total / m) / P) + (part ? kJoinCost : 0.f);
+        if (part > p.max_slots) cost = 3e38f;
       }
-      m = __reduce_add_sync(0xffffffffu, m) * p.n_hg;
-      part = __reduce_add_sync(0xffffffffu, part) * p.n_hg;
-      longest = __reduce_max_sync(0xffffffffu, longest);
-      const float total = fwork + kPieceCost * m + kPartialCost * part;
-      cost = fmaxf(longest + kPieceCost + (part ? kPartialCost : 0.f), (total + (ceilf(m / P) * P - m) * total / m) / P) +
-             (part ? kJoinCost : 0.f);
-      if (part > p.max_slots) cost = 3e38f;
-    }
-    if (lane == 0) {
-      s_cost[warp] = cost;
-      s_T[warp] = t;
+      if (lane == 0) {
+        s_cost[j] = cost;
+        s_T[j] = t;
+      }
     }
     __syncthreads();
     float best = s_cost[lane];
     int at = lane;
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) {
       const float c = __shfl_xor_sync(0xffffffffu, best, o);
       const int w = __shfl_xor_sync(0xffffffffu, at, o);
@@ -183,6 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     T = s_T[at];
   }
   int shift = 0;
+#pragma unroll 1
   while ((T >> shift) >= kBins) ++shift;
   auto bin_of = [&](int len) { return kBins - 1 - (len >> shift); };
 
@@ -195,6 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     const int tails = (last + p.n_hg - 1) / p.n_hg;  // row tiles
     cut = min(min(p.grid / (tails * p.n_hg), kMaxTailCut), p.max_slots / (tails * p.n_hg));
     if (cut >= 2) {
+#pragma unroll 1
       for (int r = tid; r < R; r += kPlanThreads) atomicAdd(&s_hist[bin_of(tiles[r].w)], 1);
       __syncthreads();
       const int mine = s_hist[tid];
@@ -210,6 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       const int bin = s_bin, whole = R - tails - s_before;
       int seen = 0;
       bool worth = false;
+#pragma unroll 1
       for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
         const int r = r0 + tid;
         const int b = r < R ? bin_of(tiles[r].w) : -1;
@@ -232,6 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   };
 
   // ---- list the pieces, longest first (a counting sort by length)
+#pragma unroll 1
   for (int r = tid; r < R; r += kPlanThreads) {
     const int4 t = tiles[r];
     const int k = pieces_of(t), len = t.w / k, more = t.w - len * k;
@@ -243,6 +263,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   const int start = block_scan(s_hist[tid], s_warp, total);
   s_hist[tid] = start;
   __syncthreads();
+#pragma unroll 1
   for (int u = tid; u < units; u += kPlanThreads) {
     const int r = fast_div(u, p.div_hg), hg = u - r * p.n_hg;
     const int4 t = tiles[r];
@@ -256,6 +277,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       p.splits[atomicAdd(&s_splits, 1)] = sp;
     }
     int at = t.z;
+#pragma unroll 1
     for (int i = 0; i < k; ++i) {
       const int c = len + (i < more ? 1 : 0);
       int4* dst = reinterpret_cast<int4*>(p.pieces + atomicAdd(&s_hist[bin_of(c)], 1));
