@@ -515,16 +515,16 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
   const int64_t ctas = (int64_t)sm_count() * (p.pair ? 2 : 1);
   // partials: at most two rounds of the grid, and no more than all tiles alone;
-  // none where no sequence has more than 8 key tiles: cutting and joining such
-  // units gains nothing for the launch it costs (one token over 700 keys, 6
-  // tiles: 13.3 us cut in six and joined, 14.0 us whole, both in a graph)
+  // none where no sequence has more than 8 key tiles: such units then need no
+  // planner either (below).  One token over 700 keys, 6 tiles, in a graph: cut in
+  // six and joined 13.3 us, whole with the planner 14.0, whole without it 10.2.
   const int64_t slots = n_kt > 8 ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
   const int64_t pieces = units + slots;
   p.max_rtiles = (int32_t)rtiles;
   p.max_slots = (int32_t)slots;
   p.grid = (int32_t)std::min<int64_t>(ctas, std::max<int64_t>(1, pieces));
   // Few short units: no planner, each CTA works out its own piece, one per row
-  // tile that a sequence may have and head group (one token that sees 60 keys: 7.2
+  // tile that a sequence may have and head group (one token that sees 60 keys: 7.3
   // us in a graph, with the planner 10.8).  More units than CTAs are left to
   // the planner's order: 8 x 1024 tokens of 12 heads, 768 units of 1 to 8 tiles,
   // took 42 us in turn, 34 us longest first.
