@@ -39,6 +39,7 @@ constexpr int kTailFlag = 1 << 30;                // in a row tile's second word
 // costs more, and what there being any to join does.
 constexpr float kPieceCost = 3.f, kPartialCost = 1.5f, kJoinCost = 4.f;
 constexpr int kMaxTailCut = 8;
+constexpr int kMaxSeqTiles = 1 << 22;  // row tiles of one sequence
 
 // Block-wide exclusive prefix sum; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
@@ -98,7 +99,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     int total;
     q.x = R + block_scan(nt, s_warp, total);
     if (s < p.n_seq) seqs[s] = q;
-    R += total;
+    // (a sum that overlapping cu_seqlens_q grow stays in 32 bits: total is at most
+    // 256 * kMaxSeqTiles, and past max_rtiles nothing depends on R)
+    R = min(R + total, p.max_rtiles + 1);
   }
   if (R > p.max_rtiles) {  // overlapping cu_seqlens_q: more tiles than the workspace lists
     if (tid == 0) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)p.n_seq);
@@ -511,7 +514,8 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // ---- bounds of the work, workspace
   int64_t rtiles = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens);
   if (cu_q) rtiles = std::min(rtiles, p.tot_q / p.rt_tokens + n_seq);
-  if (rtiles * p.n_hg > (1 << 27)) return FA_ERR_INVALID_ARG;
+  const int64_t longest = cu_q ? std::min(Sq, p.tot_q) : Sq;
+  if (rtiles * p.n_hg > (1 << 27) || (longest + p.rt_tokens - 1) / p.rt_tokens > kMaxSeqTiles) return FA_ERR_INVALID_ARG;
   const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
   const int64_t ctas = (int64_t)sm_count() * (p.pair ? 2 : 1);
   // partials: at most two rounds of the grid, and no more than all tiles alone;

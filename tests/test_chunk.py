@@ -116,6 +116,17 @@ def test_plan_without_planner_only_for_few_short_units():
     assert kernels(1000, 1, 1024) == 2    # many units: listed by the planner
 
 
+def test_plan_refuses_more_row_tiles_than_it_can_count():
+    # (strides that overlap, so that the rows need no memory of their own)
+    def rows(n):
+        return torch.empty(n * 8 + 128 * 8 + 64, dtype=BF).as_strided((n, 128, 64), (8, 8, 1))
+
+    # 128 q-heads share a K/V head: a token per query tile
+    many = lambda n: plan(rows(n), T(10, 16, 1, 64), lse=torch.empty(1).as_strided((128, n), (0, 0)),  # noqa: E731
+                          cu_seqlens_q=i32(2), lens=i32(1), block_table=i32(1, 5), max_seqlen_q=n)[0]
+    assert many(2**22) == 0 and many(2**22 + 1) == E
+
+
 def test_binding_refuses_none_for_numbers():
     with pytest.raises(TypeError):
         plan(window_left=None)

@@ -196,6 +196,24 @@ def test_lengths_and_pages_that_do_not_fit():
         assert_close(out, lse, ref)
 
 
+def test_overlapping_rows_past_32_bits():
+    # every other sequence claims all 2^20 rows, those between run backwards: 8192 row tiles times 2^19 sequences
+    m = fa()
+    n, seqs = 2**20, 2**20
+    cu = torch.zeros(seqs + 1, dtype=torch.int32)
+    cu[1::2] = n
+    assert (n // 128) * (seqs // 2) == 2**32
+    q = torch.zeros(n, 1, 64, dtype=BF, device="cuda")
+    kv = torch.zeros(1, 16, 1, 64, dtype=BF, device="cuda")
+    lens = torch.full((seqs,), 16, dtype=torch.int32, device="cuda")
+    guard = torch.full((n + 256, 1, 64), 7.0, dtype=BF, device="cuda")
+    out, _, ws = m.fa_fwd_chunk(q, kv, kv, lens, out=guard[128:128 + n], cu_seqlens_q=cu.cuda(),
+                                block_table=torch.zeros(seqs, 1, dtype=torch.int32, device="cuda"), max_seqlen_q=n,
+                                max_seqlen_k=16)
+    assert m.fa_check_device_error(ws)[0] == m._lib.FA_ERR_DEVICE_BOUNDS
+    assert (guard[:128] == 7).all() and (guard[128 + n:] == 7).all()
+
+
 def test_small_workspace_and_misaligned_arguments():
     m = fa()
     c = case(125, [4], [60])
