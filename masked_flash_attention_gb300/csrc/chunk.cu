@@ -522,7 +522,9 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // none where no sequence has more than 8 key tiles: such units then need no
   // planner either (below).  One token over 700 keys, 6 tiles, in a graph: cut in
   // six and joined 13.3 us, whole with the planner 14.0, whole without it 10.2.
-  const int64_t slots = n_kt > 8 ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
+  // None either for more tiles than 32-bit sums hold, on which the planner's bound
+  // on the partials rests (there are thousands of units then).
+  const int64_t slots = n_kt > 8 && rtiles * n_kt <= INT32_MAX ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
   const int64_t pieces = units + slots;
   p.max_rtiles = (int32_t)rtiles;
   p.max_slots = (int32_t)slots;

@@ -116,6 +116,20 @@ def test_plan_without_planner_only_for_few_short_units():
     assert kernels(1000, 1, 1024) == 2    # many units: listed by the planner
 
 
+def test_plan_cuts_only_what_its_sums_hold():
+    # one token each of n sequences over 2^18 key tiles (they share their pages): 2^31 tiles and more are not cut
+    def splits(n):
+        kc = torch.empty(1, 2**20, 1, 64, dtype=BF)
+        return plan(T(n, 1, 64), kc, cu_seqlens_q=i32(n + 1), lens=i32(n), block_table=i32(n, 32), max_seqlen_q=1,
+                    max_seqlen_k=(2**31 - 1) // 64)
+
+    n_kt = 2**18
+    rc, p = splits(2**13 - 1)
+    assert rc == 0 and p["n_k_tiles"] == n_kt and p["n_splits"] > 0
+    rc, p = splits(2**13 + 1)
+    assert rc == 0 and p["n_splits"] == 0 and p["n_kernels"] == 2
+
+
 def test_plan_refuses_more_row_tiles_than_it_can_count():
     # (strides that overlap, so that the rows need no memory of their own)
     def rows(n):
