@@ -125,6 +125,7 @@ struct Call {
   at::Tensor workspace(const at::Tensor* t, size_t bytes) {
     at::Tensor ws;
     if (t) {
+      if (!t->is_contiguous()) throw Refused();  // (its bytes would not be those behind its pointer)
       ws = *t;
     } else {
       ws = empty({(int64_t)(bytes < 256 ? 256 : bytes)}, at::kByte);

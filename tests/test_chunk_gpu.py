@@ -196,6 +196,20 @@ def test_lengths_and_pages_that_do_not_fit():
         assert_close(out, lse, ref)
 
 
+def test_workspace_has_to_be_contiguous():
+    m = fa()
+    z = lambda *s: torch.zeros(*s, dtype=BF, device="cuda")  # noqa: E731
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    for bad in (ws[:256].expand(4096, 256), ws[::2]):
+        with pytest.raises(m.FaError) as e:
+            m.fa_fwd_chunk(z(1, 1, 1, 64), z(1, 4, 1, 64), z(1, 4, 1, 64), lens, max_seqlen_k=4, workspace=bad)
+        assert e.value.status == m._lib.FA_ERR_INVALID_ARG
+        with pytest.raises(m.FaError) as e:
+            m.fa_kvcache_append(z(1, 1, 1, 64), z(1, 1, 1, 64), z(1, 4, 1, 64), z(1, 4, 1, 64), lens, workspace=bad)
+        assert e.value.status == m._lib.FA_ERR_INVALID_ARG
+
+
 def test_overlapping_rows_past_32_bits():
     # every other sequence claims all 2^20 rows, those between run backwards: 8192 row tiles times 2^19 sequences
     m = fa()
