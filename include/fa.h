@@ -449,6 +449,7 @@ int fa_kvcache_append(const fa_tensor* q, const fa_tensor* q_out, const fa_tenso
  * keys that a window hides may be, so their pages have to be in the cache too.
  * Any page size is taken; a multiple of 16 is copied fastest (the copies are
  * as high as the largest power of two that divides it).
+ * FA_ERR_INVALID_ARG: also a chunk of more than 2^22 query tiles.
  * FA_ERR_UNSUPPORTED: a stride of 0 along more than one element of q, k_cache
  * or v_cache.  The result does not depend on scheduling.  Workspace:
  * fa_fwd_chunk_plan's workspace_bytes, its first 256 bytes zero-filled once. */

@@ -210,6 +210,16 @@ def test_workspace_has_to_be_contiguous():
         assert e.value.status == m._lib.FA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, H)])
+def test_shared_and_repeated_pages(d, dtype):
+    # a common beginning of three sequences, and one sequence that holds a page twice
+    c = case(160, [5, 40, 1], [90, 90, 1200], d=d, dtype=dtype)
+    c["bt"][1, :3] = c["bt"][0, :3]
+    c["bt"][2, :3] = c["bt"][0, :3]
+    c["bt"][2, 7] = c["bt"][2, 50]
+    check(c)
+
+
 def test_overlapping_rows_past_32_bits():
     # every other sequence claims all 2^20 rows, those between run backwards: 8192 row tiles times 2^19 sequences
     m = fa()
