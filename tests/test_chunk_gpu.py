@@ -439,3 +439,40 @@ def test_nan_stays_in_its_row(d):
         keep = torch.ones(out.shape[:2], dtype=torch.bool, device=DEV)
         keep[1, 2] = False
         assert torch.equal(out[keep], ref[0][keep]) and torch.equal(lse.T[keep], ref[1].T[keep])
+
+
+def few_row_lengths(gp):
+    """New tokens per sequence that make 1, 8, 9, 31 and 32 rows of gp heads, where gp divides them."""
+    return [n // gp for n in (1, 8, 9, 31, 32) if n % gp == 0 and n >= gp] or [32 // gp]
+
+
+@pytest.mark.parametrize("hq,hkv,gp", [(2, 2, 1), (4, 2, 2), (3, 1, 3), (8, 2, 4), (5, 1, 5), (8, 1, 8), (9, 1, 9), (16, 1, 16),
+                                       (31, 1, 31), (32, 1, 32)])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (128, H), (64, BF), (64, H)])
+@pytest.mark.parametrize("far", [False, True])
+def test_form_for_few_rows(hq, hkv, gp, d, dtype, far):
+    """Calls in which no unit has more than 32 (token, head) rows: the keys of a tile are dealt to its four
+    quarters.  Up to 1500 keys and (d = 64: the other form; whole and split) up to 5000; every kind of logit."""
+    m = fa()
+    q_lens = few_row_lengths(gp) * 2
+    if max(q_lens) * gp < 32 and 32 // gp not in q_lens:
+        q_lens.append(32 // gp)
+    lens = [33, 1500, 129, 700, 1, 1000, 31, 97, 128, 260, 600] if not far else [5000, 33, 129, 2500, 1, 300, 4097, 31, 640, 700, 90]
+    kv = [max(lens[i % len(lens)], n) for i, n in enumerate(q_lens)]
+    c = case(400 + hq, q_lens, kv, hq=hq, hkv=hkv, d=d, dtype=dtype, page=32)
+    _, plan = m.fa_fwd_chunk_plan(c["q"], c["kc"], c["vc"], c["lens"], cu_seqlens_q=c["cu"], block_table=c["bt"],
+                                  max_seqlen_q=c["max_q"], max_seqlen_k=c["max_k"])
+    assert plan["rows_per_tile"] == 32 // gp and plan["n_heads_sched"] == hq // gp
+    assert c["max_q"] * gp <= 32 and (c["max_k"] > 2048) == far
+    slopes = torch.tensor([2.0 ** -(1 + h % 8) for h in range(hq)])
+    pre = torch.tensor([(0, 1, 40, 200, 10000)[i % 5] for i in range(len(q_lens))], dtype=torch.int32)
+    check(c, "plain")
+    check(c, "window", window_left=20)
+    check(c, "both windows", causal=False, window_left=200, window_right=3)
+    check(c, "prefix", prefix_lens=pre)
+    check(c, "soft-cap", logits=2.0, softcap=20.0)
+    check(c, "soft-cap and window", logits=2.0, softcap=20.0, window_left=600)
+    check(c, "soft-cap and prefix", logits=2.0, softcap=20.0, prefix_lens=pre)
+    for kw in ({}, dict(softcap=15.0), dict(prefix_lens=pre), dict(window_left=100)):
+        out, lse, _ = run(c, alibi_slopes=slopes, **kw)
+        assert_close(out, lse, oracle(c, alibi_slopes=slopes, **kw), f"alibi {list(kw)}", logits=2.0, n_keys=c["max_k"])
