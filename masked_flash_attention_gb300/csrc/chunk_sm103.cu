@@ -730,7 +730,8 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
           }
         }
         if (r_own != m_ref) {
-          l = (r_own == -INFINITY) ? 0.f : l * fast_exp2(r_own - m_ref);
+          // (before the row's first finite logit l is 0, or NaN after a NaN one: kept)
+          if (r_own != -INFINITY) l *= fast_exp2(r_own - m_ref);
           r_own = m_ref;
         }
         // one warpgroup: the P buffer is free once the PV before is done (with

@@ -476,3 +476,46 @@ def test_form_for_few_rows(hq, hkv, gp, d, dtype, far):
     for kw in ({}, dict(softcap=15.0), dict(prefix_lens=pre), dict(window_left=100)):
         out, lse, _ = run(c, alibi_slopes=slopes, **kw)
         assert_close(out, lse, oracle(c, alibi_slopes=slopes, **kw), f"alibi {list(kw)}", logits=2.0, n_keys=c["max_k"])
+
+
+def poison(c, s, lo, hi, head, what="kc"):
+    """Keys lo .. hi - 1 of sequence s as NaN for one K/V head."""
+    page = c["kc"].shape[1]
+    for j in range(lo, hi):
+        c[what][int(c["bt"][s, j // page]), j % page, head] = float("nan")
+
+
+@pytest.mark.parametrize("q_lens,kv,narrow", [([40, 3], [700, 200], False), ([2, 3], [700, 200], True),
+                                              ([40, 2], [9000, 400], False), ([3, 2], [9000, 400], True)])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, H)])
+def test_nan_keys_of_one_tile(q_lens, kv, narrow, d, dtype):
+    """Keys that are NaN fill a row's first tile (or a quarter of it) and finite ones
+    follow: output and LSE of the rows that keep them are NaN; no other changes."""
+    m = fa()
+    c = case(310, q_lens, kv, d=d, dtype=dtype)
+    _, plan = m.fa_fwd_chunk_plan(c["q"], c["kc"], c["vc"], c["lens"], cu_seqlens_q=c["cu"], block_table=c["bt"],
+                                  max_seqlen_q=c["max_q"], max_seqlen_k=c["max_k"])
+    assert plan["rows_per_tile"] == (16 if narrow else 64) and (plan["n_splits"] > 0) == (kv[0] > 1024)
+    ref = run(c)
+    for lo, hi in ((0, 128), (0, 32), (96, 128), (0, 256), (128, 256)):
+        bad = dict(c, kc=c["kc"].clone())
+        poison(bad, 0, lo, hi, 1)
+        out, lse, _ = run(bad)
+        hit = torch.zeros(out.shape[:2], dtype=torch.bool, device=DEV)
+        hit[:q_lens[0], 2:] = True  # heads 2 and 3 of sequence 0 read K/V head 1, and every row sees the first tiles
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse.T[hit]).all(), (lo, hi)
+        assert torch.equal(out[~hit], ref[0][~hit]) and torch.equal(lse.T[~hit], ref[1].T[~hit]), (lo, hi)
+    # hidden from the first rows by the causal rule, from all rows by a window
+    bad = dict(c, kc=c["kc"].clone())
+    poison(bad, 0, kv[0] - 1, kv[0], 1)
+    out, lse, _ = run(bad)
+    hit[:] = False
+    hit[q_lens[0] - 1, 2:] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse.T[hit]).all()
+    assert torch.equal(out[~hit], ref[0][~hit]) and torch.equal(lse.T[~hit], ref[1].T[~hit])
+    bad = dict(c, kc=c["kc"].clone())
+    first = kv[0] - q_lens[0] - 300
+    poison(bad, 0, first - 20, first, 1)
+    ref = run(c, window_left=300)
+    out, lse, _ = run(bad, window_left=300)
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
