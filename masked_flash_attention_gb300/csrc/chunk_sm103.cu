@@ -144,6 +144,16 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// Soft-caps above this one are far from most logits, and what 1 + e^(2 y) rounds
+// off near y = 0 would grow with them: there the logit is scale x (tanh y) / y by
+// the power series (cut after y^8: 2e-8 at |y| = 1/4).
+constexpr float kPlainSoftcap = 128.f;
+__device__ __forceinline__ float wide_softcap(float x, float k, float c1, const ChunkParams& p) {
+  const float y = x * p.scale * p.inv_softcap, y2 = y * y;
+  const float series = fmaf(y2, fmaf(y2, fmaf(y2, fmaf(y2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float far = fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x * k)), c1);
+  return fabsf(y) > 0.25f ? far : x * p.scale_log2 * series;
+}
 // Waits for this thread's TMEM loads; the registers pass through, so that no use
 // of theirs moves before the wait.
 __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
@@ -646,11 +656,16 @@ __global__ void __launch_bounds__(CCfg<D, NW, NP>::kThreads, CCfg<D, NW, NP>::kC
             // logits in log2 units: soft-cap or scale, then the distance penalty
             if (p.softcap > 0.f) {
               // cap tanh(y) = cap - 2 cap / (1 + e^(2 y)); the rounding near 1 leaves
-              // about cap 2^-23 in the logit (5e-6 at cap 30)
+              // about 3e-7 cap in the logit (1e-5 at cap 30)
               const float k = 2.f * p.scale_log2 * p.inv_softcap, c1 = p.softcap * kLog2e;
+              if (p.softcap <= kPlainSoftcap) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[e] = __float_as_uint(fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(__uint_as_float(x[e]) * k)), c1));
+                for (int e = 0; e < 32; ++e)
+                  x[e] = __float_as_uint(fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(__uint_as_float(x[e]) * k)), c1));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(wide_softcap(__uint_as_float(x[e]), k, c1, p));
+              }
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.scale_log2);

@@ -519,3 +519,15 @@ def test_nan_keys_of_one_tile(q_lens, kv, narrow, d, dtype):
     ref = run(c, window_left=300)
     out, lse, _ = run(bad, window_left=300)
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("d,dtype,q_lens", [(128, BF, [40, 3]), (64, H, [40, 3]), (128, H, [2, 1]), (64, BF, [2, 1])])
+def test_soft_caps_far_above_the_logits(d, dtype, q_lens):
+    """cap tanh(x / cap) is x itself for a cap far above it, to the rounding of fp32; and caps that
+    logits of some hundred reach."""
+    c = case(500, q_lens, [700, q_lens[1]], d=d, dtype=dtype)
+    for cap in (100.0, 1e3, 1e5, 1e8, 3e38):
+        check(c, f"cap {cap}", softcap=cap)
+    # logits of a standard deviation of 34; x is off by 34 times as much, and by up to 2e-6 |x| < 1e-3 from tanh
+    for cap in (130.0, 500.0):
+        check(c, f"cap {cap}", logits=34.0, softcap=cap, scale=3.0)
