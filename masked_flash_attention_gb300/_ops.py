@@ -16,14 +16,28 @@ import torch
 from . import _lib
 from ._lib import FA_ERR_INVALID_ARG, FA_OK, FaError, _ref, fa_rope_scaling, lib
 
+
+class _Unusable:
+    """Stands in for a compiled module that is missing or built for something
+    else: a call that needs it raises, and the rest of the package works."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{_BINDING} {self._why}: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+
+
 _BINDING = _lib.LIB_PATH.replace("libmfa_gb300.so", "_binding.so")
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError(f"{_BINDING} is missing or does not load ({e}): build it with "
-                      "`python -c 'import __graft_entry__ as g; g.build()'`") from e
-if _binding.ABI_VERSION != _lib.ABI_VERSION:
-    raise ImportError(f"{_BINDING} has ABI {_binding.ABI_VERSION}, this package ABI {_lib.ABI_VERSION}: rebuild it")
+    _binding = _Unusable(f"is missing or does not load ({e})")
+else:
+    _built_for = tuple(getattr(_binding, name, None) for name in ("ABI_VERSION", "TORCH_VERSION"))
+    if _built_for != (_lib.ABI_VERSION, torch.__version__):
+        _binding = _Unusable("was built for ABI {} and torch {}, ".format(*_built_for) +
+                             f"this is ABI {_lib.ABI_VERSION} and torch {torch.__version__}")
 
 _SCALINGS = {"linear": _lib.FA_ROPE_LINEAR, "ntk": _lib.FA_ROPE_NTK, "blend": _lib.FA_ROPE_BLEND,
              "yarn": _lib.FA_ROPE_YARN}

@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -38,6 +39,12 @@ def torch_dir() -> str:
     if spec is None:
         raise RuntimeError("torch not found: the binding is compiled against its headers")
     return os.path.dirname(spec.origin)
+
+
+def torch_version() -> str:
+    """torch.__version__, read without importing torch."""
+    with open(os.path.join(torch_dir(), "version.py")) as f:
+        return re.search(r"__version__ = ['\"](.*?)['\"]", f.read()).group(1)
 
 
 def _deps_mtime() -> float:
@@ -72,7 +79,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         include = [os.path.join(ROOT, "include"), os.path.join(torch_dir(), "include"),
                    os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"),
                    sysconfig.get_paths()["include"]]
-        run(["g++", "-O2", "-std=c++17", "-fPIC", *("-I" + d for d in include), "-c",
+        run(["g++", "-O2", "-std=c++17", "-fPIC", f'-DMFA_TORCH_VERSION="{torch_version()}"', *("-I" + d for d in include), "-c",
              os.path.join(CSRC, "binding.cpp"), "-o", obj], "g++ failed for binding.cpp")
         return obj
 

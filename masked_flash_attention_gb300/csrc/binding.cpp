@@ -307,7 +307,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 PyMODINIT_FUNC PyInit__binding(void) {
   PyObject* m = PyModule_Create(&module);
-  if (m && PyModule_AddIntConstant(m, "ABI_VERSION", FA_ABI_VERSION) < 0) {
+  // what the module was compiled against: the package checks both before it uses it
+  if (m && (PyModule_AddIntConstant(m, "ABI_VERSION", FA_ABI_VERSION) < 0 ||
+            PyModule_AddStringConstant(m, "TORCH_VERSION", MFA_TORCH_VERSION) < 0)) {
     Py_DECREF(m);
     return nullptr;
   }
