@@ -20,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmfa_gb300.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(BUILD, "built_for.txt")
 SOURCES = ["api.cu", "sched.cu", "topk.cu", "decode.cu", "prefill_sm103.cu", "prefill_f16.cu", "backward.cu", "backward_sm103.cu", "noalloc.cu", "rope.cu", "chunk.cu", "chunk_sm103.cu",
            "chunk_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,10 +56,22 @@ def _deps_mtime() -> float:
     return max(m, os.path.getmtime(__file__))
 
 
+def built_for() -> str:
+    """What the binding is compiled against, which no time of a source file tells."""
+    return f"torch {torch_version()}, python {sysconfig.get_config_var('SOABI')}\n"
+
+
+def stale() -> bool:
+    outputs = (LIB, BINDING, BUILT_FOR)
+    if not all(os.path.exists(f) for f in outputs) or min(map(os.path.getmtime, outputs)) < _deps_mtime():
+        return True
+    with open(BUILT_FOR) as f:
+        return f.read() != built_for()
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile (if stale) and return the path of the shared library."""
-    outputs = (LIB, BINDING)
-    if not force and all(os.path.exists(f) for f in outputs) and min(map(os.path.getmtime, outputs)) >= _deps_mtime():
+    if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -101,6 +114,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
          "-L" + os.path.join(torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"],
         "link of the binding failed")
     os.replace(tmp, BINDING)
+    with open(BUILT_FOR, "w") as f:
+        f.write(built_for())
     return LIB
 
 

@@ -1,5 +1,6 @@
-"""What the package needs of its compiled module ``_binding``, on the CPU: each
-case in a process of its own, as a module is imported once."""
+"""The build's staleness test, and what the package needs of its compiled module
+``_binding`` (each case in a process of its own, as a module is imported once);
+on the CPU."""
 import os
 import subprocess
 import sys
@@ -45,3 +46,19 @@ def test_package_without_its_compiled_module(setup, says):
 
 def test_compiled_module_is_of_this_torch():
     assert fa._ops._binding.TORCH_VERSION == torch.__version__
+
+
+def test_build_is_stale_for_another_torch_or_python(monkeypatch, tmp_path):
+    from masked_flash_attention_gb300 import build as B
+    assert B.torch_version() == torch.__version__
+    assert not B.stale()  # (the tests' own start has built)
+    with monkeypatch.context() as m:
+        m.setattr(B, "torch_version", lambda: "1.0")
+        assert B.stale()
+    with monkeypatch.context() as m:
+        m.setattr(B.sysconfig, "get_config_var", lambda name: "cpython-30")
+        assert B.stale()
+    with monkeypatch.context() as m:
+        m.setattr(B, "BUILT_FOR", str(tmp_path / "none.txt"))
+        assert B.stale()
+    assert not B.stale()
