@@ -238,7 +238,8 @@ struct ChunkArgs {
     scale = c.f32(12, true);
     causal = c.truth(13);
     c.opts.max_seqlen_q = c.i32(14, true);
-    c.opts.max_seqlen_k = c.i32(15, true);
+    if (c.args[15] == Py_None) throw Refused();
+    c.opts.max_seqlen_k = c.i32(15);
     c.opts.debug_flags = (uint32_t)c.i32(16);
   }
   int plan(const Call& c, fa_plan* pl) const {

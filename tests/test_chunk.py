@@ -147,3 +147,10 @@ def test_binding_refuses_none_for_numbers():
     with pytest.raises(TypeError):
         plan(softcap=None)
     assert plan(window_left=2**40)[0] == E
+
+
+def test_max_seqlen_k_is_required():
+    """Left out it stood for 0, so that every sequence with keys was recorded as out of bounds on the device."""
+    assert plan(max_seqlen_k=None)[0] == E and plan(lens=i32(2), max_seqlen_k=None, cu_seqlens_q=i32(3))[0] == E
+    assert fa.fa_fwd_chunk_plan(T(2, 3, 8, 64), T(2, 40, 2, 64), T(2, 40, 2, 64), i32(2))[0] == E
+    assert plan(max_seqlen_k=0)[0] == 0  # no sequence has a key
