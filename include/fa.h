@@ -386,7 +386,7 @@ typedef struct {
 /* Host-only: the rot/2 frequencies (radians per position) of a rotary
  * embedding with this base (> 1; > 0 and != 1 is not enough), and the mscale
  * that goes with them, written to host memory.  scaling NULL = PLAIN.  NTK
- * needs rot > 2. */
+ * needs rot > 2 and a scaled base that fp64 holds. */
 int fa_rope_inv_freq(int32_t rot, double base, const fa_rope_scaling* scaling, double* inv_freq, float* mscale);
 
 /* Append to a KV cache, with the rotation applied on the way: for row i of

@@ -61,12 +61,15 @@ def fa_rope_inv_freq(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
     high=32).  Host only; raises FaError on arguments that make no sense."""
     if scaling is not None and scaling not in _SCALINGS:
         raise FaError(FA_ERR_INVALID_ARG, f"fa_rope_inv_freq (scaling {scaling!r})")
+    rot, original_len = int(rot), int(original_len)
+    if not (-2**31 <= rot < 2**31 and -2**31 <= original_len < 2**31):  # (ctypes would wrap them)
+        raise FaError(FA_ERR_INVALID_ARG, "fa_rope_inv_freq")
     sc = None
     if scaling is not None:
-        sc = fa_rope_scaling(_SCALINGS[scaling], int(original_len), float(factor), float(low), float(high))
-    out = (ctypes.c_double * max(1, int(rot) // 2))()
+        sc = fa_rope_scaling(_SCALINGS[scaling], original_len, float(factor), float(low), float(high))
+    out = (ctypes.c_double * max(1, rot // 2))()
     m = ctypes.c_float(1.0)
-    rc = lib.fa_rope_inv_freq(int(rot), float(base), _ref(sc), out, ctypes.byref(m))
+    rc = lib.fa_rope_inv_freq(rot, float(base), _ref(sc), out, ctypes.byref(m))
     if rc != FA_OK:
         raise FaError(rc, "fa_rope_inv_freq")
     return torch.tensor(list(out), dtype=torch.float64), m.value

@@ -515,6 +515,7 @@ int fa_rope_inv_freq(int32_t rot, double base, const fa_rope_scaling* scaling, d
                 !std::isfinite(scaling->high)))
     return FA_ERR_INVALID_ARG;
   if (kind == FA_ROPE_NTK) base *= std::pow(scaling->factor, (double)rot / (rot - 2));
+  if (!std::isfinite(base)) return FA_ERR_INVALID_ARG;
   *mscale = 1.0f;
   // YaRN: pair index (real) whose frequency makes n turns in original_len
   // positions, original_len * base^(-2i/rot) = 2 pi n

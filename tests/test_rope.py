@@ -215,3 +215,13 @@ def test_bindings_refuse_host_tensors():
         fa.fa_rope(q, inv_freq=f)
     with pytest.raises(fa.FaError):
         fa.fa_kvcache_append(q, q, q, q, T(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kw", [dict(rot=64, scaling="yarn", factor=2.0, original_len=2**32 + 8192, high=32.0),
+                                dict(rot=64, scaling="blend", factor=2.0, original_len=2**31),
+                                dict(rot=4, scaling="ntk", factor=1e200), dict(rot=2**32 + 64), dict(rot=-2**32 + 64)])
+def test_frequency_arguments_past_their_range(kw):
+    """Whole numbers past 32 bits wrapped, and a base past fp64 gave frequencies of zero."""
+    with pytest.raises(fa.FaError) as e:
+        fa.fa_rope_inv_freq(**kw)
+    assert e.value.status == E
