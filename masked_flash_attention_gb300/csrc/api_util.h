@@ -60,6 +60,24 @@ inline int check_device() {
   return c == 1 ? FA_OK : FA_ERR_NO_DEVICE;
 }
 
+// SMs of the current device (152 on GB300, which a plan without a device assumes).
+inline int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 152;
+  }
+  const int n = cached[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+    cudaGetLastError();
+    return 152;
+  }
+  cached[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
 // NVTX range around the host-side enqueue of one stage (a profiler's trace
 // shows it beside the stage's kernels); none while g_trace_ranges is off.
 struct TraceRange {

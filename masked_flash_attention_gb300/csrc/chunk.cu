@@ -360,23 +360,6 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   }
 }
 
-int sm_count() {
-  static std::atomic<int> cached[64];
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return 152;
-  }
-  const int n = cached[dev].load(std::memory_order_relaxed);
-  if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
-    cudaGetLastError();
-    return 152;
-  }
-  cached[dev].store(v, std::memory_order_relaxed);
-  return v;
-}
-
 // Arguments checked, geometry and workspace laid out (offsets from `base`,
 // which may be null for a plan).
 int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_tensor* out, const fa_tensor* lse,
@@ -570,7 +553,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
 template <int D, bool F16>
 cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
   const int64_t rows = (int64_t)p.max_slots / 2 * kChunkRows;
-  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(rows / (1024 / D), 152 * 8));
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(rows / (1024 / D), sm_count() * 8));
   return launch_overlapped(chunk_join_kernel<D, F16>, blocks, 256, 0, overlap, st, p);
 }
 

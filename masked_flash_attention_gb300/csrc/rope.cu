@@ -368,14 +368,14 @@ int launch_rope(RopeParams& p, int d, bool f16, bool interleaved, const fa_opts*
   // Tokens per CTA: the fewest that one wave of CTAs takes, at most eight.  With
   // one, the heads go over the grid's second dimension too, so that a thread has
   // one head (1050 tokens in two waves of one each took 9.1 us, in one of four 4.7).
-  const int slots = kRopeThreads / (d / 16);
+  const int slots = kRopeThreads / (d / 16), sms = sm_count();
   p.tb = 1;
-  while (p.tb < kMaxTokens && p.rows > (int64_t)152 * kRopeBlocks * p.tb) p.tb *= 2;
+  while (p.tb < kMaxTokens && p.rows > (int64_t)sms * kRopeBlocks * p.tb) p.tb *= 2;
   const int64_t blocks = (p.rows + p.tb - 1) / p.tb;
   int ysplit = 1;
   if (p.tb == 1) {
     const int most = (p.heads + slots - 1) / slots;
-    ysplit = blocks * most <= 8 * 152 ? most : 1;
+    ysplit = blocks * most <= 8 * sms ? most : 1;
   }
   if (e == cudaSuccess && (blocks > 0 || p.n_seq > 0)) {
     const dim3 grid((unsigned)(blocks > 0 ? blocks : 1), (unsigned)ysplit);
