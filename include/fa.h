@@ -85,6 +85,8 @@
 extern "C" {
 #endif
 
+/* Changes with a structure or a prototype.  A function that is added leaves it:
+ * a library without one is told by the missing name. */
 #define FA_ABI_VERSION 8
 
 typedef enum {
@@ -129,10 +131,10 @@ typedef struct {
 
 /* Debug flags (opts->debug_flags). */
 #define FA_DEBUG_NO_SKIP 0x1u /* schedule EMPTY tiles too (as PARTIAL): exercises the -inf guard */
-#define FA_DEBUG_WITHHOLD 0x2u /* test only: the prefill kernel's key producer withholds each CTA's first
-                                * key tile (unmasked or dense-mask variants), so that the waits behind it
-                                * give up after their bound (FA_ERR_DEVICE_TIMEOUT); the output is then
-                                * undefined */
+#define FA_DEBUG_WITHHOLD 0x2u /* test only: the key producer of the prefill kernel (unmasked or dense-mask
+                                * variants) and of fa_fwd_chunk's withholds each CTA's first key tile, so
+                                * that the waits behind it give up after their bound
+                                * (FA_ERR_DEVICE_TIMEOUT); the output is then undefined */
 #define FA_DEBUG_VALIDATE 0x4u /* check mask values on the device: a dense mask must be finite or -inf,
                                 * top-k scores finite (FA_ERR_DEVICE_VALUE otherwise); off by default */
 
@@ -146,7 +148,10 @@ typedef struct {
   int32_t reserved;
   /* Optional cudaEvent_t handles (NULL = none), recorded on `stream` right
    * before the main attention kernel is enqueued and right after its last
-   * pass (split combine included): lets a caller time that kernel alone. */
+   * pass (split combine included): lets a caller time that kernel alone.
+   * fa_fwd_chunk: event_begin comes after its planner, which event_begin ..
+   * event_end leaves out; and event_begin or event_attn_end keeps its kernels
+   * from overlapping, so that a timed call takes longer than one without. */
   void* event_begin;
   void* event_end;
   /* Optional ALiBi slopes (NULL = none): device pointer to Hq fp32 values,
@@ -162,8 +167,8 @@ typedef struct {
   /* Optional cudaEvent_t (NULL = none), recorded on `stream` right after the
    * main attention kernel itself, before the split combine pass of the
    * decode path (for the prefill path, at the same point as event_end):
-   * with event_begin it times the attention kernel alone.  fa_fwd and
-   * fa_fwd_kvcache only. */
+   * with event_begin it times the attention kernel alone.  fa_fwd,
+   * fa_fwd_kvcache and fa_fwd_chunk (before its join) only. */
   void* event_attn_end;
 } fa_opts;
 

@@ -16,10 +16,10 @@
 // in registers and walks the token's heads, two of them in flight; four CTAs per
 // SM hide each other's starts (three with four heads in flight were 4 % slower,
 // six spill).  Measured (copy rate 6792 GB/s): q and k of 8192 tokens, 32 / 8
-// heads, d = 128, in a graph 29.8 us, 0.83 of the copy rate; of 65536 tokens 196
+// heads, d = 128, in a graph 29.5 us, 0.84 of the copy rate; of 65536 tokens 196
 // us, 1.01 (201, 0.98, after an L2 flush); 16384 tokens appended with q 67.2 us,
-// 0.88; one token 3.1 us.  Pairs whose
-// columns no 16-byte load holds (kHalfOdd) run at 0.45.
+// 0.88; one token 3.2 us.  Pairs whose
+// columns no 16-byte load holds (kHalfOdd) run at 0.46.
 #include <climits>
 #include <cmath>
 #include <cstring>
