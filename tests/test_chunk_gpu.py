@@ -531,3 +531,20 @@ def test_soft_caps_far_above_the_logits(d, dtype, q_lens):
     # logits of a standard deviation of 34; x is off by 34 times as much, and by up to 2e-6 |x| < 1e-3 from tanh
     for cap in (130.0, 500.0):
         check(c, f"cap {cap}", logits=34.0, softcap=cap, scale=3.0)
+
+
+@pytest.mark.parametrize("q_len,kv,d,dtype", [(1, 1500, 128, BF), (1, 2500, 64, H), (40, 1100, 64, BF), (40, 1100, 128, H)])
+def test_many_units_with_a_short_last_round(q_len, kv, d, dtype):
+    """More row tiles than the planner keeps in shared memory, whose last round would leave most of the grid idle: its
+    units are cut in five to fill it, the others stay whole.  The shortest units of 1100 keys and more have 9 key
+    tiles, and a fifth of them saves 7.2, more than a partial and a join cost (5.5); those of 700 have 6, which save
+    4.8 and are not cut."""
+    n = 152 * 10 + 30
+    rng = np.random.default_rng(5)
+    lens = rng.integers(kv - 400, kv, n).tolist()
+    c = case(600, [q_len] * n, lens, hq=1, hkv=1, d=d, dtype=dtype, page=64)
+    out, lse, ws = run(c)
+    pieces, slots, splits, tiles = ws[256:272].view(torch.int32).tolist()
+    assert tiles == n and pieces == n - splits + slots
+    assert (splits, slots) == ((30, 150) if q_len == 1 else (0, 0))
+    assert_close(out, lse, oracle(c), n_keys=kv)
