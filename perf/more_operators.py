@@ -18,7 +18,7 @@ own = False
 
 DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 E4M3 = torch.float8_e4m3fn
-LOWEST, HIGHEST = -60, 60  # exponents of the scales
+LOWEST, HIGHEST = -40, 40  # exponents of the scales
 EPS = 1e-6
 WORKSPACE = 64 << 20
 
