@@ -102,7 +102,8 @@ typedef enum {
                               * by fa_check_device_error; info = the mask tile or top-k bucket) */
 } fa_status;
 
-typedef enum { FA_DTYPE_BF16 = 1, FA_DTYPE_F32 = 2, FA_DTYPE_I32 = 3, FA_DTYPE_F16 = 4, FA_DTYPE_F64 = 5 } fa_dtype;
+typedef enum { FA_DTYPE_BF16 = 1, FA_DTYPE_F32 = 2, FA_DTYPE_I32 = 3, FA_DTYPE_F16 = 4, FA_DTYPE_F64 = 5,
+               FA_DTYPE_E4M3 = 6 } fa_dtype;
 
 /* A strided view of device memory; shape/stride are in elements, outermost
  * first; only the first ndim entries are read. */
@@ -394,6 +395,35 @@ typedef struct {
  * needs rot > 2 and a scaled base that fp64 holds. */
 int fa_rope_inv_freq(int32_t rot, double base, const fa_rope_scaling* scaling, double* inv_freq, float* mscale);
 
+/* Queries and keys normalised for each head, weighted and rotated, in one pass:
+ * with r = (mean(x^2) + eps)^(-1/2) over a head's d columns,
+ *     y = rope(weight * x * r)
+ * with rope() as for fa_rope (its mscale, layouts, positions and partial
+ * rotation; inv_freq NULL: none, and positions and mscale are ignored).
+ *   q, k, q_out, k_out, positions, inv_freq  as for fa_rope (k and k_out may be
+ *                     NULL); q_out may be q itself, else must not overlap it
+ *   q_weight, k_weight  [d], fp32 or q's element type, or NULL (ones); k_weight
+ *                     only with k
+ *   eps               > 0
+ * Sums and products are fp32 and each element is rounded once.  opts: stream and
+ * the event_begin / event_end pair are used; no workspace. */
+int fa_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_weight, const fa_tensor* k_weight,
+                    const fa_tensor* q_out, const fa_tensor* k_out, const fa_tensor* positions,
+                    const fa_tensor* inv_freq, float eps, float mscale, int32_t interleaved, const fa_opts* opts);
+
+/* Its gradients, for the same arguments: dq and dk from dq_out and dk_out (the
+ * gradients of the rotated rows), and the weights' (fp32 [d], each may be NULL;
+ * dk_weight only with k), summed over all rows and heads.  The sums are fp32 in
+ * a fixed order, their last stage fp64: the result does not depend on
+ * scheduling.  dq may be q or dq_out itself, dk likewise (same pointer and
+ * strides), else they overlap neither.  Workspace (only with a weight gradient):
+ * FA_QK_NORM_ROPE_BWD_WORKSPACE_BYTES. */
+#define FA_QK_NORM_ROPE_BWD_WORKSPACE_BYTES ((size_t)256 + ((size_t)1 << 20))
+int fa_qk_norm_rope_bwd(const fa_tensor* dq_out, const fa_tensor* dk_out, const fa_tensor* q, const fa_tensor* k,
+                        const fa_tensor* q_weight, const fa_tensor* k_weight, const fa_tensor* dq, const fa_tensor* dk,
+                        const fa_tensor* dq_weight, const fa_tensor* dk_weight, const fa_tensor* positions,
+                        const fa_tensor* inv_freq, float eps, float mscale, int32_t interleaved, const fa_opts* opts);
+
 /* Append to a KV cache, with the rotation applied on the way: for row i of
  * sequence s (q_len_s new rows, L_s = cache_seqlens[s] keys cached before), at
  * position p = positions[row] (NULL: L_s + i),
@@ -427,6 +457,58 @@ int fa_kvcache_append(const fa_tensor* q, const fa_tensor* q_out, const fa_tenso
                       const fa_tensor* cache_seqlens, const fa_tensor* block_table, const fa_tensor* positions,
                       const fa_tensor* inv_freq, float mscale, int32_t interleaved, const fa_tensor* seqlens_out,
                       const fa_opts* opts);
+
+/* A KV cache held in 8 bits: e4m3 codes, and one fp32 scale, a power of two, for
+ * each block of tokens of a page and each head, for K and V apart; an element is
+ * code * scale.
+ *   k_cache, v_cache  FA_DTYPE_E4M3 [num_pages, page_size, Hkv, d] with a block
+ *                     table, or padded [n_seq, cap, Hkv, d]; strides of multiples
+ *                     of 16 bytes, the last 1; base pointers 16-byte aligned
+ *   k_scale, v_scale  fp32 [num_pages, page_size / block, Hkv], or [n_seq, cap /
+ *                     block, Hkv], any strides.  The block is told by the shapes:
+ *                     16, 32, 64 or 128 tokens, a divisor of page_size (or cap),
+ *                     the same for K and V.  Scales lie within 2^-40 .. 2^40; of a
+ *                     scale only the exponent is read.
+ *
+ * fa_kvcache_append_q8: fa_kvcache_append into such a cache.  A block's scale is the
+ * smallest power of two whose 448-fold holds every finite element of the block
+ * (2^-40 where there is none but zeros).  Where the first new token enters a block
+ * that earlier ones have begun, the block keeps its scale, unless the new tokens
+ * need a larger one: the codes before them are then rounded again to it.  Elements
+ * are rounded to nearest even from fp32 (rotated keys are not rounded to the input
+ * type first); beyond 448 * 2^40 they saturate, and a NaN or an infinity becomes
+ * the NaN code and does not count for the scale.
+ *   q, q_out, k_new, v_new, cu_seqlens_q, cache_seqlens, block_table, positions,
+ *   inv_freq, mscale, interleaved, seqlens_out, opts  as for fa_kvcache_append
+ *   eps               > 0: the rows of q and k are normalised first, as by
+ *                     fa_qk_norm_rope with q_weight and k_weight (NULL: ones); 0:
+ *                     they are not, and the weights have to be NULL
+ * Errors of lengths and pages are recorded as for fa_kvcache_append; a page index
+ * outside the cache leaves its blocks' tokens unwritten.  Two sequences must not
+ * append to the same block, and k_scale and v_scale must not overlap. */
+int fa_kvcache_append_q8(const fa_tensor* q, const fa_tensor* q_out, const fa_tensor* k_new, const fa_tensor* v_new,
+                         const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* k_scale,
+                         const fa_tensor* v_scale, const fa_tensor* cu_seqlens_q, const fa_tensor* cache_seqlens,
+                         const fa_tensor* block_table, const fa_tensor* positions, const fa_tensor* inv_freq,
+                         float mscale, int32_t interleaved, const fa_tensor* q_weight, const fa_tensor* k_weight,
+                         float eps, const fa_tensor* seqlens_out, const fa_opts* opts);
+
+/* Keys and values read back from an 8-bit cache, in bf16 or fp16 (each product
+ * code * scale rounded once; bf16 holds all of them exactly).
+ *   k_out, v_out      [total_k, Hkv, d] with cu_seqlens_k (int32 [n_seq + 1]): key j
+ *                     of sequence s goes to row cu_seqlens_k[s] + j, and the sums tell
+ *                     how many there are; or [n_seq, S, Hkv, d] with seqlens_k (int32
+ *                     [n_seq], at most S): rows past a sequence's keys, like packed
+ *                     rows of no sequence, are left as they were
+ *   exactly one of cu_seqlens_k and seqlens_k is given
+ * A length that does not fit the cache or the output is recorded as
+ * FA_ERR_DEVICE_BOUNDS and none of that sequence's rows is written; a page index
+ * outside the cache likewise, for its rows.  opts->workspace: the error word, as for
+ * fa_kvcache_append. */
+int fa_kvcache_read_q8(const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* k_scale,
+                       const fa_tensor* v_scale, const fa_tensor* cu_seqlens_k, const fa_tensor* seqlens_k,
+                       const fa_tensor* block_table, const fa_tensor* k_out, const fa_tensor* v_out,
+                       const fa_opts* opts);
 
 /* Attention of a chunk of new tokens per sequence over a KV cache that holds
  * their keys already (fa_kvcache_append): from one token a sequence (a decoding
@@ -472,6 +554,31 @@ int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_ten
                       const fa_tensor* block_table, const fa_tensor* prefix_lens, int32_t window_left,
                       int32_t window_right, float softcap, float scale, int32_t causal, const fa_opts* opts,
                       fa_plan* plan_out);
+
+/* fa_fwd_chunk over a cache in 8 bits (above): the same logits, masks, layouts and
+ * rules, and one mask more,
+ *     window_left: key j is kept when j >= i + off - window_left, or when
+ *     j < sink_keys: the sequence's first keys stay visible to every row that
+ *     the other rules let see them
+ * (sink_keys 0: none; without a window every key is visible anyway).  Q enters the
+ * products in fp16 after a power of two per row and the codes of K and V as they are; the
+ * scales join in fp32, and the weights are fp16 against fp32 sums.
+ * Keys that the masks hide from every row of a query tile are not read: table entries
+ * that only such keys would use may hold anything.  Any strides of q, out and lse as
+ * for fa_fwd_chunk, and a cache stride may be 0.  Workspace: fa_fwd_chunk_q8_plan's. */
+int fa_fwd_chunk_q8(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* k_scale,
+                    const fa_tensor* v_scale, const fa_tensor* out, const fa_tensor* lse, const fa_tensor* cu_seqlens_q,
+                    const fa_tensor* seqlens_k, const fa_tensor* block_table, const fa_tensor* prefix_lens,
+                    int32_t sink_keys, int32_t window_left, int32_t window_right, float softcap, float scale,
+                    int32_t causal, const fa_opts* opts);
+
+/* Host-only: validate the arguments of fa_fwd_chunk_q8 and describe its plan (as
+ * fa_fwd_chunk_plan). */
+int fa_fwd_chunk_q8_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache,
+                         const fa_tensor* k_scale, const fa_tensor* v_scale, const fa_tensor* out, const fa_tensor* lse,
+                         const fa_tensor* cu_seqlens_q, const fa_tensor* seqlens_k, const fa_tensor* block_table,
+                         const fa_tensor* prefix_lens, int32_t sink_keys, int32_t window_left, int32_t window_right,
+                         float softcap, float scale, int32_t causal, const fa_opts* opts, fa_plan* plan_out);
 
 /* Backward pass: dq, dk, dv of the forward for the same arguments
  * (InfiniTrain pull request 193, "FlashAttention native backend": the

@@ -30,7 +30,13 @@ from ._lib import (  # noqa: F401
 from ._ops import (  # noqa: F401
     fa_fwd_chunk,
     fa_fwd_chunk_plan,
+    fa_fwd_chunk_q8,
+    fa_fwd_chunk_q8_plan,
     fa_kvcache_append,
+    fa_kvcache_append_q8,
+    fa_kvcache_read_q8,
+    fa_qk_norm_rope,
+    fa_qk_norm_rope_bwd,
     fa_rope,
     fa_rope_inv_freq,
 )

@@ -31,7 +31,7 @@ FA_ERR_DEVICE_BOUNDS = 6
 FA_ERR_NO_DEVICE = 7
 FA_ERR_DEVICE_VALUE = 8
 
-FA_DTYPE_BF16, FA_DTYPE_F32, FA_DTYPE_I32, FA_DTYPE_F16, FA_DTYPE_F64 = 1, 2, 3, 4, 5
+FA_DTYPE_BF16, FA_DTYPE_F32, FA_DTYPE_I32, FA_DTYPE_F16, FA_DTYPE_F64, FA_DTYPE_E4M3 = 1, 2, 3, 4, 5, 6
 FA_MASK_NONE, FA_MASK_DENSE, FA_MASK_TOPK = 0, 1, 2
 FA_DEBUG_NO_SKIP = 0x1
 FA_DEBUG_WITHHOLD = 0x2
@@ -40,9 +40,10 @@ FA_PATH_DECODE, FA_PATH_PREFILL = 1, 2
 FA_TILE_EMPTY, FA_TILE_FULL, FA_TILE_PARTIAL = 0, 1, 2
 FA_ROPE_PLAIN, FA_ROPE_LINEAR, FA_ROPE_NTK, FA_ROPE_BLEND, FA_ROPE_YARN = 0, 1, 2, 3, 4
 FA_KVCACHE_APPEND_WORKSPACE_BYTES = 256
+FA_QK_NORM_ROPE_BWD_WORKSPACE_BYTES = 256 + (1 << 20)
 
 _DTYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float32: FA_DTYPE_F32, torch.int32: FA_DTYPE_I32,
-           torch.float16: FA_DTYPE_F16, torch.float64: FA_DTYPE_F64}
+           torch.float16: FA_DTYPE_F16, torch.float64: FA_DTYPE_F64, torch.float8_e4m3fn: FA_DTYPE_E4M3}
 
 
 class fa_tensor(ctypes.Structure):
@@ -107,6 +108,25 @@ _ROPE_ARGS = [_P(fa_tensor)] * 6 + [ctypes.c_float, ctypes.c_int32, ctypes.c_int
 # block_table, positions, inv_freq, mscale, interleaved, seqlens_out, opts
 _APPEND_ARGS = [_P(fa_tensor)] * 11 + [ctypes.c_float, ctypes.c_int32, _P(fa_tensor), _P(fa_opts)]
 
+# fa_qk_norm_rope: q, k, q_weight, k_weight, q_out, k_out, positions, inv_freq, eps, mscale, interleaved, opts
+_NORM_ARGS = [_P(fa_tensor)] * 8 + [ctypes.c_float, ctypes.c_float, ctypes.c_int32, _P(fa_opts)]
+
+# fa_qk_norm_rope_bwd: dq_out, dk_out, q, k, q_weight, k_weight, dq, dk, dq_weight, dk_weight, positions,
+# inv_freq, eps, mscale, interleaved, opts
+_NORM_BWD_ARGS = [_P(fa_tensor)] * 12 + [ctypes.c_float, ctypes.c_float, ctypes.c_int32, _P(fa_opts)]
+
+# fa_kvcache_append_q8: q, q_out, k_new, v_new, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cache_seqlens,
+# block_table, positions, inv_freq, mscale, interleaved, q_weight, k_weight, eps, seqlens_out, opts
+_APPEND_Q8_ARGS = [_P(fa_tensor)] * 13 + [ctypes.c_float, ctypes.c_int32, _P(fa_tensor), _P(fa_tensor), ctypes.c_float,
+                                          _P(fa_tensor), _P(fa_opts)]
+
+# fa_kvcache_read_q8: k_cache, v_cache, k_scale, v_scale, cu_seqlens_k, seqlens_k, block_table, k_out, v_out, opts
+_READ_Q8_ARGS = [_P(fa_tensor)] * 9 + [_P(fa_opts)]
+
+# fa_fwd_chunk_q8 / fa_fwd_chunk_q8_plan: q, k_cache, v_cache, k_scale, v_scale, out, lse, cu_seqlens_q, seqlens_k,
+# block_table, prefix_lens, sink_keys, window_left, window_right, softcap, scale, causal, opts
+_CHUNK_Q8_ARGS = [_P(fa_tensor)] * 11 + [ctypes.c_int32] * 3 + [ctypes.c_float, ctypes.c_float, ctypes.c_int32, _P(fa_opts)]
+
 # fa_fwd_chunk / fa_fwd_chunk_plan: q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k,
 # block_table, prefix_lens, window_left, window_right, softcap, scale, causal, opts
 _CHUNK_ARGS = [_P(fa_tensor)] * 9 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_float,
@@ -115,7 +135,8 @@ _CHUNK_ARGS = [_P(fa_tensor)] * 9 + [ctypes.c_int32, ctypes.c_int32, ctypes.c_fl
 EXPORTS = ("fa_fwd", "fa_fwd_plan", "fa_fwd_workspace_size", "fa_fwd_kvcache", "fa_fwd_kvcache_plan",
            "fa_bwd", "fa_bwd_plan", "fa_fwd_noalloc", "fa_check_device_error", "fa_status_string",
            "fa_abi_version", "fa_fwd_debug_dump", "fa_debug_dump_bytes", "fa_rope", "fa_rope_inv_freq",
-           "fa_kvcache_append", "fa_fwd_chunk", "fa_fwd_chunk_plan")
+           "fa_kvcache_append", "fa_fwd_chunk", "fa_fwd_chunk_plan", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_kvcache_append_q8", "fa_kvcache_read_q8", "fa_fwd_chunk_q8", "fa_fwd_chunk_q8_plan")
 
 
 def _load():
@@ -168,6 +189,11 @@ def _load():
     lib.fa_fwd_chunk.restype = ctypes.c_int
     lib.fa_fwd_chunk_plan.argtypes = _CHUNK_ARGS + [_P(fa_plan)]
     lib.fa_fwd_chunk_plan.restype = ctypes.c_int
+    for name, argtypes in (("fa_qk_norm_rope", _NORM_ARGS), ("fa_qk_norm_rope_bwd", _NORM_BWD_ARGS),
+                           ("fa_kvcache_append_q8", _APPEND_Q8_ARGS), ("fa_kvcache_read_q8", _READ_Q8_ARGS),
+                           ("fa_fwd_chunk_q8", _CHUNK_Q8_ARGS), ("fa_fwd_chunk_q8_plan", _CHUNK_Q8_ARGS + [_P(fa_plan)])):
+        getattr(lib, name).argtypes = argtypes
+        getattr(lib, name).restype = ctypes.c_int
     # a library built from other headers would read these structures wrongly
     if lib.fa_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI {lib.fa_abi_version()}, this binding describes ABI {ABI_VERSION}: "

@@ -25,6 +25,7 @@
 #include "api_util.h"
 #include "chunk.h"
 #include "fa_device.cuh"
+#include "q8_device.cuh"
 
 namespace mfa {
 namespace {
@@ -68,6 +69,8 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
 // everything else and its code once, from a cold instruction cache, so it is kept
 // short: loops not unrolled, one warp-wide step where one will do (64 single
 // tokens: 5.7 us, of which 1.2 the first loads; unrolled, with 1024 threads, 7.6).
+// SINKS: key tiles by row_tile_sinks.
+template <bool SINKS>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ int4 s_seq[kSeqSmem];
   __shared__ int4 s_tile[kTileSmem];
@@ -124,7 +127,13 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     }
     const int4 q = seqs[lo];
     int kt0, n;
-    row_tile_keys(p, q, r - q.x, kt0, n);
+    if constexpr (SINKS) {
+      const SinkTiles t = row_tile_sinks(p, q, r - q.x);
+      kt0 = t.kt0;
+      n = t.count;
+    } else {
+      row_tile_keys(p, q, r - q.x, kt0, n);
+    }
     tiles[r] = make_int4(lo, r - q.x, kt0, n);
     nmax = max(nmax, n);
     work += n;
@@ -313,30 +322,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // thread.  Bound by the latency of its loads (a few L2 reads one behind the
 // other), so the rows get as many threads as there are and the first pieces'
 // rows are asked for before the weights are known.
-template <int D, bool F16>
+// ROWS: rows of a partial.
+template <int D, bool F16, int ROWS>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int kLanes = D / 4, kRows = 256 / kLanes;  // threads per row, rows per block
   constexpr int kAhead = 4;
   const int c = threadIdx.x % kLanes;
   wait_for_previous();
-  const int n_rows = p.counts->n_splits * kChunkRows;
+  const int n_rows = p.counts->n_splits * ROWS;
   for (int w = blockIdx.x * kRows + threadIdx.x / kLanes; w < n_rows; w += gridDim.x * kRows) {
-    const ChunkSplit sp = p.splits[w / kChunkRows];
-    const int row = w % kChunkRows;
+    const ChunkSplit sp = p.splits[w / ROWS];
+    const int row = w % ROWS;
     const int tok = fast_div(row, p.div_gp), i = sp.rt * p.rt_tokens + tok;
     if (tok >= p.rt_tokens || i >= chunk_qlen(p, sp.b)) continue;
-    const float* po = p.part_o + ((int64_t)sp.slot0 * kChunkRows + row) * D + 4 * c;
-    const float* pl = p.part_lse + (int64_t)sp.slot0 * kChunkRows + row;
+    const float* po = p.part_o + ((int64_t)sp.slot0 * ROWS + row) * D + 4 * c;
+    const float* pl = p.part_lse + (int64_t)sp.slot0 * ROWS + row;
     float4 v[kAhead];
     float ls[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const bool have = k < sp.n;
-      v[k] = have ? *reinterpret_cast<const float4*>(po + (int64_t)k * kChunkRows * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-      ls[k] = have ? pl[k * kChunkRows] : -INFINITY;
+      v[k] = have ? *reinterpret_cast<const float4*>(po + (int64_t)k * ROWS * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+      ls[k] = have ? pl[k * ROWS] : -INFINITY;
     }
     float mx = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
-    for (int k = kAhead; k < sp.n; ++k) mx = fmaxf(mx, pl[k * kChunkRows]);
+    for (int k = kAhead; k < sp.n; ++k) mx = fmaxf(mx, pl[k * ROWS]);
     const float ref = mx == -INFINITY ? 0.f : mx;  // no piece has a key of the row: all weights 0
     float sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     for (int k = 0; k < kAhead; ++k) add(ls[k], v[k]);
 #pragma unroll 4
     for (int k = kAhead; k < sp.n; ++k)
-      add(pl[k * kChunkRows], *reinterpret_cast<const float4*>(po + (int64_t)k * kChunkRows * D));
+      add(pl[k * ROWS], *reinterpret_cast<const float4*>(po + (int64_t)k * ROWS * D));
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int h = sp.hg * p.gp + row - tok * p.gp;
     const int64_t qrow = (p.cu_q ? p.cu_q[sp.b] : 0) + i, ob = p.cu_q ? 0 : sp.b;
@@ -360,20 +370,47 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   }
 }
 
+// A cache in 8 bits: rows of a query tile of the form for few rows (chunk_q8.cu), 16
+// or 32.  As many q-heads of a K/V head as divide them and fit in 16 rows share
+// one: where the sequences have few tokens simply the most, else the most that
+// leave at most an eighth of the rows empty.
+void plan_q8_rows(ChunkParams& p) {
+  p.gp = 1;
+  for (int g = 1; g <= p.G && g <= 16; ++g)
+    if (p.G % g == 0 && ((int64_t)p.Sq * g <= 16 || g * (16 / g) >= 14)) p.gp = g;
+  p.form = (int64_t)p.Sq * p.gp <= 16 ? 1 : 2;
+  p.part_rows = 16 * p.form;
+  p.rt_tokens = 16 * p.form / p.gp;
+  p.n_hg = p.Hq / p.gp;
+  p.narrow = 0;
+}
+
 // Arguments checked, geometry and workspace laid out (offsets from `base`,
 // which may be null for a plan).
+// q8: the scales and the visible first keys of a cache in 8 bits, null for one in q's type.
+struct Q8Cache {
+  const fa_tensor *ks, *vs;
+  int32_t sinks;
+};
 int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_tensor* out, const fa_tensor* lse,
                const fa_tensor* cu_q, const fa_tensor* seqlens_k, const fa_tensor* block_table,
                const fa_tensor* prefix, int32_t wl, int32_t wr, float softcap, float scale, int32_t causal,
-               const fa_opts* opts, ChunkParams* P, fa_plan* pub) {
+               const fa_opts* opts, const Q8Cache* q8, ChunkParams* P, fa_plan* pub) {
   if (!q || !k || !v || !out || !lse || !seqlens_k || !opts) return FA_ERR_INVALID_ARG;
   memset(P, 0, sizeof(*P));
   memset(pub, 0, sizeof(*pub));
   ChunkParams& p = *P;
   int rc;
   const int nd = cu_q ? 3 : 4;
-  if ((rc = check_bf16(q, nd)) || (rc = check_bf16(out, nd)) || (rc = check_bf16(k, 4)) || (rc = check_bf16(v, 4)))
+  if ((rc = check_bf16(q, nd)) || (rc = check_bf16(out, nd))) return rc;
+  if (q8) {
+    int64_t block = 0, v_block = 0;
+    if ((rc = check_q8(k, q8->ks, &block)) || (rc = check_q8(v, q8->vs, &v_block))) return rc;
+    if (block != v_block || q8->sinks < 0) return FA_ERR_INVALID_ARG;
+    while ((1 << p.block_shift) < block) ++p.block_shift;
+  } else if ((rc = check_bf16(k, 4)) || (rc = check_bf16(v, 4))) {
     return rc;
+  }
   int64_t n_seq, Sq;
   if (cu_q) {
     if (cu_q->ndim != 1 || cu_q->shape[0] < 1) return FA_ERR_INVALID_ARG;
@@ -401,7 +438,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   }
   for (int i = 0; i < 4; ++i)
     if (v->shape[i] != k->shape[i]) return FA_ERR_INVALID_ARG;
-  if (k->dtype != q->dtype || v->dtype != q->dtype || out->dtype != q->dtype) return FA_ERR_INVALID_ARG;
+  if (out->dtype != q->dtype || (!q8 && (k->dtype != q->dtype || v->dtype != q->dtype))) return FA_ERR_INVALID_ARG;
   if ((rc = check_i32_vec(seqlens_k, n_seq))) return rc;
   if (prefix && ((rc = check_i32_vec(prefix, n_seq)) || !causal)) return FA_ERR_INVALID_ARG;
   // ---- LSE
@@ -443,7 +480,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // TMA reads q and the cache: no stride of 0 along more than one element
   const fa_tensor* in[3] = {q, k, v};
   for (const fa_tensor* t : in)
-    for (int i = 0; i < t->ndim; ++i)
+    for (int i = 0; i < t->ndim && !q8; ++i)
       if (t->shape[i] > 1 && t->stride[i] == 0) return FA_ERR_UNSUPPORTED;
   p.k_sb = k->stride[0]; p.k_ss = k->stride[1]; p.k_sh = k->stride[2];
   p.v_sb = v->stride[0]; p.v_ss = v->stride[1]; p.v_sh = v->stride[2];
@@ -452,8 +489,18 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
     return FA_ERR_INVALID_ARG;
   if (scale <= 0.f) scale = 1.0f / std::sqrt((float)d);
   p.q = static_cast<const uint16_t*>(q->data);
-  p.k = static_cast<const uint16_t*>(k->data);
-  p.v = static_cast<const uint16_t*>(v->data);
+  if (q8) {
+    p.k8 = static_cast<const uint8_t*>(k->data);
+    p.v8 = static_cast<const uint8_t*>(v->data);
+    p.ks = static_cast<const float*>(q8->ks->data);
+    p.vs = static_cast<const float*>(q8->vs->data);
+    p.ks_sb = q8->ks->stride[0]; p.ks_ss = q8->ks->stride[1]; p.ks_sh = q8->ks->stride[2];
+    p.vs_sb = q8->vs->stride[0]; p.vs_ss = q8->vs->stride[1]; p.vs_sh = q8->vs->stride[2];
+    p.sinks = q8->sinks;
+  } else {
+    p.k = static_cast<const uint16_t*>(k->data);
+    p.v = static_cast<const uint16_t*>(v->data);
+  }
   p.o = static_cast<uint16_t*>(out->data);
   p.lse = static_cast<float*>(lse->data);
   p.kv_len = static_cast<const int32_t*>(seqlens_k->data);
@@ -486,11 +533,13 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // form that deals each key tile's keys to the tile's four quarters
   p.narrow = Sq > 0 && Sq * p.gp <= 32;
   if (p.narrow) p.rt_tokens = 32 / p.gp;
+  p.part_rows = kChunkRows;
+  if (q8) plan_q8_rows(p);
   // d = 64: two CTAs per SM overlap their units' ends, which short units need;
   // one CTA with two softmax warpgroups keeps the tensor cores fed better along
   // long ones (two and one: 8 x 512 tokens, 12 heads, over 512 keys 24.0 and 26.6
   // us, over 4096 keys 95 and 87; 64 single tokens over up to 1500 keys 44 and 48)
-  p.pair = d == 64 && Sk <= (p.narrow ? 2048 : 1024);
+  p.pair = q8 ? p.form == 1 : d == 64 && Sk <= (p.narrow ? 2048 : 1024);
   p.div_gp = make_fastdiv((uint32_t)p.gp);
   p.div_hg = make_fastdiv((uint32_t)p.n_hg);
 
@@ -533,8 +582,8 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   p.rtiles = reinterpret_cast<int4*>(take((size_t)rtiles * sizeof(int4)));
   p.pieces = reinterpret_cast<ChunkPiece*>(take((size_t)pieces * sizeof(ChunkPiece)));
   p.splits = reinterpret_cast<ChunkSplit*>(take((size_t)(slots / 2) * sizeof(ChunkSplit)));
-  p.part_lse = reinterpret_cast<float*>(take((size_t)slots * kChunkRows * 4));
-  p.part_o = reinterpret_cast<float*>(take((size_t)slots * kChunkRows * d * 4));
+  p.part_lse = reinterpret_cast<float*>(take((size_t)slots * p.part_rows * 4));
+  p.part_o = reinterpret_cast<float*>(take((size_t)slots * p.part_rows * d * 4));
 
   pub->path = FA_PATH_PREFILL;
   pub->n_seq = p.n_seq;
@@ -550,11 +599,56 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   return FA_OK;
 }
 
+template <int D, bool F16, int ROWS>
+cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.max_slots / 2 * ROWS;
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(rows / (1024 / D), sm_count() * 8));
+  return launch_overlapped(chunk_join_kernel<D, F16, ROWS>, blocks, 256, 0, overlap, st, p);
+}
 template <int D, bool F16>
 cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  const int64_t rows = (int64_t)p.max_slots / 2 * kChunkRows;
-  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(rows / (1024 / D), sm_count() * 8));
-  return launch_overlapped(chunk_join_kernel<D, F16>, blocks, 256, 0, overlap, st, p);
+  if (p.part_rows == 16) return launch_join<D, F16, 16>(p, overlap, st);
+  if (p.part_rows == 32) return launch_join<D, F16, 32>(p, overlap, st);
+  return launch_join<D, F16, kChunkRows>(p, overlap, st);
+}
+
+// The kernels of a planned call, on its stream.
+int enqueue_chunk(const ChunkParams& p, const fa_plan& pub, const fa_opts* opts, const char* range) {
+  int rc;
+  if (!opts->workspace || (reinterpret_cast<uintptr_t>(opts->workspace) % kAlign) != 0 ||
+      opts->workspace_bytes < pub.workspace_bytes)
+    return FA_ERR_WORKSPACE;
+  if ((rc = check_device()) != FA_OK) return rc;
+  TraceRange tr(range);
+  cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
+  cudaError_t e = cudaSuccess;
+  auto record = [&](void* ev) {
+    if (e == cudaSuccess && ev) e = cudaEventRecord(static_cast<cudaEvent_t>(ev), st);
+  };
+  const bool any = pub.n_items > 0;
+  // (events between the kernels would be recorded late if these overlapped)
+  const bool overlap = !opts->event_begin && !opts->event_attn_end;
+  if (any && !p.direct) {
+    if (p.sinks > 0) chunk_plan_kernel<true><<<1, kPlanThreads, 0, st>>>(p);
+    else chunk_plan_kernel<false><<<1, kPlanThreads, 0, st>>>(p);
+    e = cudaGetLastError();
+  }
+  record(opts->event_begin);
+  if (any && e == cudaSuccess) {
+    const bool with = overlap && !p.direct;
+    e = p.k8 ? launch_chunk_q8(p, with, st) : p.f16 ? launch_chunk_attn_f16(p, with, st) : launch_chunk_attn(p, with, st);
+  }
+  record(opts->event_attn_end);
+  if (any && e == cudaSuccess && p.max_slots > 0) {
+    if (p.d == 64) e = p.f16 ? launch_join<64, true>(p, overlap, st) : launch_join<64, false>(p, overlap, st);
+    else e = p.f16 ? launch_join<128, true>(p, overlap, st) : launch_join<128, false>(p, overlap, st);
+  }
+  record(opts->event_end);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
 }
 
 }  // namespace
@@ -571,38 +665,8 @@ int fa_fwd_chunk(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* 
   ChunkParams p;
   fa_plan pub;
   int rc = plan_chunk(q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens, window_left,
-                      window_right, softcap, scale, causal, opts, &p, &pub);
-  if (rc != FA_OK) return rc;
-  if (!opts->workspace || (reinterpret_cast<uintptr_t>(opts->workspace) % kAlign) != 0 ||
-      opts->workspace_bytes < pub.workspace_bytes)
-    return FA_ERR_WORKSPACE;
-  if ((rc = check_device()) != FA_OK) return rc;
-  TraceRange tr("mfa.fwd_chunk");
-  cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
-  cudaError_t e = cudaSuccess;
-  auto record = [&](void* ev) {
-    if (e == cudaSuccess && ev) e = cudaEventRecord(static_cast<cudaEvent_t>(ev), st);
-  };
-  const bool any = pub.n_items > 0;
-  // (events between the kernels would be recorded late if these overlapped)
-  const bool overlap = !opts->event_begin && !opts->event_attn_end;
-  if (any && !p.direct) {
-    chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
-    e = cudaGetLastError();
-  }
-  record(opts->event_begin);
-  if (any && e == cudaSuccess) e = p.f16 ? launch_chunk_attn_f16(p, overlap && !p.direct, st) : launch_chunk_attn(p, overlap && !p.direct, st);
-  record(opts->event_attn_end);
-  if (any && e == cudaSuccess && p.max_slots > 0) {
-    if (p.d == 64) e = p.f16 ? launch_join<64, true>(p, overlap, st) : launch_join<64, false>(p, overlap, st);
-    else e = p.f16 ? launch_join<128, true>(p, overlap, st) : launch_join<128, false>(p, overlap, st);
-  }
-  record(opts->event_end);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return FA_ERR_CUDA;
-  }
-  return FA_OK;
+                      window_right, softcap, scale, causal, opts, nullptr, &p, &pub);
+  return rc == FA_OK ? enqueue_chunk(p, pub, opts, "mfa.fwd_chunk") : rc;
 }
 
 int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* out,
@@ -613,7 +677,34 @@ int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_ten
   ChunkParams p;
   fa_plan pub;
   int rc = plan_chunk(q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens, window_left,
-                      window_right, softcap, scale, causal, opts, &p, &pub);
+                      window_right, softcap, scale, causal, opts, nullptr, &p, &pub);
+  if (rc == FA_OK && plan_out) *plan_out = pub;
+  return rc;
+}
+
+int fa_fwd_chunk_q8(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* k_scale,
+                    const fa_tensor* v_scale, const fa_tensor* out, const fa_tensor* lse, const fa_tensor* cu_seqlens_q,
+                    const fa_tensor* seqlens_k, const fa_tensor* block_table, const fa_tensor* prefix_lens,
+                    int32_t sink_keys, int32_t window_left, int32_t window_right, float softcap, float scale,
+                    int32_t causal, const fa_opts* opts) {
+  ChunkParams p;
+  fa_plan pub;
+  const Q8Cache q8 = {k_scale, v_scale, sink_keys};
+  int rc = plan_chunk(q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens, window_left,
+                      window_right, softcap, scale, causal, opts, &q8, &p, &pub);
+  return rc == FA_OK ? enqueue_chunk(p, pub, opts, "mfa.fwd_chunk_q8") : rc;
+}
+
+int fa_fwd_chunk_q8_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache,
+                         const fa_tensor* k_scale, const fa_tensor* v_scale, const fa_tensor* out, const fa_tensor* lse,
+                         const fa_tensor* cu_seqlens_q, const fa_tensor* seqlens_k, const fa_tensor* block_table,
+                         const fa_tensor* prefix_lens, int32_t sink_keys, int32_t window_left, int32_t window_right,
+                         float softcap, float scale, int32_t causal, const fa_opts* opts, fa_plan* plan_out) {
+  ChunkParams p;
+  fa_plan pub;
+  const Q8Cache q8 = {k_scale, v_scale, sink_keys};
+  int rc = plan_chunk(q, k_cache, v_cache, out, lse, cu_seqlens_q, seqlens_k, block_table, prefix_lens, window_left,
+                      window_right, softcap, scale, causal, opts, &q8, &p, &pub);
   if (rc == FA_OK && plan_out) *plan_out = pub;
   return rc;
 }

@@ -69,12 +69,21 @@ struct ChunkParams {
   const uint16_t *q, *k, *v;
   int64_t q_sb, q_ss, q_sh, k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;
   int64_t cache_rows, cache_outer;  // page_size x num_pages, or cap x n_seq
+  // a cache in 8 bits (q8_device.cuh): codes with k's and v's strides above, scales
+  const uint8_t *k8, *v8;  // null: a cache in the type of q
+  const float *ks, *vs;
+  int64_t ks_sb, ks_ss, ks_sh, vs_sb, vs_ss, vs_sh;
+  int32_t block_shift;  // tokens of a block = 2^block_shift
+  int32_t sinks;        // first keys that the window does not hide
+  int32_t part_rows;    // rows of a partial (kChunkRows, fewer for the 8-bit forms of few rows)
+  int32_t form;         // 8 bits: 16-row tiles of the form for few rows (1, 2), 0 = the tensor-core form
 };
 
 // `overlap`: the kernel may start while the one before it on the stream runs
 // (programmatic dependent launch; it waits for that one's results itself).
 cudaError_t launch_chunk_attn(const ChunkParams& p, bool overlap, cudaStream_t st);      // bf16
 cudaError_t launch_chunk_attn_f16(const ChunkParams& p, bool overlap, cudaStream_t st);  // fp16
+cudaError_t launch_chunk_q8(const ChunkParams& p, bool overlap, cudaStream_t st);  // 8-bit cache, few rows
 
 #ifdef __CUDACC__
 // Launch with or without overlap of the preceding kernel's end.
@@ -146,6 +155,27 @@ __device__ __forceinline__ void row_tile_keys(const ChunkParams& p, int4 seq, in
   if (lo0 > hi1) return;
   kt0 = lo0 / kKeysPerTile;
   count = hi1 / kKeysPerTile - kt0 + 1;
+}
+
+// The same where the first `sinks` keys stay visible: the tiles that hold them come
+// first, and tile v of the list is key tile v + (v >= first ? gap : 0).
+struct SinkTiles {
+  int kt0, count, first, gap;
+};
+__device__ __forceinline__ SinkTiles row_tile_sinks(const ChunkParams& p, int4 seq, int rt) {
+  SinkTiles t = {0, 0, 0, 0};
+  row_tile_keys(p, seq, rt, t.kt0, t.count);
+  if (p.sinks <= 0 || p.wl < 0 || (p.debug_flags & FA_DEBUG_NO_SKIP)) return t;
+  const int q_len = seq.y, kv = seq.z, off = kv - q_len;
+  const int i1 = min((rt + 1) * p.rt_tokens, q_len) - 1;
+  int lo1, hi1;
+  chunk_row_keys(p, i1, off, kv, seq.w, lo1, hi1);
+  const int last = min(p.sinks - 1, hi1);  // the last sink that some row sees
+  if (last < 0) return t;
+  const int n = last / kKeysPerTile + 1;
+  if (t.count == 0) return {0, n, 0, 0};
+  if (n >= t.kt0) return {0, max(n, t.kt0 + t.count), 0, 0};
+  return {0, n + t.count, n, t.kt0 - n};
 }
 #endif
 

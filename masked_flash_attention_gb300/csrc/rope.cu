@@ -20,16 +20,12 @@
 // us, 1.01 (201, 0.98, after an L2 flush); 16384 tokens appended with q 67.2 us,
 // 0.88; one token 3.2 us.  Pairs whose
 // columns no 16-byte load holds (kHalfOdd) run at 0.46.
-#include <climits>
 #include <cmath>
 #include <cstring>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "api_util.h"
-#include "fa_internal.h"
+#include "rope_common.cuh"
 
 using namespace mfa;
 
@@ -71,74 +67,17 @@ struct RopeParams {
   WsHeader* ws;
 };
 
-// f / (2 pi) modulo 1 in units of 2^-64: f = m * 2^(e - 63) with the 64-bit
-// mantissa m, and m * round(2^66 / (2 pi)) / 2^64 = m * 4 / (2 pi), so the
-// fraction is that product times 2^(e - 1).
-__device__ __forceinline__ uint64_t turn_step(double f) {
-  const uint64_t bits = (uint64_t)__double_as_longlong(f);
-  const int ex = (int)((bits >> 52) & 0x7ff);
-  if (ex == 0 || ex == 0x7ff) return 0;  // zero (and what is too small to turn); not finite: not accepted
-  const uint64_t m = (bits << 11) | (1ull << 63);
-  const uint64_t hi = __umul64hi(m, 0xa2f9836e4e44152aull);
-  const int sh = ex - 1023 - 1;
-  uint64_t u = 0;
-  if (sh >= 0) u = sh < 64 ? hi << sh : 0;
-  else u = -sh < 64 ? hi >> -sh : 0;
-  return (bits >> 63) ? 0 - u : u;
-}
-
-// The sequence whose rows [cu[s], cu[s + 1]) hold `row`, found by a warp: 32
-// probes a step instead of one.  -1 when there is none.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int n_seq, int64_t row, int lane) {
-  int lo = 0, hi = n_seq;  // the number of sequences that start at or before row is in (lo, hi]
-  while (hi - lo > 32) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const int c = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= row));
-    if (c == 0) return -1;
-    lo += (c - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  const int at = lo + lane;
-  const int c = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= row));
-  if (c == 0) return -1;
-  const int s = lo + c - 1;
-  return (__ldg(cu + s) <= row && row < __ldg(cu + s + 1)) ? s : -1;
-}
-
 // Append: a sequence whose rows [c0, c0 + n) or L cached keys do not fit.
 __device__ __forceinline__ bool seq_bad(const RopeParams& p, int64_t L, int64_t c0, int64_t n) {
   return L < 0 || n < 0 || c0 < 0 || c0 + n > p.rows || L + n > p.cap;
 }
 
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t u) {
-  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
-  else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (F16) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  } else {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-}
-template <bool F16>
-__device__ __forceinline__ float to_float(uint16_t u) {
-  if constexpr (F16) return __half2float(__ushort_as_half(u));
-  else return __uint_as_float((uint32_t)u << 16);
-}
-
-// Layouts of the pairs.  kHalf: columns i and i + half, half a multiple of 8,
+// Layouts of the pairs here.  kHalf: columns i and i + half, half a multiple of 8,
 // so a thread's two 16-byte pieces are the two sides of 8 pairs.
 // kInterleaved: columns 2i and 2i + 1 of 16 consecutive columns.  kHalfOdd: as
 // kHalf with any half; a thread reads its columns' partners one by one (they
 // come from L1) and the head's threads, all of one warp, meet between reads and
 // writes, so that in-place calls hold.
-enum { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
-
 template <int D, bool F16, int LAYOUT, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 16;  // threads per head
@@ -396,72 +335,11 @@ int launch_rope(RopeParams& p, int d, bool f16, bool interleaved, const fa_opts*
   return FA_OK;
 }
 
-// Strides of a [B, S, H, d] or [total, H, d] tensor.
-void strides_of(const fa_tensor* t, int64_t& sb, int64_t& ss, int64_t& sh) {
-  if (t->ndim == 3) { sb = 0; ss = t->stride[0]; sh = t->stride[1]; }
-  else { sb = t->stride[0]; ss = t->stride[1]; sh = t->stride[2]; }
-}
-
-bool same_shape(const fa_tensor* a, const fa_tensor* b) {
-  if (a->ndim != b->ndim) return false;
-  for (int i = 0; i < a->ndim; ++i)
-    if (a->shape[i] != b->shape[i]) return false;
-  return true;
-}
-
-// A written tensor holds every element once: no stride of 0 along more than
-// one element.
-bool writable(const fa_tensor* t) {
-  for (int i = 0; i < t->ndim; ++i)
-    if (t->shape[i] > 1 && t->stride[i] == 0) return false;
-  return true;
-}
-
-// x and its output: one shape and type, like `like` but for the heads.
-int check_pair(const fa_tensor* x, const fa_tensor* y, const fa_tensor* like) {
-  int rc;
-  if ((rc = check_bf16(x, like->ndim)) || (rc = check_bf16(y, like->ndim))) return rc;
-  if (x->dtype != like->dtype || y->dtype != like->dtype || !same_shape(x, y) || !writable(y))
-    return FA_ERR_INVALID_ARG;
-  for (int i = 0; i < like->ndim; ++i)
-    if (i != like->ndim - 2 && x->shape[i] != like->shape[i]) return FA_ERR_INVALID_ARG;
-  return x->shape[like->ndim - 2] < 1 ? FA_ERR_INVALID_ARG : FA_OK;
-}
-
-int check_freq(const fa_tensor* f, int64_t d, int32_t* half) {
-  if (!f->data || f->dtype != FA_DTYPE_F64 || f->ndim != 1 || f->stride[0] != 1 ||
-      (reinterpret_cast<uintptr_t>(f->data) & 7u) != 0 || f->shape[0] < 1 || 2 * f->shape[0] > d)
-    return FA_ERR_INVALID_ARG;
-  *half = (int32_t)f->shape[0];
-  return FA_OK;
-}
-
-int check_positions(const fa_tensor* t, const fa_tensor* x, RopeParams& p) {
-  const int nd = x->ndim - 2;  // [B, S] or [total]
-  if (!t->data || t->dtype != FA_DTYPE_I32 || t->ndim != nd || (reinterpret_cast<uintptr_t>(t->data) & 3u) != 0)
-    return FA_ERR_INVALID_ARG;
-  for (int i = 0; i < nd; ++i)
-    if (t->shape[i] != x->shape[i] || t->stride[i] < 0) return FA_ERR_INVALID_ARG;
-  p.positions = static_cast<const int32_t*>(t->data);
-  p.pos_sb = nd == 2 ? t->stride[0] : 0;
-  p.pos_ss = t->stride[nd - 1];
-  return FA_OK;
-}
-
 void set_rows(RopeRows& r, const fa_tensor* x, const fa_tensor* y) {
   r.in = static_cast<const uint16_t*>(x->data);
   r.out = static_cast<uint16_t*>(y->data);
   strides_of(x, r.in_sb, r.in_ss, r.in_sh);
   strides_of(y, r.out_sb, r.out_ss, r.out_sh);
-}
-
-// Rows of q-like tensor x: total, and rows per sequence of its layout.
-int check_rows(const fa_tensor* x, RopeParams& p) {
-  const int64_t B = x->ndim == 4 ? x->shape[0] : 1, S = x->shape[x->ndim - 3];
-  if (B > INT32_MAX / 64 || S > INT32_MAX / 64 || (S > 0 && B > INT32_MAX / S)) return FA_ERR_INVALID_ARG;
-  p.rows = B * S;
-  p.S = (int32_t)(S > 0 ? S : 1);
-  return FA_OK;
 }
 
 }  // namespace
