@@ -563,9 +563,11 @@ int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_ten
  * (sink_keys 0: none; without a window every key is visible anyway).  Q enters the
  * products in fp16 after a power of two per row and the codes of K and V as they are; the
  * scales join in fp32, and the weights are fp16 against fp32 sums.
- * Keys that the masks hide from every row of a query tile are not read: table entries
- * that only such keys would use may hold anything.  Any strides of q, out and lse as
- * for fa_fwd_chunk, and a cache stride may be 0.  Workspace: fa_fwd_chunk_q8_plan's. */
+ * A run of 16 keys that the masks hide from every row of a query tile is not read: table
+ * entries that only such keys would use may hold anything, as may the cache's rows past
+ * a sequence's keys.  A NaN in V reaches the rows that see its key and no others.
+ * FA_ERR_UNSUPPORTED: a stride of 0 along more than one element of k_cache or
+ * v_cache.  Workspace: fa_fwd_chunk_q8_plan's. */
 int fa_fwd_chunk_q8(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* k_scale,
                     const fa_tensor* v_scale, const fa_tensor* out, const fa_tensor* lse, const fa_tensor* cu_seqlens_q,
                     const fa_tensor* seqlens_k, const fa_tensor* block_table, const fa_tensor* prefix_lens,

@@ -370,17 +370,18 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   }
 }
 
-// A cache in 8 bits: rows of a query tile of the form for few rows (chunk_q8.cu), 16
-// or 32.  As many q-heads of a K/V head as divide them and fit in 16 rows share
-// one: where the sequences have few tokens simply the most, else the most that
-// leave at most an eighth of the rows empty.
+// A cache in 8 bits: rows of a query tile of the form for few rows (chunk_q8.cu): 8,
+// 16 or 32.  As many q-heads of a K/V head share a tile as divide them and fit:
+// where the sequences have few tokens simply the most, else the most that leave at
+// most an eighth of 32 rows empty.
 void plan_q8_rows(ChunkParams& p) {
   p.gp = 1;
-  for (int g = 1; g <= p.G && g <= 16; ++g)
-    if (p.G % g == 0 && ((int64_t)p.Sq * g <= 16 || g * (16 / g) >= 14)) p.gp = g;
-  p.form = (int64_t)p.Sq * p.gp <= 16 ? 1 : 2;
-  p.part_rows = 16 * p.form;
-  p.rt_tokens = 16 * p.form / p.gp;
+  for (int g = 1; g <= p.G && g <= 32; ++g)
+    if (p.G % g == 0 && ((int64_t)p.Sq * g <= 32 || g * (32 / g) >= 28)) p.gp = g;
+  const int64_t rows = (int64_t)p.Sq * p.gp;
+  p.form = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  p.part_rows = 8 * p.form;
+  p.rt_tokens = p.part_rows / p.gp;
   p.n_hg = p.Hq / p.gp;
   p.narrow = 0;
 }
@@ -480,7 +481,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // TMA reads q and the cache: no stride of 0 along more than one element
   const fa_tensor* in[3] = {q, k, v};
   for (const fa_tensor* t : in)
-    for (int i = 0; i < t->ndim && !q8; ++i)
+    for (int i = q8 && t == q ? t->ndim : 0; i < t->ndim; ++i)  // (with q8 the kernel reads q itself)
       if (t->shape[i] > 1 && t->stride[i] == 0) return FA_ERR_UNSUPPORTED;
   p.k_sb = k->stride[0]; p.k_ss = k->stride[1]; p.k_sh = k->stride[2];
   p.v_sb = v->stride[0]; p.v_ss = v->stride[1]; p.v_sh = v->stride[2];
@@ -539,7 +540,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // one CTA with two softmax warpgroups keeps the tensor cores fed better along
   // long ones (two and one: 8 x 512 tokens, 12 heads, over 512 keys 24.0 and 26.6
   // us, over 4096 keys 95 and 87; 64 single tokens over up to 1500 keys 44 and 48)
-  p.pair = q8 ? p.form == 1 : d == 64 && Sk <= (p.narrow ? 2048 : 1024);
+  p.pair = q8 ? p.form <= 2 : d == 64 && Sk <= (p.narrow ? 2048 : 1024);
   p.div_gp = make_fastdiv((uint32_t)p.gp);
   p.div_hg = make_fastdiv((uint32_t)p.n_hg);
 
@@ -607,6 +608,7 @@ cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
 }
 template <int D, bool F16>
 cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
+  if (p.part_rows == 8) return launch_join<D, F16, 8>(p, overlap, st);
   if (p.part_rows == 16) return launch_join<D, F16, 16>(p, overlap, st);
   if (p.part_rows == 32) return launch_join<D, F16, 32>(p, overlap, st);
   return launch_join<D, F16, kChunkRows>(p, overlap, st);

@@ -76,7 +76,7 @@ struct ChunkParams {
   int32_t block_shift;  // tokens of a block = 2^block_shift
   int32_t sinks;        // first keys that the window does not hide
   int32_t part_rows;    // rows of a partial (kChunkRows, fewer for the 8-bit forms of few rows)
-  int32_t form;         // 8 bits: 16-row tiles of the form for few rows (1, 2), 0 = the tensor-core form
+  int32_t form;         // 8 bits: 8-row tiles of the form for few rows (1, 2, 4), 0 = the tensor-core form
 };
 
 // `overlap`: the kernel may start while the one before it on the stream runs

@@ -4,16 +4,17 @@
 //
 // Bound: HBM, one byte per cached element.  A CTA runs one piece of a query tile's
 // keys (the planner of chunk.cu); of each 128-key tile its eight warps take 16 keys
-// each, and every lane copies with cp.async exactly the bytes that it will feed
-// to the matrix instructions itself, so a warp streams its keys through a private
-// ring without any barrier.  With two CTAs per SM 190 KB are in flight.
+// each.  A warp streams its keys through a ring of its own, by two TMA copies for 16
+// keys, and waits for nobody else.  With two CTAs per SM 190 KB are in flight.
 //
-// Products are m16n8k16 in fp16 with fp32 sums.  e4m3 is exact in fp16.  A row of
-// Q is scaled by a power of two into fp16 (its largest element to 2^7 .. 2^8, so
-// what fp16 rounds off is below 2^-32 of it), whatever its own type.  The order of
-// columns in a product is free as long as both sides agree, so a lane's 16-byte
-// loads of a key are its operands of four steps; for P V the bytes of two keys
-// are interleaved (two byte permutes for eight values) before they widen.
+// Products are m16n8k16 in fp16 with fp32 sums, S^T = K Q^T and O^T = V^T P^T, so that
+// the 16 rows of an operand are keys or columns and eight query rows fill the other.
+// e4m3 is exact in fp16.  A row of Q is scaled by a power of two into fp16 (its
+// largest element to 2^7 .. 2^8, so what fp16 rounds off is below 2^-32 of it),
+// whatever its own type.  The order of columns in a product is free as long as both
+// sides agree, so a lane's 16-byte loads of a key are its operands of four steps; for
+// V the bytes of two keys are interleaved (two byte permutes for eight values)
+// before they widen.
 //
 // The scales: with K's scale 2^a and V's 2^b of a key's block, the logit is
 // x = 2^a scale <q, code>, and with y = x log2 e + b the weight w = 2^(y - ref)
@@ -24,12 +25,14 @@
 // bits of those down to 2^-21 of the largest (the sum is of unrounded ones).
 // The warps' results are joined by their ref through shared memory.
 //
-// A key that the masks hide from every row of the tile is never read.  One that
-// some rows see and others do not is multiplied by a weight of 0 for these; where
-// such a key's V holds a NaN, its product is made apart, so that it reaches the
-// rows that see it and no others.
+// Sixteen keys that the masks hide from every row of the tile are never read.  A key
+// that some rows see and others do not, or one behind the sequence's end in its
+// block, is multiplied by a weight of 0; where such a key's V holds a NaN, its
+// product is made apart, so that it reaches the rows that see it and no others.
+#include <algorithm>
 #include <climits>
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -40,6 +43,7 @@
 #include "mma_sync.cuh"
 #include "q8_device.cuh"
 #include "rope_common.cuh"
+#include "tc_sm103.cuh"
 
 namespace mfa {
 
@@ -49,35 +53,34 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kTop = 7.f, kRaise = 15.f;  // log2 of the weights at the top
 
-// MT: 16-row tiles of a query tile.
-template <int D, int MT>
+// NT: 8-row tiles of a query tile.
+template <int D, int NT>
 struct QCfg {
-  static constexpr int kRows = 16 * MT;
-  static constexpr int kCtas = MT == 1 ? 2 : 1;         // per SM
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kCtas = NT <= 2 ? 2 : 1;         // per SM
   static constexpr int kStageBytes = 2 * 16 * D;        // K and V of 16 keys
-  static constexpr int kStages = (MT == 1 ? 3 : 6) * 128 / D;
+  static constexpr int kStages = (NT <= 2 ? 3 : 6) * 128 / D;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQStride = 2 * D + 16;           // bytes of a Q row
-  static constexpr int kOStride = D + 4 * (D / 32);     // floats of a row of the join
+  static constexpr int kOStride = D + 36;               // floats of a row of the join: eight runs of D / 8 + 4, and 4
   static constexpr int kQOff = kRing;
   static constexpr int kRowOff = kQOff + kRows * kQStride;           // per row: factor, keys, place, slope
   static constexpr int kSumOff = kRowOff + kRows * 5 * 4;            // ref and sum [kWarps][kRows]
-  static constexpr int kExpOff = kSumOff + kWarps * kRows * 8;       // scales' exponents [kWarps][64]
-  static constexpr int kOwnOff = kExpOff + kWarps * 64 * 4;
-  static constexpr int kSmem = kOwnOff + 32;
+  static constexpr int kInfoOff = kSumOff + kWarps * kRows * 8;      // {page, row, first key, exponents} [kWarps][64]
+  static constexpr int kBarOff = kInfoOff + kWarps * 64 * 16;         // [kWarps][kStages], abort flag
+  static constexpr int kOwnOff = kBarOff + kWarps * kStages * 8 + 16;
+  static constexpr int kGeoOff = kOwnOff + 32;  // what only the look-ups need of the piece
+  static constexpr int kSmem = kGeoOff + 48 + 1024;                  // (the ring starts on a 1024-byte boundary)
   static_assert(kWarps * kRows * kOStride * 4 <= kRing, "the join's rows take the ring's place");
   static_assert(kSmem <= (kCtas == 1 ? 227 * 1024 : 113 * 1024), "shared memory budget");
 };
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool real) {
-  const uint32_t n = real ? BYTES : 0;  // zero-filled otherwise
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// The transposed of an 8 x 8 matrix of 16-bit elements, lane (g, t) holding row g, columns 2 t and 2 t + 1.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t u) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(u));
+  return r;
 }
-
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
@@ -104,31 +107,56 @@ __device__ __forceinline__ ChunkPiece own_piece(const ChunkParams& p, int i) {
 }
 
 // GEN: soft-cap and / or ALiBi.
-template <int D, int MT, bool GEN>
-__global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(const __grid_constant__ ChunkParams p) {
-  using C = QCfg<D, MT>;
+template <int D, int NT, bool GEN>
+__global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
+    chunk_q8_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmv) {
+  using C = QCfg<D, NT>;
   constexpr int NST = C::kStages, kRows = C::kRows;
-  constexpr int NP = D / 64;                  // 16-byte pieces of a key of K per lane
-  constexpr int kVBytes = D / 8;              // bytes of a key of V per lane
-  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int NP = D / 64;  // 16-byte pieces of a key of K per lane
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   unsigned char* ring = smem + warp * NST * C::kStageBytes;
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  // where this lane's operands stand in 16 rows of D bytes, which TMA swizzles by 16-byte
+  // pieces (128- and 64-byte patterns): K's piece 4 q + t of key g, V's columns (D / 8) g
+  // of keys 2 t and 2 t + 1; eight keys later is 8 D bytes on
+  int k_at[NP], v_at[2];
+  if constexpr (D == 128) {
+    k_at[0] = g * 128 + ((t ^ g) << 4);
+    k_at[NP - 1] = g * 128 + (((4 + t) ^ g) << 4);
+    v_at[0] = 2 * t * 128 + ((g ^ (2 * t)) << 4);
+    v_at[1] = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
+  } else {
+    k_at[0] = g * 64 + ((t ^ (g >> 1)) << 4);
+    v_at[0] = 2 * t * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1);
+    v_at[1] = v_at[0] + 64;
+  }
   float* s_fac = reinterpret_cast<float*>(smem + C::kRowOff);  // logit per dot product (GEN: without scale)
   int* s_lo = reinterpret_cast<int*>(s_fac + kRows);
   int* s_hi = s_lo + kRows;
   int* s_place = s_hi + kRows;
   float* s_slope = reinterpret_cast<float*>(s_place + kRows);
   float2* s_sum = reinterpret_cast<float2*>(smem + C::kSumOff);
-  int* s_exp = reinterpret_cast<int*>(smem + C::kExpOff) + warp * 64;
+  int4* s_info = reinterpret_cast<int4*>(smem + C::kInfoOff) + warp * 64;
+  volatile int* s_geo = reinterpret_cast<volatile int*>(smem + C::kGeoOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * NST;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + kWarps * NST * 8);
   float* s_o = reinterpret_cast<float*>(smem);
   ChunkPiece* own = reinterpret_cast<ChunkPiece*>(smem + C::kOwnOff);
 
-  wait_for_previous();
-  if (p.direct) {
-    if (tid == 0) *own = own_piece(p, blockIdx.x);
-    __syncthreads();
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int k = 0; k < kWarps * NST; ++k) tc::mbar_init(reinterpret_cast<uint64_t*>(smem + C::kBarOff) + k, 1);
+    tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&tmk);
+    tc::tma_prefetch_desc(&tmv);
   }
+  wait_for_previous();
+  if (p.direct && tid == 0) *own = own_piece(p, blockIdx.x);
+  __syncthreads();
+  uint32_t phases = 0;  // parity of each stage's next full phase
+  bool withhold = p.debug_flags & FA_DEBUG_WITHHOLD;  // test only: the first copy of K is never sent
   const int n_pieces = p.direct ? 1 : p.counts->n_pieces;
 
   for (int round = 0;; ++round) {
@@ -136,20 +164,28 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
     const int at = p.direct ? round
                             : round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
     if (at >= n_pieces) break;
+    int count, all_lo, all_hi, sinks;  // all_lo .. all_hi: the keys that every row sees
+    {
     const ChunkPiece w = p.direct ? *own : p.pieces[at];
     if (w.count < 0) continue;
+    count = w.count;
     const int q_len = chunk_qlen(p, w.b), kv_len = p.kv_len[w.b], prefix = p.prefix ? p.prefix[w.b] : 0, off = kv_len - q_len;
     const int i0 = w.rt * p.rt_tokens, i1 = min(i0 + p.rt_tokens, q_len) - 1;
-    const int head0 = w.hg * p.gp, hk = head0 / p.G;
+    const int head0 = w.hg * p.gp;
     const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[w.b] : 0, qb = p.cu_q ? 0 : w.b;
-    const SinkTiles geo = row_tile_sinks(p, make_int4(0, q_len, kv_len, prefix), w.rt);
-    // the keys that some row sees: at or below need_hi, and at or above need_lo or among the first `sinks`
-    const int sinks = p.wl >= 0 ? p.sinks : 0;
-    int need_lo, need_hi, lo_, hi_;
-    chunk_row_keys(p, i0, off, kv_len, prefix, need_lo, hi_);
-    chunk_row_keys(p, i1, off, kv_len, prefix, lo_, need_hi);
+    // the keys that some row sees: at or below need_hi, and at or above need_lo or
+    // among the first `sinks` (both ends of a row's keys move right with the row)
+    sinks = p.wl >= 0 ? p.sinks : 0;
+    int need_lo, need_hi;
+    chunk_row_keys(p, i0, off, kv_len, prefix, need_lo, all_hi);
+    chunk_row_keys(p, i1, off, kv_len, prefix, all_lo, need_hi);
+    if (tid == 0) {
+      const SinkTiles geo = row_tile_sinks(p, make_int4(0, q_len, kv_len, prefix), w.rt);
+      const int v[9] = {w.kt0, w.count, geo.first, geo.gap, need_lo, need_hi, sinks, w.b, head0 / p.G};
+      for (int k = 0; k < 9; ++k) s_geo[k] = v[k];
+    }
 
-    // ---- Q: two rows per warp and 16-row tile, scaled into fp16
+    // ---- Q, scaled into fp16: a row per warp and 8-row tile
     for (int r = warp; r < kRows; r += kWarps) {
       const int tok = fast_div(r, p.div_gp), i = i0 + tok, h = head0 + r - tok * p.gp;
       const bool exists = tok < p.rt_tokens && i < q_len;
@@ -192,23 +228,23 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
         s_slope[r] = (GEN && p.alibi && exists) ? __ldg(p.alibi + h) * kLog2e : 0.f;
       }
     }
+    }
     __syncthreads();
 
-    // ---- the warp's 16 keys of tile v of the piece
+    // ---- the warp's 16 keys of each tile of the piece.  32 tiles are looked up at once,
+    // one by each lane, and the pages of the 32 after them asked for; what is found goes
+    // to shared memory (two sets: the copies run ahead of the products).
+    int next_page = -1;
     auto first_key = [&](int v) {
-      const int tile = w.kt0 + v;
-      return (tile + (tile >= geo.first ? geo.gap : 0)) * kKeysPerTile + 16 * warp;
+      const int tile = s_geo[0] + v;
+      return (tile + (tile >= s_geo[2] ? s_geo[3] : 0)) * kKeysPerTile + 16 * warp;
     };
-    auto needed = [&](int j0) { return j0 <= need_hi && (j0 + 15 >= need_lo || j0 < sinks); };
-    // The pages of 32 tiles are looked up at once, one by each lane, and those of
-    // the 32 after them asked for; the scales' exponents go to shared memory (two sets:
-    // the copies run ahead of the products).
-    int page = -1, next_page = -1;
     auto ask = [&](int v) {
       const int j0 = first_key(v);
-      if (v >= w.count || !needed(j0)) return -1;
-      if (!p.block_table) return w.b;
-      const int pg = __ldg(p.block_table + (int64_t)w.b * p.bt_stride + fast_div(j0, p.div_page));
+      // no row sees these keys
+      if (v >= s_geo[1] || j0 > s_geo[5] || (j0 + 15 < s_geo[4] && j0 >= s_geo[6])) return -1;
+      if (!p.block_table) return s_geo[7];
+      const int pg = __ldg(p.block_table + (int64_t)s_geo[7] * p.bt_stride + fast_div(j0, p.div_page));
       if (pg < 0 || pg >= p.num_pages) {
         chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)pg);
         return -1;
@@ -216,184 +252,170 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
       return pg;
     };
     auto look_up = [&](int v) {
-      page = next_page;
-      const int j0 = first_key(v + lane);
+      const int page = next_page, j0 = first_key(v + lane), h = s_geo[8];
+      const int r = p.block_table ? j0 - fast_div(j0, p.div_page) * p.page_size : j0;
       int ex = 0;
       if (page >= 0) {
-        const int r = p.block_table ? j0 - fast_div(j0, p.div_page) * p.page_size : j0;
         const int64_t b = r >> p.block_shift;
-        const int ke = scale_exponent(__ldg(p.ks + page * p.ks_sb + b * p.ks_ss + hk * p.ks_sh));
-        const int ve = scale_exponent(__ldg(p.vs + page * p.vs_sb + b * p.vs_ss + hk * p.vs_sh));
-        ex = (ke & 0xff) | ((ve & 0xff) << 8) | (1 << 16);  // (bit 16: there are keys)
+        const int ke = scale_exponent(__ldg(p.ks + page * p.ks_sb + b * p.ks_ss + h * p.ks_sh));
+        const int ve = scale_exponent(__ldg(p.vs + page * p.vs_sb + b * p.vs_ss + h * p.vs_sh));
+        ex = (ke & 0xff) | ((ve & 0xff) << 8);
       }
-      s_exp[(v + lane) & 63] = ex;
+      s_info[(v + lane) & 63] = make_int4(page, r, j0, ex);
       next_page = ask(v + 32 + lane);
       __syncwarp();
     };
     next_page = ask(lane);
     auto issue = [&](int v, int stage) {
-      if (v < w.count) {
-        if ((v & 31) == 0) look_up(v);
-        const int pg = __shfl_sync(0xffffffffu, page, v & 31);
-        if (pg >= 0) {
-          const int j0 = first_key(v);
-          const int r = p.block_table ? j0 - fast_div(j0, p.div_page) * p.page_size : j0;
-          const uint8_t* kp = p.k8 + pg * p.k_sb + r * p.k_ss + hk * p.k_sh;
-          const uint8_t* vp = p.v8 + pg * p.v_sb + r * p.v_ss + hk * p.v_sh;
-          const uint32_t dst = ring_at + stage * C::kStageBytes;
-          auto real = [&](int m) {
-            const int j = j0 + m;
-            return j <= need_hi && (j >= need_lo || j < sinks);
-          };
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int m = g + 8 * n;
-            const bool ok = real(m);
-#pragma unroll
-            for (int q = 0; q < NP; ++q)
-              copy_async<16>(dst + ((n * NP + q) * 32 + lane) * 16, ok ? kp + m * p.k_ss + 64 * q + 16 * t : p.k8, ok);
-          }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const int m = 2 * t + (n & 1) + 8 * (n >> 1);
-            const bool ok = real(m);
-            copy_async<kVBytes>(dst + 16 * D + (n * 32 + lane) * kVBytes, ok ? vp + m * p.v_ss + kVBytes * g : p.v8, ok);
-          }
+      if (v >= count) return;
+      if ((v & 31) == 0) look_up(v);
+      if (lane == 0) {
+        const int4 at = s_info[v & 63];
+        if (at.x >= 0) {
+          const int h = s_geo[8];
+          unsigned char* dst = ring + stage * C::kStageBytes;
+          tc::mbar_arrive_expect_tx(full + stage, C::kStageBytes);
+          if (!withhold) tc::tma_load_4d(dst, &tmk, full + stage, 0, h, at.y, at.x);
+          tc::tma_load_4d(dst + 16 * D, &tmv, full + stage, 0, h, at.y, at.x);
+          withhold = false;
         }
       }
-      cp_async_commit();
     };
 
-    float o[MT][D / 8][4];
-    float ref[MT][2], l[MT][2], fac[MT][2];
+    // O^T: rows 2 t + r of tile m, columns (D / 8) g + 2 i and, two on, + 1
+    float o[NT][D / 16][4];
+    float ref[NT][2], l[NT][2], fac[NT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NT; ++m) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[m][i][c] = 0.f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         ref[m][r] = -INFINITY;
         l[m][r] = 0.f;
-        fac[m][r] = s_fac[16 * m + 8 * r + g];
+        fac[m][r] = s_fac[8 * m + 2 * t + r];
       }
     }
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s) issue(s, s);
     int stage = 0;
 #pragma unroll 1
-    for (int v = 0; v < w.count; ++v) {
+    for (int v = 0; v < count; ++v) {
+      __syncwarp();  // the stage before is read
       issue(v + NST - 1, stage == 0 ? NST - 1 : stage - 1);
-      cp_async_wait<NST - 1>();
       const unsigned char* src = ring + stage * C::kStageBytes;
+      const int st = stage;
       if (++stage == NST) stage = 0;
-      const int ex = s_exp[v & 63];
-      if (!(ex >> 16)) continue;  // no row sees these keys
-      const int ke = (int)(int8_t)ex, ve = (int)(int8_t)(ex >> 8);
-      const int j0 = first_key(v);
+      const int4 info = s_info[v & 63];
+      if (info.x < 0) continue;  // no row sees these keys
+      const int ke = (int)(int8_t)info.w, ve = (int)(int8_t)(info.w >> 8), j0 = info.z;
+      if (!tc::mbar_wait(full + st, (phases >> st) & 1, abort_flag)) {
+        if (!*abort_flag) {
+          *abort_flag = 1;
+          chunk_error(p, FA_ERR_DEVICE_TIMEOUT, 1u);
+        }
+        // let the copies under way land: every stage asked for, up to a limit
+        for (int k = 0; k < NST; ++k)
+          if (v + k < count && s_info[(v + k) & 63].x >= 0)
+            tc::mbar_wait_drain(full + (st + k) % NST, (phases >> ((st + k) % NST)) & 1, 100000000ull);
+        break;
+      }
+      phases ^= 1u << st;
 
-      // ---- S = Q K^T: keys j0 + 2 t, + 1 (first tile) and + 8, + 9 (second)
-      float s[MT][2][4];
+      // ---- S^T = K Q^T: keys j0 + g (first two) and j0 + g + 8, rows 2 t and 2 t + 1
+      float s[NT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < NT; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[m][n][c] = 0.f;
+        for (int c = 0; c < 4; ++c) s[m][c] = 0.f;
 #pragma unroll
       for (int q = 0; q < NP; ++q) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(src + (q * 32 + lane) * 16);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(src + ((NP + q) * 32 + lane) * 16);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(src + k_at[q]);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(src + k_at[q] + 8 * D);
         const uint32_t kw[2][4] = {{k0.x, k0.y, k0.z, k0.w}, {k1.x, k1.y, k1.z, k1.w}};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint4 qa[MT], qc[MT];
+          uint4 qb[NT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const unsigned char* row = smem + C::kQOff + (16 * m + g) * C::kQStride + 128 * q + 32 * t + 16 * half;
-            qa[m] = *reinterpret_cast<const uint4*>(row);
-            qc[m] = *reinterpret_cast<const uint4*>(row + 8 * C::kQStride);
+          for (int m = 0; m < NT; ++m)
+            qb[m] = *reinterpret_cast<const uint4*>(smem + C::kQOff + (8 * m + g) * C::kQStride + 128 * q + 32 * t + 16 * half);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t u0 = kw[0][2 * half + e], u1 = kw[1][2 * half + e];
+            const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)u0), e4m3x2_to_f16x2((uint16_t)u1),
+                                   e4m3x2_to_f16x2((uint16_t)(u0 >> 16)), e4m3x2_to_f16x2((uint16_t)(u1 >> 16))};
+#pragma unroll
+            for (int m = 0; m < NT; ++m) mma_bf16<true>(s[m], a, e ? qb[m].z : qb[m].x, e ? qb[m].w : qb[m].y);
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t u = kw[n][2 * half + e];
-              const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)u), b1 = e4m3x2_to_f16x2((uint16_t)(u >> 16));
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                const uint32_t a[4] = {e ? qa[m].z : qa[m].x, e ? qc[m].z : qc[m].x, e ? qa[m].w : qa[m].y, e ? qc[m].w : qc[m].y};
-                mma_bf16<true>(s[m][n], a, b0, b1);
-              }
-            }
         }
       }
 
       // ---- logits in log2 units plus V's exponent, masks, the reference
       const float kf = pow2f(ke), vf = (float)ve, per_v = pow2f(-ve);
-      bool raise = false, part = false;
-      float mx[MT][2];
+      bool raise = false;
+      // some row does not see all 16 keys (the same for all lanes)
+      const bool part = j0 + 15 > all_hi || (j0 < all_lo && j0 + 15 >= sinks);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < NT; ++m)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = 16 * m + 8 * r + g;
+          const int row = 8 * m + 2 * t + r;
           const float f = fac[m][r] * kf;
+          float &x0 = s[m][r], &x1 = s[m][2 + r];
           if constexpr (GEN) {
-            const float k = 2.f * p.scale_log2 * p.inv_softcap, c1 = p.softcap * kLog2e;
-            const float slope = s_slope[row];
-            const int place = s_place[row];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float x = s[m][n][2 * r + c] * f;
-                if (p.softcap > 0.f)
-                  x = p.softcap <= kPlainSoftcap ? fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x * k)), c1) : wide_softcap(x, k, c1, p);
-                else
-                  x *= p.scale_log2;
-                if (p.alibi) x -= slope * (float)abs(place - (j0 + 8 * n + 2 * t + c));
-                s[m][n][2 * r + c] = x + vf;
+            x0 *= f;
+            x1 *= f;
+            if (p.softcap > 0.f) {
+              const float k = 2.f * p.scale_log2 * p.inv_softcap, c1 = p.softcap * kLog2e;
+              if (p.softcap <= kPlainSoftcap) {
+                x0 = fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x0 * k)), c1);
+                x1 = fmaf(-2.f * c1, fast_rcp(1.f + fast_exp2(x1 * k)), c1);
+              } else {
+                x0 = wide_softcap(x0, k, c1, p);
+                x1 = wide_softcap(x1, k, c1, p);
               }
+            } else {
+              x0 *= p.scale_log2;
+              x1 *= p.scale_log2;
+            }
+            if (p.alibi) {
+              const float slope = s_slope[row];
+              const int dist = s_place[row] - j0 - g;
+              x0 -= slope * (float)abs(dist);
+              x1 -= slope * (float)abs(dist - 8);
+            }
+            x0 += vf;
+            x1 += vf;
           } else {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) s[m][n][2 * r + c] = fmaf(s[m][n][2 * r + c], f, vf);
+            x0 = fmaf(x0, f, vf);
+            x1 = fmaf(x1, f, vf);
           }
-          const int lo = s_lo[row], hi = s_hi[row];
-          const bool cut = (lo > j0 && sinks < j0 + 16) || hi < j0 + 15;
-          part |= cut;
-          if (cut) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int j = j0 + 8 * n + 2 * t + c;
-                if (!(j <= hi && (j >= lo || j < sinks))) s[m][n][2 * r + c] = -INFINITY;
-              }
+          if (part) {
+            const int lo = s_lo[row], hi = s_hi[row], j = j0 + g;
+            if (!(j <= hi && (j >= lo || j < sinks))) x0 = -INFINITY;
+            if (!(j + 8 <= hi && (j + 8 >= lo || j + 8 < sinks))) x1 = -INFINITY;
           }
-          mx[m][r] = fmaxf(fmaxf(s[m][0][2 * r], s[m][0][2 * r + 1]), fmaxf(s[m][1][2 * r], s[m][1][2 * r + 1]));
-          raise |= mx[m][r] > ref[m][r] + kRaise;
+          raise |= fmaxf(x0, x1) > ref[m][r] + kRaise;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NT; ++m)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float top = mx[m][r];
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            float top = fmaxf(s[m][r], s[m][2 + r]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             if (top > ref[m][r] + kRaise) {
               const float up = top - kTop;
               if (ref[m][r] != -INFINITY) {
                 const float f = fast_exp2(ref[m][r] - up);
                 l[m][r] *= f;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                  o[m][i][2 * r] *= f;
-                  o[m][i][2 * r + 1] *= f;
+                for (int i = 0; i < D / 16; ++i) {
+                  o[m][i][r] *= f;
+                  o[m][i][2 + r] *= f;
                 }
               }
               ref[m][r] = up;
@@ -401,29 +423,27 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
           }
       }
 
-      // ---- weights
-      uint32_t pa[MT][4];
+      // ---- weights: P^T of keys and rows, turned to rows and keys in registers
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int m = 0; m < NT; ++m) {
+        float e[4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float base = ref[m][r] == -INFINITY ? 0.f : ref[m][r];
-          float e[4];
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) e[2 * n + c] = fast_exp2(s[m][n][2 * r + c] - base);
-          l[m][r] = fmaf((e[0] + e[1]) + (e[2] + e[3]), per_v, l[m][r]);
-          pa[m][r] = pack2<true>(e[0], e[1]);
-          pa[m][2 + r] = pack2<true>(e[2], e[3]);
+          e[r] = fast_exp2(s[m][r] - base);
+          e[2 + r] = fast_exp2(s[m][2 + r] - base);
+          l[m][r] = fmaf(e[r] + e[2 + r], per_v, l[m][r]);
         }
+        pb[m][0] = transpose_8x8(pack2<true>(e[0], e[1]));
+        pb[m][1] = transpose_8x8(pack2<true>(e[2], e[3]));
       }
 
-      // ---- O += P V: column i of lane group n is d = (D / 8) n + i
-      uint32_t vw[4][D / 32];
+      // ---- O^T += V^T P^T
+      uint32_t vw[4][D / 32];  // this lane's columns of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const unsigned char* at_v = src + 16 * D + (n * 32 + lane) * kVBytes;
+        const unsigned char* at_v = src + 16 * D + v_at[n & 1] + (n >> 1) * 8 * D;
         if constexpr (D == 128) {
           const uint4 u = *reinterpret_cast<const uint4*>(at_v);
           vw[n][0] = u.x; vw[n][1] = u.y; vw[n][2] = u.z; vw[n][3] = u.w;
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
         }
       }
       bool apart = false;
-      if (__any_sync(0xffffffffu, part)) {
+      if (part) {
         uint32_t nan = 0;
 #pragma unroll
         for (int n = 0; n < 4; ++n)
@@ -442,61 +462,53 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
         apart = __any_sync(0xffffffffu, (nan & 0x80808080u) != 0);
       }
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t x[2][2];  // [keys][columns 4 i, + 1 and + 2, + 3]
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t sel = i & 1 ? 0x7362 : 0x5140;  // columns 2 i and 2 i + 1 of two keys
+        const uint32_t x0 = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel), x1 = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
+        uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)x1),
+                         e4m3x2_to_f16x2((uint16_t)(x1 >> 16))};
+        if (apart) {
+          uint32_t is_nan[4];  // 1 where V is NaN, and V without those
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          x[n][0] = __byte_perm(vw[2 * n][i], vw[2 * n + 1][i], 0x5140);
-          x[n][1] = __byte_perm(vw[2 * n][i], vw[2 * n + 1][i], 0x7362);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(x[0][e >> 1] >> (16 * (e & 1))));
-          uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(x[1][e >> 1] >> (16 * (e & 1))));
-          if (apart) {
-            // 1 where V is NaN, and V without those
-            const uint32_t n0 = half2_bits(__hneu2(bits_half2(b0), bits_half2(b0)));
-            const uint32_t n1 = half2_bits(__hneu2(bits_half2(b1), bits_half2(b1)));
-            b0 &= ~__hneu2_mask(bits_half2(b0), bits_half2(b0));
-            b1 &= ~__hneu2_mask(bits_half2(b1), bits_half2(b1));
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              float hit[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_bf16<true>(hit, pa[m], n0, n1);
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (hit[c] > 0.f) o[m][4 * i + e][c] = __int_as_float(0x7fffffff);
-            }
+          for (int c = 0; c < 4; ++c) {
+            is_nan[c] = half2_bits(__hneu2(bits_half2(a[c]), bits_half2(a[c])));
+            a[c] &= ~__hneu2_mask(bits_half2(a[c]), bits_half2(a[c]));
           }
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma_bf16<true>(o[m][4 * i + e], pa[m], b0, b1);
+          for (int m = 0; m < NT; ++m) {
+            float hit[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16<true>(hit, is_nan, pb[m][0], pb[m][1]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (hit[c] > 0.f) o[m][i][c] = __int_as_float(0x7fffffff);
+          }
         }
+#pragma unroll
+        for (int m = 0; m < NT; ++m) mma_bf16<true>(o[m][i], a, pb[m][0], pb[m][1]);
       }
     }
 
     // ---- the warps' rows, joined
     __syncthreads();  // the ring is read
+    if (*abort_flag) break;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = 16 * m + 8 * r + g;
+        const int row = 8 * m + 2 * t + r;
         float sum = l[m][r];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (t == 0) s_sum[warp * kRows + row] = make_float2(ref[m][r], sum);
-        // this lane's columns: lane groups 2 t and 2 t + 1, D / 8 each, in runs of 32 padded by 4
-        float* dst = s_o + (warp * kRows + row) * C::kOStride;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (g == 0) s_sum[warp * kRows + row] = make_float2(ref[m][r], sum);
+        float* dst = s_o + (warp * kRows + row) * C::kOStride + (D / 8 + 4) * g;
 #pragma unroll
-          for (int i = 0; i < D / 8; i += 4) {
-            const int d = (2 * t + c) * (D / 8) + i;
-            *reinterpret_cast<float4*>(dst + d + 4 * (d / 32)) =
-                make_float4(o[m][i][2 * r + c], o[m][i + 1][2 * r + c], o[m][i + 2][2 * r + c], o[m][i + 3][2 * r + c]);
-          }
+        for (int i = 0; i < D / 16; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[m][i][r], o[m][i][2 + r], o[m][i + 1][r], o[m][i + 1][2 + r]);
       }
     __syncthreads();
+    const ChunkPiece w = p.direct ? *own : p.pieces[at];
+    const int q_len = chunk_qlen(p, w.b), i0 = w.rt * p.rt_tokens, head0 = w.hg * p.gp;
+    const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[w.b] : 0, qb = p.cu_q ? 0 : w.b;
     for (int e = tid; e < kRows * (D / 4); e += kThreads) {
       const int row = e / (D / 4), d = 4 * (e % (D / 4));
       const int tok = fast_div(row, p.div_gp), i = i0 + tok, h = head0 + row - tok * p.gp;
@@ -512,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
         if (ml.y == 0.f) continue;  // (no key seen)
         // (no reference but a sum: a NaN logit before any other)
         const float f = ml.x == -INFINITY ? ml.y : fast_exp2(ml.x - top);
-        const float4 v = *reinterpret_cast<const float4*>(s_o + (k * kRows + row) * C::kOStride + d + 4 * (d / 32));
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (k * kRows + row) * C::kOStride + d + 4 * (d / (D / 8)));
         sum = fmaf(f, ml.y, sum);
         x.x = fmaf(f, v.x, x.x); x.y = fmaf(f, v.y, x.y); x.z = fmaf(f, v.z, x.z); x.w = fmaf(f, v.w, x.w);
       }
@@ -531,27 +543,50 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, MT>::kCtas) chunk_q8_kernel(
         if (d == 0) p.lse[qb * p.lse_sb + (int64_t)h * p.lse_sh + (qbase + i) * p.lse_ss] = lse2 * kLn2;
       }
     }
-    __syncthreads();  // the next piece overwrites the rows
+    tc::fence_proxy_async_smem();  // the next piece's copies overwrite the rows
+    __syncthreads();
   }
 }
 
-template <int D, int MT, bool GEN>
-cudaError_t launch(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  using C = QCfg<D, MT>;
-  const cudaError_t e = ensure_smem_attr<chunk_q8_kernel<D, MT, GEN>>(C::kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_overlapped(chunk_q8_kernel<D, MT, GEN>, (unsigned)p.grid, kThreads, C::kSmem, overlap, st, p);
+// Tensor map of a cache's bytes {d, heads, rows, outer}, 16 rows of a head per copy.
+template <int D>
+bool encode_codes(CUtensorMap* m, const uint8_t* base, int heads, int64_t rows, int64_t outer, int64_t s_h, int64_t s_row,
+                  int64_t s_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  outer = std::max<int64_t>(outer, 1);
+  if (heads == 1) s_h = D;
+  if (outer == 1) s_outer = s_row;  // (an extent of 1 gets a harmless stride)
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[3] = {(cuuint64_t)s_h, (cuuint64_t)s_row, (cuuint64_t)s_outer};
+  cuuint32_t box[4] = {(cuuint32_t)D, 1, 16, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <int D, int MT>
+
+template <int D, int NT, bool GEN>
 cudaError_t launch(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  return (p.softcap > 0.f || p.alibi) ? launch<D, MT, true>(p, overlap, st) : launch<D, MT, false>(p, overlap, st);
+  using C = QCfg<D, NT>;
+  const cudaError_t e = ensure_smem_attr<chunk_q8_kernel<D, NT, GEN>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  if (!encode_codes<D>(&mk, p.k8, p.Hq / p.G, p.cache_rows, p.cache_outer, p.k_sh, p.k_ss, p.k_sb) ||
+      !encode_codes<D>(&mv, p.v8, p.Hq / p.G, p.cache_rows, p.cache_outer, p.v_sh, p.v_ss, p.v_sb))
+    return cudaErrorInvalidValue;
+  return launch_overlapped(chunk_q8_kernel<D, NT, GEN>, (unsigned)p.grid, kThreads, C::kSmem, overlap, st, p, mk, mv);
+}
+template <int D, int NT>
+cudaError_t launch(const ChunkParams& p, bool overlap, cudaStream_t st) {
+  return (p.softcap > 0.f || p.alibi) ? launch<D, NT, true>(p, overlap, st) : launch<D, NT, false>(p, overlap, st);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_q8(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  if (p.d == 64) return p.form == 1 ? launch<64, 1>(p, overlap, st) : launch<64, 2>(p, overlap, st);
-  return p.form == 1 ? launch<128, 1>(p, overlap, st) : launch<128, 2>(p, overlap, st);
+  if (p.d == 64) return p.form == 1 ? launch<64, 1>(p, overlap, st) : p.form == 2 ? launch<64, 2>(p, overlap, st) : launch<64, 4>(p, overlap, st);
+  return p.form == 1 ? launch<128, 1>(p, overlap, st) : p.form == 2 ? launch<128, 2>(p, overlap, st) : launch<128, 4>(p, overlap, st);
 }
 
 }  // namespace mfa
