@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmfa_gb300.so")
 BINDING = os.path.join(PKG, "_binding.so")
 BUILT_FOR = os.path.join(BUILD, "built_for.txt")
 SOURCES = ["api.cu", "sched.cu", "topk.cu", "decode.cu", "prefill_sm103.cu", "prefill_f16.cu", "backward.cu", "backward_sm103.cu", "noalloc.cu", "rope.cu", "chunk.cu", "chunk_sm103.cu",
-           "chunk_f16.cu", "qknorm.cu", "kvcache_q8.cu", "chunk_q8.cu"]
+           "chunk_f16.cu", "qknorm.cu", "kvcache_q8.cu", "chunk_q8.cu", "chunk_q8_sm103.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -370,20 +370,16 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   }
 }
 
-// A cache in 8 bits: rows of a query tile of the form for few rows (chunk_q8.cu): 8,
-// 16 or 32.  As many q-heads of a K/V head share a tile as divide them and fit:
-// where the sequences have few tokens simply the most, else the most that leave at
-// most an eighth of 32 rows empty.
+// A cache in 8 bits, and at most 32 rows (tokens x q-heads of a K/V head) in a sequence:
+// one query tile of 8, 16 or 32 rows in the form for few rows (chunk_q8.cu).
 void plan_q8_rows(ChunkParams& p) {
-  p.gp = 1;
-  for (int g = 1; g <= p.G && g <= 32; ++g)
-    if (p.G % g == 0 && ((int64_t)p.Sq * g <= 32 || g * (32 / g) >= 28)) p.gp = g;
+  if ((int64_t)p.Sq * p.G > 32) return;
+  p.gp = p.G;
   const int64_t rows = (int64_t)p.Sq * p.gp;
   p.form = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   p.part_rows = 8 * p.form;
   p.rt_tokens = p.part_rows / p.gp;
   p.n_hg = p.Hq / p.gp;
-  p.narrow = 0;
 }
 
 // Arguments checked, geometry and workspace laid out (offsets from `base`,
@@ -532,7 +528,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   p.n_hg = p.Hq / p.gp;
   // few rows in every sequence: query tiles of at most 32 rows, and the kernel
   // form that deals each key tile's keys to the tile's four quarters
-  p.narrow = Sq > 0 && Sq * p.gp <= 32;
+  p.narrow = !q8 && Sq > 0 && Sq * p.gp <= 32;
   if (p.narrow) p.rt_tokens = 32 / p.gp;
   p.part_rows = kChunkRows;
   if (q8) plan_q8_rows(p);
@@ -540,7 +536,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // one CTA with two softmax warpgroups keeps the tensor cores fed better along
   // long ones (two and one: 8 x 512 tokens, 12 heads, over 512 keys 24.0 and 26.6
   // us, over 4096 keys 95 and 87; 64 single tokens over up to 1500 keys 44 and 48)
-  p.pair = q8 ? p.form <= 2 : d == 64 && Sk <= (p.narrow ? 2048 : 1024);
+  p.pair = !q8 && d == 64 && Sk <= (p.narrow ? 2048 : 1024);
   p.div_gp = make_fastdiv((uint32_t)p.gp);
   p.div_hg = make_fastdiv((uint32_t)p.n_hg);
 
@@ -550,7 +546,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   const int64_t longest = cu_q ? std::min(Sq, p.tot_q) : Sq;
   if (rtiles * p.n_hg > (1 << 27) || (longest + p.rt_tokens - 1) / p.rt_tokens > kMaxSeqTiles) return FA_ERR_INVALID_ARG;
   const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
-  const int64_t ctas = (int64_t)sm_count() * (p.pair ? 2 : 1);
+  const int64_t ctas = (int64_t)sm_count() * (p.form ? q8_ctas(p.form) : p.pair ? 2 : 1);
   // partials: at most two rounds of the grid, and no more than all tiles alone;
   // none where no sequence has more than 8 key tiles: such units then need no
   // planner either (below).  One token over 700 keys, 6 tiles, in a graph: cut in
@@ -638,7 +634,7 @@ int enqueue_chunk(const ChunkParams& p, const fa_plan& pub, const fa_opts* opts,
   record(opts->event_begin);
   if (any && e == cudaSuccess) {
     const bool with = overlap && !p.direct;
-    e = p.k8 ? launch_chunk_q8(p, with, st) : p.f16 ? launch_chunk_attn_f16(p, with, st) : launch_chunk_attn(p, with, st);
+    e = p.form ? launch_chunk_q8(p, with, st) : p.k8 ? launch_chunk_q8_tc(p, with, st) : p.f16 ? launch_chunk_attn_f16(p, with, st) : launch_chunk_attn(p, with, st);
   }
   record(opts->event_attn_end);
   if (any && e == cudaSuccess && p.max_slots > 0) {

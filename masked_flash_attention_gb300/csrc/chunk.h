@@ -79,11 +79,15 @@ struct ChunkParams {
   int32_t form;         // 8 bits: 8-row tiles of the form for few rows (1, 2, 4), 0 = the tensor-core form
 };
 
+// CTAs per SM of the 8-bit form for few rows.
+constexpr int q8_ctas(int form) { return form <= 2 ? 2 : 1; }
+
 // `overlap`: the kernel may start while the one before it on the stream runs
 // (programmatic dependent launch; it waits for that one's results itself).
 cudaError_t launch_chunk_attn(const ChunkParams& p, bool overlap, cudaStream_t st);      // bf16
 cudaError_t launch_chunk_attn_f16(const ChunkParams& p, bool overlap, cudaStream_t st);  // fp16
-cudaError_t launch_chunk_q8(const ChunkParams& p, bool overlap, cudaStream_t st);  // 8-bit cache, few rows
+cudaError_t launch_chunk_q8(const ChunkParams& p, bool overlap, cudaStream_t st);     // 8-bit cache, few rows
+cudaError_t launch_chunk_q8_tc(const ChunkParams& p, bool overlap, cudaStream_t st);  // 8-bit cache, many rows
 
 #ifdef __CUDACC__
 // Launch with or without overlap of the preceding kernel's end.

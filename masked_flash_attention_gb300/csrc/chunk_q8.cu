@@ -29,15 +29,13 @@
 // that some rows see and others do not, or one behind the sequence's end in its
 // block, is multiplied by a weight of 0; where such a key's V holds a NaN, its
 // product is made apart, so that it reaches the rows that see it and no others.
-#include <algorithm>
 #include <climits>
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "chunk.h"
-#include "chunk_logit.cuh"
+#include "chunk_device.cuh"
 #include "fa_device.cuh"
 #include "host_util.h"
 #include "mma_sync.cuh"
@@ -51,13 +49,14 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kBatch = 16;                   // tiles that a warp looks up at once
 constexpr float kTop = 7.f, kRaise = 15.f;  // log2 of the weights at the top
 
 // NT: 8-row tiles of a query tile.
 template <int D, int NT>
 struct QCfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = NT <= 2 ? 2 : 1;         // per SM
+  static constexpr int kCtas = q8_ctas(NT);             // per SM
   static constexpr int kStageBytes = 2 * 16 * D;        // K and V of 16 keys
   static constexpr int kStages = (NT <= 2 ? 3 : 6) * 128 / D;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
@@ -66,13 +65,13 @@ struct QCfg {
   static constexpr int kQOff = kRing;
   static constexpr int kRowOff = kQOff + kRows * kQStride;           // per row: factor, keys, place, slope
   static constexpr int kSumOff = kRowOff + kRows * 5 * 4;            // ref and sum [kWarps][kRows]
-  static constexpr int kInfoOff = kSumOff + kWarps * kRows * 8;      // {page, row, first key, exponents} [kWarps][64]
-  static constexpr int kBarOff = kInfoOff + kWarps * 64 * 16;         // [kWarps][kStages], abort flag
+  static constexpr int kInfoOff = kSumOff + kWarps * kRows * 8;      // {page, row, first key, exponents} [kWarps][2 kBatch]
+  static constexpr int kBarOff = kInfoOff + kWarps * 2 * kBatch * 16;         // [kWarps][kStages], abort flag
   static constexpr int kOwnOff = kBarOff + kWarps * kStages * 8 + 16;
   static constexpr int kGeoOff = kOwnOff + 32;  // what only the look-ups need of the piece
   static constexpr int kSmem = kGeoOff + 48 + 1024;                  // (the ring starts on a 1024-byte boundary)
   static_assert(kWarps * kRows * kOStride * 4 <= kRing, "the join's rows take the ring's place");
-  static_assert(kSmem <= (kCtas == 1 ? 227 * 1024 : 113 * 1024), "shared memory budget");
+  static_assert(kSmem <= (kCtas == 1 ? 227 : 113) * 1024, "shared memory budget");
 };
 
 // The transposed of an 8 x 8 matrix of 16-bit elements, lane (g, t) holding row g, columns 2 t and 2 t + 1.
@@ -83,28 +82,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t u) {
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-
-// No planner: the piece of CTA i (count -1: the sequence has no such tile), and the check of its lengths.
-__device__ __forceinline__ ChunkPiece own_piece(const ChunkParams& p, int i) {
-  const int n_rt = (p.Sq + p.rt_tokens - 1) / p.rt_tokens;
-  ChunkPiece w;
-  w.hg = i % p.n_hg;
-  w.rt = i / p.n_hg % n_rt;
-  w.b = i / p.n_hg / n_rt;
-  w.kt0 = 0;
-  w.count = -1;
-  w.slot = -1;
-  w.pad[0] = w.pad[1] = 0;
-  int4 q = make_int4(0, 0, 0, 0);
-  if (!chunk_seq(p, w.b, q)) {
-    if (w.rt == 0 && w.hg == 0) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)w.b);
-  } else if (w.rt * p.rt_tokens < q.y) {
-    const SinkTiles t = row_tile_sinks(p, q, w.rt);
-    w.kt0 = t.kt0;
-    w.count = t.count;
-  }
-  return w;
-}
 
 // GEN: soft-cap and / or ALiBi.
 template <int D, int NT, bool GEN>
@@ -138,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
   int* s_place = s_hi + kRows;
   float* s_slope = reinterpret_cast<float*>(s_place + kRows);
   float2* s_sum = reinterpret_cast<float2*>(smem + C::kSumOff);
-  int4* s_info = reinterpret_cast<int4*>(smem + C::kInfoOff) + warp * 64;
+  int4* s_info = reinterpret_cast<int4*>(smem + C::kInfoOff) + warp * 2 * kBatch;
   volatile int* s_geo = reinterpret_cast<volatile int*>(smem + C::kGeoOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * NST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + kWarps * NST * 8);
@@ -153,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
     tc::tma_prefetch_desc(&tmv);
   }
   wait_for_previous();
-  if (p.direct && tid == 0) *own = own_piece(p, blockIdx.x);
+  if (p.direct && tid == 0) *own = q8_own_piece(p, blockIdx.x);
   __syncthreads();
   uint32_t phases = 0;  // parity of each stage's next full phase
   bool withhold = p.debug_flags & FA_DEBUG_WITHHOLD;  // test only: the first copy of K is never sent
@@ -210,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
       for (int e = 0; e < D / 32; ++e) top = fmaxf(top, fabsf(fmaf(x[e], 0.f, x[e])));  // (finite ones)
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127 - 7, -100), 120) : 0;
+      const int e = q_exponent(top);
       const float down = pow2f(-e);
       uint32_t o[D / 64];
 #pragma unroll
@@ -231,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
     }
     __syncthreads();
 
-    // ---- the warp's 16 keys of each tile of the piece.  32 tiles are looked up at once,
-    // one by each lane, and the pages of the 32 after them asked for; what is found goes
+    // ---- the warp's 16 keys of each tile of the piece.  16 tiles are looked up at once,
+    // one by each lane, and the pages of the 16 after them asked for; what is found goes
     // to shared memory (two sets: the copies run ahead of the products).
     int next_page = -1;
     auto first_key = [&](int v) {
@@ -242,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
     auto ask = [&](int v) {
       const int j0 = first_key(v);
       // no row sees these keys
-      if (v >= s_geo[1] || j0 > s_geo[5] || (j0 + 15 < s_geo[4] && j0 >= s_geo[6])) return -1;
+      if (lane >= kBatch || v >= s_geo[1] || j0 > s_geo[5] || (j0 + 15 < s_geo[4] && j0 >= s_geo[6])) return -1;
       if (!p.block_table) return s_geo[7];
       const int pg = __ldg(p.block_table + (int64_t)s_geo[7] * p.bt_stride + fast_div(j0, p.div_page));
       if (pg < 0 || pg >= p.num_pages) {
@@ -261,16 +238,16 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
         const int ve = scale_exponent(__ldg(p.vs + page * p.vs_sb + b * p.vs_ss + h * p.vs_sh));
         ex = (ke & 0xff) | ((ve & 0xff) << 8);
       }
-      s_info[(v + lane) & 63] = make_int4(page, r, j0, ex);
-      next_page = ask(v + 32 + lane);
+      if (lane < kBatch) s_info[(v + lane) % (2 * kBatch)] = make_int4(page, r, j0, ex);
+      next_page = ask(v + kBatch + lane);
       __syncwarp();
     };
     next_page = ask(lane);
     auto issue = [&](int v, int stage) {
       if (v >= count) return;
-      if ((v & 31) == 0) look_up(v);
+      if (v % kBatch == 0) look_up(v);
       if (lane == 0) {
-        const int4 at = s_info[v & 63];
+        const int4 at = s_info[v % (2 * kBatch)];
         if (at.x >= 0) {
           const int h = s_geo[8];
           unsigned char* dst = ring + stage * C::kStageBytes;
@@ -308,17 +285,17 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
       const unsigned char* src = ring + stage * C::kStageBytes;
       const int st = stage;
       if (++stage == NST) stage = 0;
-      const int4 info = s_info[v & 63];
+      const int4 info = s_info[v % (2 * kBatch)];
       if (info.x < 0) continue;  // no row sees these keys
       const int ke = (int)(int8_t)info.w, ve = (int)(int8_t)(info.w >> 8), j0 = info.z;
-      if (!tc::mbar_wait(full + st, (phases >> st) & 1, abort_flag)) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(full + st, (phases >> st) & 1, abort_flag))) {  // (the warp stays together)
         if (!*abort_flag) {
           *abort_flag = 1;
           chunk_error(p, FA_ERR_DEVICE_TIMEOUT, 1u);
         }
         // let the copies under way land: every stage asked for, up to a limit
         for (int k = 0; k < NST; ++k)
-          if (v + k < count && s_info[(v + k) & 63].x >= 0)
+          if (v + k < count && s_info[(v + k) % (2 * kBatch)].x >= 0)
             tc::mbar_wait_drain(full + (st + k) % NST, (phases >> ((st + k) % NST)) & 1, 100000000ull);
         break;
       }
@@ -548,32 +525,15 @@ __global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
   }
 }
 
-// Tensor map of a cache's bytes {d, heads, rows, outer}, 16 rows of a head per copy.
-template <int D>
-bool encode_codes(CUtensorMap* m, const uint8_t* base, int heads, int64_t rows, int64_t outer, int64_t s_h, int64_t s_row,
-                  int64_t s_outer) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  outer = std::max<int64_t>(outer, 1);
-  if (heads == 1) s_h = D;
-  if (outer == 1) s_outer = s_row;  // (an extent of 1 gets a harmless stride)
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)outer};
-  cuuint64_t strides[3] = {(cuuint64_t)s_h, (cuuint64_t)s_row, (cuuint64_t)s_outer};
-  cuuint32_t box[4] = {(cuuint32_t)D, 1, 16, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int NT, bool GEN>
 cudaError_t launch(const ChunkParams& p, bool overlap, cudaStream_t st) {
   using C = QCfg<D, NT>;
   const cudaError_t e = ensure_smem_attr<chunk_q8_kernel<D, NT, GEN>>(C::kSmem);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
-  if (!encode_codes<D>(&mk, p.k8, p.Hq / p.G, p.cache_rows, p.cache_outer, p.k_sh, p.k_ss, p.k_sb) ||
-      !encode_codes<D>(&mv, p.v8, p.Hq / p.G, p.cache_rows, p.cache_outer, p.v_sh, p.v_ss, p.v_sb))
+  const CUtensorMapSwizzle swz = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!encode_codes(&mk, p.k8, D, p.Hq / p.G, p.cache_rows, p.cache_outer, p.k_sh, p.k_ss, p.k_sb, 16, swz) ||
+      !encode_codes(&mv, p.v8, D, p.Hq / p.G, p.cache_rows, p.cache_outer, p.v_sh, p.v_ss, p.v_sb, 16, swz))
     return cudaErrorInvalidValue;
   return launch_overlapped(chunk_q8_kernel<D, NT, GEN>, (unsigned)p.grid, kThreads, C::kSmem, overlap, st, p, mk, mv);
 }

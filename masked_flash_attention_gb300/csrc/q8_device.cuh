@@ -8,12 +8,15 @@
 // attention's ratios of them stay well inside fp32.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "api_util.h"
+#include "host_util.h"
 
 namespace mfa {
 
@@ -34,6 +37,12 @@ __device__ __forceinline__ int block_exponent(float top) {
   const uint32_t u = __float_as_uint(top);
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
   return min(max(e, kQ8Low), kQ8High);
+}
+
+// The power of two that a row of Q is divided by on its way to fp16: its largest
+// finite element comes to 2^7 .. 2^8.
+__device__ __forceinline__ int q_exponent(float top) {
+  return top > 0.f ? min(max((int)(__float_as_uint(top) >> 23) - 127 - 7, -100), 120) : 0;
 }
 
 // Four fp32 values as e4m3 bytes, rounded to nearest even, saturated (NaN stays NaN).
@@ -73,6 +82,23 @@ inline int check_q8(const fa_tensor* c, const fa_tensor* s, int64_t* block) {
   if (b < kQ8MinBlock || b > kQ8MaxBlock || (b & (b - 1)) != 0) return FA_ERR_INVALID_ARG;
   *block = b;
   return FA_OK;
+}
+
+// Tensor map of a cache's codes {d, heads, rows, outer} (strides in bytes), box_rows
+// rows of a head per copy.  False when the driver rejects it or has no encoder.
+inline bool encode_codes(CUtensorMap* m, const uint8_t* base, int d, int heads, int64_t rows, int64_t outer, int64_t s_h,
+                         int64_t s_row, int64_t s_outer, int box_rows, CUtensorMapSwizzle swz) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  outer = std::max<int64_t>(outer, 1);
+  if (heads == 1) s_h = d;
+  if (outer == 1) s_outer = s_row;  // (an extent of 1 gets a harmless stride)
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[3] = {(cuuint64_t)s_h, (cuuint64_t)s_row, (cuuint64_t)s_outer};
+  cuuint32_t box[4] = {(cuuint32_t)d, 1, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace mfa
