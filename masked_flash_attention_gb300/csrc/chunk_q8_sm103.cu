@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
   if (warp == 0) {
     // ------------------------------------------------------------ codes and scales
     // Raw tiles K_0, V_0, K_1, V_1 .. through the ring: box x of a tile (its rows x *
-    // box_rows ..) is sent by lane x.  Lanes 0 .. 7 fetch the scales of the tile's
-    // groups of 16 keys.
+    // box_rows ..) is sent by lane x.  Lanes 16 .. 23 fetch the scales of the tile's
+    // groups of 16 keys.  Pages are looked up one tile ahead, and a tile's scales
+    // are stored one tile later: no load is waited for.
     if (lane == 0) {
       tc::tma_prefetch_desc(&tmk);
       tc::tma_prefetch_desc(&tmv);
@@ -222,42 +223,42 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
     int s = 0, g = 0;
     uint32_t phase = 1;
     bool ok = true, withhold = p.debug_flags & FA_DEBUG_WITHHOLD;  // test only: the first tile of K is never sent
+    const bool boxes = lane < 16;
     ChunkPiece w;
     for (int r = next_with_keys<C>(p, n_pieces, 0, w); ok && r >= 0; r = next_with_keys<C>(p, n_pieces, r + 1, w)) {
       const Geo geo = geo_of(p, w);
       const int head = w.hg * p.gp / p.G;
       const int32_t* table = p.block_table ? p.block_table + (int64_t)w.b * p.bt_stride : nullptr;
-      for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const int key = geo.first_key(i), rows = min(kKeysPerTile, geo.kv_len - key);
-        // this lane's box, and its group of 16 keys
-        const int nb = (rows + p.box_rows - 1) >> p.box_shift;
-        int row = 0, page = -1;
-        const int at = key + (lane << p.box_shift);
-        const bool want = lane < nb && at <= geo.need_hi && (at + p.box_rows > geo.need_lo || at < geo.sinks);
-        if (want) {
-          const int pi = fast_div(at, p.div_page);
-          row = at - pi * p.page_size;
-          page = table ? __ldg(table + pi) : w.b;
-        }
-        const bool good = want && page >= 0 && page < p.num_pages;
-        if (want && !good) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)page);
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, good)) * p.box_rows * (uint32_t)D;
-        if (lane < kGroups) {
-          float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
-          const int k0 = key + 16 * lane;
-          if (k0 < geo.kv_len) {
-            const int pi = fast_div(k0, p.div_page), pg = table ? __ldg(table + pi) : w.b;
-            if (pg >= 0 && pg < p.num_pages) {
-              const int64_t b = (k0 - pi * p.page_size) >> p.block_shift;
-              const int ke = scale_exponent(__ldg(p.ks + pg * p.ks_sb + b * p.ks_ss + head * p.ks_sh));
-              const int ve = scale_exponent(__ldg(p.vs + pg * p.vs_sb + b * p.vs_ss + head * p.vs_sh));
-              sc = make_float4(pow2f(ke), (float)ve, pow2f(-ve), 0.f);
-            }
-          }
-          s_sca[(g % kScaleRing) * kGroups + lane] = sc;  // (its last reader is done: the rings behind are shorter)
+      // this lane's box or group of tile i: its first key (-1: none that is seen), and its page
+      auto key_of = [&](int i) {
+        const int key = geo.first_key(i), step = boxes ? p.box_rows : 16, x = boxes ? lane : lane - 16;
+        const int at = key + x * step;
+        return (x * step < kKeysPerTile && at <= geo.need_hi && (at + step > geo.need_lo || at < geo.sinks)) ? at : -1;
+      };
+      auto page_of = [&](int at) { return at < 0 ? -1 : table ? __ldg(table + fast_div(at, p.div_page)) : w.b; };
+      int at = key_of(0), page = page_of(at);
+      float ks = 1.f, vs = 1.f;
+      auto store_scales = [&](int tile) {
+        if (!boxes && lane < 16 + kGroups) {
+          const int ve = scale_exponent(vs);
+          s_sca[(tile % kScaleRing) * kGroups + lane - 16] = make_float4(pow2f(scale_exponent(ks)), (float)ve, pow2f(-ve), 0.f);
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sc_full + g % kScaleRing);
+        if (lane == 0) tc::mbar_arrive(sc_full + tile % kScaleRing);  // (the slot's last reader is done: the rings behind are shorter)
+      };
+      for (int i = 0; ok && i < w.count; ++i, ++g) {
+        const int at_n = i + 1 < w.count ? key_of(i + 1) : -1, page_n = page_of(at_n);
+        const int row = at - fast_div(max(at, 0), p.div_page) * p.page_size;
+        const bool good = at >= 0 && page >= 0 && page < p.num_pages;
+        if (boxes && at >= 0 && !good) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)page);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, good) & 0xffffu) * p.box_rows * (uint32_t)D;
+        if (i > 0) store_scales(g - 1);
+        ks = vs = 1.f;
+        if (!boxes && good) {
+          const int64_t b = row >> p.block_shift;
+          ks = __ldg(p.ks + page * p.ks_sb + b * p.ks_ss + head * p.ks_sh);
+          vs = __ldg(p.vs + page * p.vs_sb + b * p.vs_ss + head * p.vs_sh);
+        }
         for (int v = 0; v < 2; ++v) {
           bool go = true;
           if (lane == 0) go = tc::mbar_wait(raw_empty + s, phase, abort_flag);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
           }
           if (lane == 0) tc::mbar_arrive_expect_tx(raw_full + s, bytes);
           __syncwarp();
-          if (good && !withhold)
+          if (boxes && good && !withhold)
             tc::tma_load_4d(smem + C::kRawOff + s * C::kRawBytes + lane * p.box_rows * D, v ? &tmv : &tmk, raw_full + s, 0, head, row, page);
           withhold = false;
           if (++s == NR) {
@@ -277,7 +278,10 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
             phase ^= 1;
           }
         }
+        at = at_n;
+        page = page_n;
       }
+      if (ok) store_scales(g - 1);
     }
     if (lane == 0 && *abort_flag) {
       // let the copies under way land: each stage's next full phase, up to a limit
@@ -416,28 +420,45 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
                (g < NS || tc::mbar_wait((v ? v_empty : k_empty) + s, ((g - NS) / NS) & 1, abort_flag));
           ok = __all_sync(0xffffffffu, ok);  // (the warp stays together)
           if (!ok) break;
-          // 8 codes to 16 bytes: a thread's piece is one of the row's D / 8
+          // 8 codes to 16 bytes: a thread's piece is one of the row's D / 8, in every
+          // kStep-th row, a multiple of 8: its place in the swizzle stays
           constexpr int kPieces = D / 8, kStep = 128 / kPieces;
           const int t = 32 * cw + lane, c = t % kPieces, row0 = t / kPieces;
           const unsigned char* src = smem + C::kRawOff + rs * C::kRawBytes + t * 8;
-          unsigned char* dst = smem + (v ? C::kVOff : C::kKOff) + s * C::kTileBytes + (c >> 3) * C::kHalfStep;
-          const bool check = v && part;
+          unsigned char* dst = smem + (v ? C::kVOff : C::kKOff) + s * C::kTileBytes + (c >> 3) * C::kHalfStep + row0 * 128 +
+                               (((c & 7) ^ (row0 & 7)) << 4);
+          auto widen = [](uint2 u) {
+            return make_uint4(e4m3x2_to_f16x2((uint16_t)u.x), e4m3x2_to_f16x2((uint16_t)(u.x >> 16)), e4m3x2_to_f16x2((uint16_t)u.y),
+                              e4m3x2_to_f16x2((uint16_t)(u.y >> 16)));
+          };
           uint32_t nans = 0;
-#pragma unroll 4
-          for (int n = 0; n < 128 / kStep; ++n) {
-            const int row = row0 + n * kStep;
-            const uint2 u = *reinterpret_cast<const uint2*>(src + n * 1024);
-            uint4 h = make_uint4(e4m3x2_to_f16x2((uint16_t)u.x), e4m3x2_to_f16x2((uint16_t)(u.x >> 16)), e4m3x2_to_f16x2((uint16_t)u.y),
-                                 e4m3x2_to_f16x2((uint16_t)(u.y >> 16)));
-            if (v && row >= rows) h = make_uint4(0, 0, 0, 0);
-            if (check && row < rows && (has_nan(u.x) || has_nan(u.y))) {
-              // (what stands for a key that no row sees does not count)
-              nans |= key + row <= geo.need_hi && (key + row >= geo.need_lo || key + row < geo.sinks);
-              uint32_t* x = reinterpret_cast<uint32_t*>(&h);
+          if (v == 0 || !part) {
+            // (a tile of V that every row sees whole has no row past the end)
+            constexpr int kAhead = 8;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] &= ~__hneu2_mask(*reinterpret_cast<__half2*>(x + e), *reinterpret_cast<__half2*>(x + e));
+            for (int n0 = 0; n0 < kPieces; n0 += kAhead) {
+              uint2 u[kAhead];
+#pragma unroll
+              for (int n = 0; n < kAhead; ++n) u[n] = *reinterpret_cast<const uint2*>(src + (n0 + n) * 1024);
+#pragma unroll
+              for (int n = 0; n < kAhead; ++n) *reinterpret_cast<uint4*>(dst + (n0 + n) * kStep * 128) = widen(u[n]);
             }
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = h;
+          } else {
+#pragma unroll 2
+            for (int n = 0; n < kPieces; ++n) {
+              const int row = row0 + n * kStep;
+              const uint2 u = *reinterpret_cast<const uint2*>(src + n * 1024);
+              uint4 h = widen(u);
+              if (has_nan(u.x) || has_nan(u.y)) {
+                // (what stands for a key that no row sees does not count)
+                nans |= key + row <= geo.need_hi && (key + row >= geo.need_lo || key + row < geo.sinks);
+                uint32_t* x = reinterpret_cast<uint32_t*>(&h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] &= ~__hneu2_mask(*reinterpret_cast<__half2*>(x + e), *reinterpret_cast<__half2*>(x + e));
+              }
+              if (row >= rows) h = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(dst + n * kStep * 128) = h;
+            }
           }
           if (nans) nan_piece[kk % kRowRing] = kk + 1;
           tc::fence_proxy_async_smem();
