@@ -7,11 +7,11 @@
 // cache is in 8 bits (q8_device.cuh), and three things differ:
 //  - K and V tiles come as codes, by TMA into a ring of raw tiles, and a warpgroup
 //    widens them to fp16, which is exact, into the swizzled tiles that the products
-//    read.  One conversion serves 128 rows; it costs 64 KB of writes to shared memory
-//    and 32 KB of reads per pair of tiles beside the products' 96 KB of reads, which is
-//    what bounds the kernel (128 bytes per cycle);
+//    read.  One conversion serves 128 rows.  Beside the products' operands (96 KB per
+//    pair of tiles) shared memory takes 32 KB of codes in, 32 KB out and 64 KB of fp16
+//    in, and the conversion shares the issue slots with the softmax: this is the bound;
 //  - Q enters in fp16 after a power of two per row (its largest element at 2^7 .. 2^8),
-//    loaded by the same warpgroup;
+//    written by the same warps;
 //  - the scales, one per 16 keys or more, join in the softmax: with K's scale 2^a and
 //    V's 2^b the logit in log2 units is x = 2^a f <q, code>, y = x + b, the weight
 //    w = 2^(y - ref) multiplies V's codes and the row sum adds w 2^-b.  The maximum of
@@ -23,9 +23,16 @@
 // epilogue of a marked piece looks the NaNs of the keys that each row sees up in the
 // cache.  Rows past the sequence's end are written as 0.
 //
-// Warp roles (16 warps): 0 loads codes and scales, 1 issues QK, 3 PV, 4 .. 11 softmax,
-// 12 .. 15 widen.  512 threads launch at 128 registers, split 72 / 184.  Every mbarrier
-// wait is bounded as in chunk_sm103.cu.
+// Warp roles (16 warps): 0 copies codes, 1 issues QK, 2 looks up pages and scales, 3 issues
+// PV, 4 .. 11 softmax, 12 .. 15 widen.  512 threads launch at 128 registers, split 72 / 184
+// / 72.  Every mbarrier wait is bounded as in chunk_sm103.cu.
+//
+// Measured (32 heads on 8, d 128, pages of 64 keys): 2048 tokens over 32768 keys 1255 us
+// (849 TFLOP/s; the 16-bit cache 682 us), 4 x 512 over 4096 keys 194 us, 64 x 16 over 4016
+// keys 197 us (2.8 TB/s).  With eight pieces of the conversion's loads ahead; one at a time
+// takes 334 us for the second.  A second warpgroup for the conversion (20 warps of fewer
+// registers) took 207, 256 rows to a CTA 219, codes by plain loads straight into
+// registers more than 230.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -48,18 +55,19 @@ namespace {
 
 constexpr float kTop = 7.f, kRaise = 15.f;  // log2 of the weights at the top
 constexpr int kGroups = kKeysPerTile / 16;  // keys with one scale, at least
-constexpr int kScaleRing = 16;              // tiles whose scales are held
-constexpr int kRowRing = 4;                 // pieces whose row factors are held
+constexpr int kScaleRing = 32;              // tiles whose scales are held
+constexpr int kPlaceRing = 16;              // tiles whose places in the cache are held
+constexpr int kRowRing = 8;                 // pieces whose row factors are held (Q is two ahead, S buffers three)
 
 template <int D>
 struct TCfg {
   static constexpr int kThreads = 512;
-  static constexpr int kLaunchRegs = 128, kOtherRegs = 72, kSoftmaxRegs = 184;
-  static_assert(256 * kOtherRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "the register split must fit the launch");
+  static constexpr int kLaunchRegs = 128, kOtherRegs = 72, kWidenRegs = 72, kSoftmaxRegs = 184;
+  static_assert(128 * kOtherRegs + 128 * kWidenRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "the register split must fit the launch");
   static constexpr uint32_t kCols = 512, kOCol = 384;  // TMEM: three S buffers, each overwritten by its P, and O
   static constexpr int NB = 3;
-  static constexpr int NS = D == 128 ? 2 : 4;          // widened tiles of K, and of V
-  static constexpr int NR = D == 128 ? 3 : 6;          // raw tiles of both, in turn
+  static constexpr int NS = D == 128 ? 2 : 4;          // tiles of K, and of V
+  static constexpr int NR = D == 128 ? 3 : 6;          // raw tiles of both
   static constexpr int kRawBytes = 128 * D, kTileBytes = 2 * kRawBytes;
   static constexpr int kHalfStep = 16384;  // D / 64 halves of 128 rows by 128 bytes
   static constexpr int kQOff = 0;
@@ -70,8 +78,9 @@ struct TCfg {
   static constexpr int kRefOff = kAuxOff + 1024;              // row references [2][128]
   static constexpr int kSumOff = kRefOff + 2 * 128 * 4;       // row sums [2][2][128]
   static constexpr int kFacOff = kSumOff + 2 * 2 * 128 * 4;   // row factors [kRowRing][128]
-  static constexpr int kScaOff = kFacOff + kRowRing * 128 * 4;  // {2^a, b, 2^-b, -} [kScaleRing][kGroups]
-  static constexpr int kOwnOff = kScaOff + kScaleRing * kGroups * 16;
+  static constexpr int kScaOff = kFacOff + kRowRing * 128 * 4;  // {2^a, b, 2^-b, of the tile: first key, 1 if not whole, first and last key seen, 0 ..} [kScaleRing][kGroups]
+  static constexpr int kPlaOff = kScaOff + kScaleRing * kGroups * 16;  // {page (-1: not seen), row in it} [kPlaceRing][kGroups]
+  static constexpr int kOwnOff = kPlaOff + kPlaceRing * kGroups * 8;
   static constexpr int kSmem = kOwnOff + 32 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -131,8 +140,11 @@ __device__ __forceinline__ Geo geo_of(const ChunkParams& p, const ChunkPiece& w)
   return g;
 }
 
-__device__ __forceinline__ bool has_nan(uint32_t codes) { return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
+// 0xff in the bytes that are NaN codes.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t codes) {
+  const uint32_t m = ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return m | (m - (m >> 7));
+}
 // GEN: soft-cap and / or ALiBi.
 template <int D, bool GEN>
 __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tmk,
@@ -144,7 +156,7 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kAuxOff);
   uint64_t* raw_full = bars;               // [NR] codes landed
-  uint64_t* raw_empty = raw_full + NR;     // [NR] codes widened (4 warps)
+  uint64_t* raw_empty = raw_full + NR;     // [NR] codes read (4 warps)
   uint64_t* k_full = raw_empty + NR;       // [NS] widened (4 warps)
   uint64_t* k_empty = k_full + NS;         // [NS] QK done
   uint64_t* v_full = k_empty + NS;         // [NS]
@@ -159,12 +171,15 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
   uint64_t* sumx = drained + 2;            // [1] row sums posted (256 threads)
   uint64_t* refb = sumx + 1;               // [2] row references posted (128 threads)
   uint64_t* sc_full = refb + 2;            // [kScaleRing] scales written
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + kScaleRing);
+  uint64_t* pl_full = sc_full + kScaleRing;   // [kPlaceRing] places written
+  uint64_t* pl_empty = pl_full + kPlaceRing;  // [kPlaceRing] places read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pl_empty + kPlaceRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* nan_piece = abort_flag + 1;  // [kRowRing] the busy piece whose partly seen tiles hold a NaN, + 1
-  static_assert((2 * NR + 4 * NS + kRowRing + 1 + 3 * NB + 1 + 2 + 1 + 2 + kScaleRing) * 8 + 8 + 4 * kRowRing <= 1024, "barriers");
+  static_assert((2 * NR + 4 * NS + kRowRing + 1 + 3 * NB + 1 + 2 + 1 + 2 + kScaleRing + 2 * kPlaceRing) * 8 + 8 + 4 * kRowRing <= 1024, "barriers");
   float* s_fac = reinterpret_cast<float*>(smem + C::kFacOff);
   float4* s_sca = reinterpret_cast<float4*>(smem + C::kScaOff);
+  int2* s_pla = reinterpret_cast<int2*>(smem + C::kPlaOff);
 
   if (tid == 0) {
     for (int k = 0; k < NR; ++k) {
@@ -181,19 +196,23 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
       tc::mbar_init(q_full + k, 4);
       nan_piece[k] = 0;
     }
-    tc::mbar_init(q_empty, 1);
     for (int k = 0; k < NB; ++k) {
       tc::mbar_init(s_full + k, 1);
       tc::mbar_init(p_full + k, 128);
       tc::mbar_init(p_free + k, 1);
     }
     tc::mbar_init(o_full, 1);
+    tc::mbar_init(q_empty, 1);
     for (int k = 0; k < 2; ++k) {
       tc::mbar_init(drained + k, 1);
       tc::mbar_init(refb + k, 128);
     }
     tc::mbar_init(sumx, 256);
     for (int k = 0; k < kScaleRing; ++k) tc::mbar_init(sc_full + k, 1);
+    for (int k = 0; k < kPlaceRing; ++k) {
+      tc::mbar_init(pl_full + k, 1);
+      tc::mbar_init(pl_empty + k, 1);
+    }
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
@@ -209,13 +228,14 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
   const uint32_t tbase = *tmem_slot;
   const int n_pieces = p.direct ? 1 : p.counts->n_pieces;
 
-  if (warp < 4 || warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+  // (one register limit to a branch: where two met, the compiler would take the lower)
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
   if (warp == 0) {
-    // ------------------------------------------------------------ codes and scales
-    // Raw tiles K_0, V_0, K_1, V_1 .. through the ring: box x of a tile (its rows x *
-    // box_rows ..) is sent by lane x.  Lanes 16 .. 23 fetch the scales of the tile's
-    // groups of 16 keys.  Pages are looked up one tile ahead, and a tile's scales
-    // are stored one tile later: no load is waited for.
+    // ------------------------------------------------------------ codes
+    // Raw tiles K_0, K_1, V_0, K_2, V_1 .. through the ring (V's place is free once a
+    // product of two tiles back is done, which K does not have to wait for): box x of a
+    // tile (its rows x * box_rows ..) is sent by lane x.
     if (lane == 0) {
       tc::tma_prefetch_desc(&tmk);
       tc::tma_prefetch_desc(&tmv);
@@ -223,70 +243,111 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
     int s = 0, g = 0;
     uint32_t phase = 1;
     bool ok = true, withhold = p.debug_flags & FA_DEBUG_WITHHOLD;  // test only: the first tile of K is never sent
-    const bool boxes = lane < 16;
+    const int box0 = lane << p.box_shift >> 4;                     // this lane's box: its first group of 16 keys
     ChunkPiece w;
     for (int r = next_with_keys<C>(p, n_pieces, 0, w); ok && r >= 0; r = next_with_keys<C>(p, n_pieces, r + 1, w)) {
-      const Geo geo = geo_of(p, w);
       const int head = w.hg * p.gp / p.G;
-      const int32_t* table = p.block_table ? p.block_table + (int64_t)w.b * p.bt_stride : nullptr;
-      // this lane's box or group of tile i: its first key (-1: none that is seen), and its page
-      auto key_of = [&](int i) {
-        const int key = geo.first_key(i), step = boxes ? p.box_rows : 16, x = boxes ? lane : lane - 16;
-        const int at = key + x * step;
-        return (x * step < kKeysPerTile && at <= geo.need_hi && (at + step > geo.need_lo || at < geo.sinks)) ? at : -1;
-      };
-      auto page_of = [&](int at) { return at < 0 ? -1 : table ? __ldg(table + fast_div(at, p.div_page)) : w.b; };
-      int at = key_of(0), page = page_of(at);
-      float ks = 1.f, vs = 1.f;
-      auto store_scales = [&](int tile) {
-        if (!boxes && lane < 16 + kGroups) {
-          const int ve = scale_exponent(vs);
-          s_sca[(tile % kScaleRing) * kGroups + lane - 16] = make_float4(pow2f(scale_exponent(ks)), (float)ve, pow2f(-ve), 0.f);
+      int2 at = make_int2(-1, 0), at_v = at;
+      uint32_t bytes = 0, bytes_v = 0;
+      for (int i = 0; ok && i <= w.count; ++i) {
+        // K of tile i, and V of the tile before it
+        at_v = at;
+        bytes_v = bytes;
+        if (i < w.count) {
+          const int e = g % kPlaceRing;
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(pl_full + e, (g / kPlaceRing) & 1, abort_flag));
+          if (!ok) break;
+          at = box0 < kGroups ? s_pla[e * kGroups + box0] : make_int2(-1, 0);
+          bytes = __popc(__ballot_sync(0xffffffffu, at.x >= 0)) * p.box_rows * (uint32_t)D;
+          if (lane == 0) tc::mbar_arrive(pl_empty + e);
+          ++g;
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sc_full + tile % kScaleRing);  // (the slot's last reader is done: the rings behind are shorter)
-      };
-      for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const int at_n = i + 1 < w.count ? key_of(i + 1) : -1, page_n = page_of(at_n);
-        const int row = at - fast_div(max(at, 0), p.div_page) * p.page_size;
-        const bool good = at >= 0 && page >= 0 && page < p.num_pages;
-        if (boxes && at >= 0 && !good) chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)page);
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, good) & 0xffffu) * p.box_rows * (uint32_t)D;
-        if (i > 0) store_scales(g - 1);
-        ks = vs = 1.f;
-        if (!boxes && good) {
-          const int64_t b = row >> p.block_shift;
-          ks = __ldg(p.ks + page * p.ks_sb + b * p.ks_ss + head * p.ks_sh);
-          vs = __ldg(p.vs + page * p.vs_sb + b * p.vs_ss + head * p.vs_sh);
-        }
-        for (int v = 0; v < 2; ++v) {
+        for (int v = i < w.count ? 0 : 1; v < (i > 0 ? 2 : 1); ++v) {
           bool go = true;
-          if (lane == 0) go = tc::mbar_wait(raw_empty + s, phase, abort_flag);
-          go = __shfl_sync(0xffffffffu, go, 0);
-          if (!go) {
-            if (lane == 0) fail(p, abort_flag, 1);
-            ok = false;
-            break;
+          if (lane == 0) {
+            go = tc::mbar_wait(raw_empty + s, phase, abort_flag);
+            if (go) tc::mbar_arrive_expect_tx(raw_full + s, v ? bytes_v : bytes);
           }
-          if (lane == 0) tc::mbar_arrive_expect_tx(raw_full + s, bytes);
-          __syncwarp();
-          if (boxes && good && !withhold)
-            tc::tma_load_4d(smem + C::kRawOff + s * C::kRawBytes + lane * p.box_rows * D, v ? &tmv : &tmk, raw_full + s, 0, head, row, page);
+          ok = __shfl_sync(0xffffffffu, go, 0);
+          if (!ok) break;
+          unsigned char* dst = smem + C::kRawOff + s * C::kRawBytes + lane * p.box_rows * D;
+          if (v == 0 && at.x >= 0 && !withhold) tc::tma_load_4d(dst, &tmk, raw_full + s, 0, head, at.y, at.x);
+          if (v == 1 && at_v.x >= 0) tc::tma_load_4d(dst, &tmv, raw_full + s, 0, head, at_v.y, at_v.x);
           withhold = false;
           if (++s == NR) {
             s = 0;
             phase ^= 1;
           }
         }
-        at = at_n;
-        page = page_n;
       }
-      if (ok) store_scales(g - 1);
     }
+    if (!ok && lane == 0) fail(p, abort_flag, 1);
     if (lane == 0 && *abort_flag) {
       // let the copies under way land: each stage's next full phase, up to a limit
       for (int k = 0; k < NR; ++k) tc::mbar_wait_drain(raw_full + k, k < s ? phase ^ 1 : phase, 100000000ull);
     }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ pages and scales
+    // Four tiles at a time, ahead of the copies, by a lane for each group of 16 keys: its page
+    // and row (-1: no row of the tile sees its box) and its scales.  The softmax is less than
+    // 16 tiles behind the copies (by the rings between), so the place of a tile's scales,
+    // kScaleRing behind, is free when that of its pages is.
+    bool ok = true;
+    int g = 0;
+    const int x = lane & 7, tt = lane >> 3;
+    ChunkPiece w;
+    for (int r = next_with_keys<C>(p, n_pieces, 0, w); ok && r >= 0; r = next_with_keys<C>(p, n_pieces, r + 1, w)) {
+      const Geo geo = geo_of(p, w);
+      const int head = w.hg * p.gp / p.G, box_keys = p.box_rows;
+      const int32_t* table = p.block_table ? p.block_table + (int64_t)w.b * p.bt_stride : nullptr;
+      // (the group of tile i0 + tt, and the next four tiles' asked for)
+      auto key_of = [&](int i0) {
+        if (i0 + tt >= w.count) return -1;
+        const int key = geo.first_key(i0 + tt) + 16 * x, box = key & ~(box_keys - 1);  // (a box is copied whole)
+        return box <= geo.need_hi && (box + box_keys > geo.need_lo || box < geo.sinks) && key < geo.kv_len ? key : -1;
+      };
+      auto page_of = [&](int key) { return key < 0 ? -1 : table ? __ldg(table + fast_div(key, p.div_page)) : w.b; };
+      int key = key_of(0), page = page_of(key);
+      for (int i0 = 0; ok && i0 < w.count; i0 += 4) {
+        const int n = min(4, w.count - i0);
+        const int key_n = key_of(i0 + 4), page_n = page_of(key_n);
+        bool good = key >= 0;
+        if (good && (page < 0 || page >= p.num_pages)) {
+          chunk_error(p, FA_ERR_DEVICE_BOUNDS, (uint32_t)page);
+          good = false;
+        }
+        const int row = good ? key - fast_div(key, p.div_page) * p.page_size : 0;
+        float ks = 1.f, vs = 1.f;
+        if (good) {
+          const int64_t b = row >> p.block_shift;
+          ks = __ldg(p.ks + page * p.ks_sb + b * p.ks_ss + head * p.ks_sh);
+          vs = __ldg(p.vs + page * p.vs_sb + b * p.vs_ss + head * p.vs_sh);
+        }
+        const int to = g + i0 + tt;
+        bool go = true;
+        if (tt < n && to >= kPlaceRing) go = tc::mbar_wait(pl_empty + to % kPlaceRing, ((to - kPlaceRing) / kPlaceRing) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, go);
+        if (!ok) break;
+        if (tt < n) {
+          s_pla[(to % kPlaceRing) * kGroups + x] = make_int2(good ? page : -1, row);
+          const int ve = scale_exponent(vs), key0 = geo.first_key(i0 + tt);
+          // not whole: some row does not see all of the tile, or it goes past the end
+          const bool part = key0 + kKeysPerTile - 1 > geo.all_hi || (key0 < geo.all_lo && key0 + kKeysPerTile - 1 >= geo.sinks);
+          const int about = x == 0 ? key0 : x == 1 ? (int)part : x == 2 ? geo.need_lo : x == 3 ? geo.need_hi : 0;
+          s_sca[(to % kScaleRing) * kGroups + x] = make_float4(pow2f(scale_exponent(ks)), (float)ve, pow2f(-ve), __int_as_float(about));
+        }
+        __syncwarp();
+        if (x == 0 && tt < n) {
+          tc::mbar_arrive(pl_full + to % kPlaceRing);
+          tc::mbar_arrive(sc_full + to % kScaleRing);
+        }
+        key = key_n;
+        page = page_n;
+      }
+      g += w.count;
+    }
+    if (!ok && lane == 0) fail(p, abort_flag, 7);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issuer
@@ -353,38 +414,43 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
       tc::mbar_wait_drain(drained + 1, 0, 200000000ull);
     }
     __syncwarp();
+  }
   } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWidenRegs));
     // ------------------------------------------------------------ Q, and the widening
     const int cw = warp - 12;
+    // 8 codes to 16 bytes: a thread's piece is one of the row's D / 8, in every kRows-th
+    // row, a multiple of 8: its place in the swizzle stays
+    constexpr int kPieces = D / 8, kRows = 128 / kPieces;
+    const int t = 32 * cw + lane, c = t % kPieces, row0 = t / kPieces;
+    const unsigned char* const src0 = smem + C::kRawOff + t * 8;
+    unsigned char* const dst0 = smem + (c >> 3) * C::kHalfStep + row0 * 128 + (((c & 7) ^ (row0 & 7)) << 4);
     bool ok = true;
-    int g = 0, kk = 0, rs = 0;
+    int g = 0, kk = 0, rs = 0;  // tiles and busy pieces so far, raw tile
     uint32_t rphase = 0;
     ChunkPiece w;
     for (int r = next_with_keys<C>(p, n_pieces, 0, w); ok && r >= 0; r = next_with_keys<C>(p, n_pieces, r + 1, w), ++kk) {
-      const Geo geo = geo_of(p, w);
-      const int i0 = w.rt * p.rt_tokens;
       {
-        // Q: D / 8 lanes per row, 16 bytes each; a warp has rows cw, cw + 4 .. (pairs of
-        // them at d = 128, fours at 64), eight loads in flight
-        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kSteps = 128 / (4 * kPer), kAhead = 8;
+        // Q: D / 8 lanes per row, 16 bytes each, kAhead loads in flight
+        constexpr int kQLanes = D / 8, kPer = 32 / kQLanes, kSteps = 128 / (4 * kPer), kAhead = 4;
         const int64_t qbase = p.cu_q ? (int64_t)p.cu_q[w.b] : 0, qb = p.cu_q ? 0 : w.b;
-        const int c = lane % kLanes;
+        const int i0 = w.rt * p.rt_tokens, qc = lane % kQLanes, q_len = chunk_qlen(p, w.b);
         float* fac = s_fac + (kk % kRowRing) * 128;
+#pragma unroll 1
         for (int s0 = 0; ok && s0 < kSteps; s0 += kAhead) {
           uint4 u[kAhead];
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
-            const int row = ((s0 + k) * 4 + cw) * kPer + lane / kLanes, tok = fast_div(row, p.div_gp);
+            const int row = ((s0 + k) * 4 + cw) * kPer + lane / kQLanes, tok = fast_div(row, p.div_gp);
             u[k] = make_uint4(0, 0, 0, 0);
-            if (s0 + k < kSteps && tok < p.rt_tokens && i0 + tok < geo.q_len)
+            if (tok < p.rt_tokens && i0 + tok < q_len)
               u[k] = *reinterpret_cast<const uint4*>(p.q + qb * p.q_sb + (qbase + i0 + tok) * p.q_ss +
-                                                     (int64_t)(w.hg * p.gp + row - tok * p.gp) * p.q_sh + 8 * c);
+                                                     (int64_t)(w.hg * p.gp + row - tok * p.gp) * p.q_sh + 8 * qc);
           }
           if (s0 == 0 && kk > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(q_empty, (kk - 1) & 1, abort_flag));
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
-            if (s0 + k >= kSteps) continue;
-            const int row = ((s0 + k) * 4 + cw) * kPer + lane / kLanes;
+            const int row = ((s0 + k) * 4 + cw) * kPer + lane / kQLanes;
             const uint32_t v[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
             float x[8], top = 0.f;
 #pragma unroll
@@ -396,87 +462,79 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(fmaf(x[e], 0.f, x[e])));  // (finite ones)
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 1; o < kQLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const int e = q_exponent(top);
             const float down = pow2f(-e);
-            const uint4 h = make_uint4(pack2<true>(x[0] * down, x[1] * down), pack2<true>(x[2] * down, x[3] * down),
-                                       pack2<true>(x[4] * down, x[5] * down), pack2<true>(x[6] * down, x[7] * down));
-            *reinterpret_cast<uint4*>(smem + C::kQOff + (c >> 3) * C::kHalfStep + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = h;
-            if (c == 0) fac[row] = GEN ? pow2f(e) : pow2f(e) * p.scale_log2;
+            *reinterpret_cast<uint4*>(smem + C::kQOff + (qc >> 3) * C::kHalfStep + row * 128 + (((qc & 7) ^ (row & 7)) << 4)) =
+                make_uint4(pack2<true>(x[0] * down, x[1] * down), pack2<true>(x[2] * down, x[3] * down),
+                           pack2<true>(x[4] * down, x[5] * down), pack2<true>(x[6] * down, x[7] * down));
+            if (qc == 0) fac[row] = GEN ? pow2f(e) : pow2f(e) * p.scale_log2;
           }
         }
-        if (cw == 0 && lane == 0) nan_piece[kk % kRowRing] = 0;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(q_full + kk % kRowRing);
       }
-      for (int i = 0; ok && i < w.count; ++i, ++g) {
-        const int key = geo.first_key(i), rows = geo.kv_len - key;
-        const bool part = key + kKeysPerTile - 1 > geo.all_hi || (key < geo.all_lo && key + kKeysPerTile - 1 >= geo.sinks);
-        const int s = g % NS;
+      // (the raw tiles come as K_0, K_1, V_0, K_2, V_1 .. V_n-1)
 #pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          ok = tc::mbar_wait(raw_full + rs, rphase, abort_flag) &&
-               (g < NS || tc::mbar_wait((v ? v_empty : k_empty) + s, ((g - NS) / NS) & 1, abort_flag));
-          ok = __all_sync(0xffffffffu, ok);  // (the warp stays together)
-          if (!ok) break;
-          // 8 codes to 16 bytes: a thread's piece is one of the row's D / 8, in every
-          // kStep-th row, a multiple of 8: its place in the swizzle stays
-          constexpr int kPieces = D / 8, kStep = 128 / kPieces;
-          const int t = 32 * cw + lane, c = t % kPieces, row0 = t / kPieces;
-          const unsigned char* src = smem + C::kRawOff + rs * C::kRawBytes + t * 8;
-          unsigned char* dst = smem + (v ? C::kVOff : C::kKOff) + s * C::kTileBytes + (c >> 3) * C::kHalfStep + row0 * 128 +
-                               (((c & 7) ^ (row0 & 7)) << 4);
-          auto widen = [](uint2 u) {
-            return make_uint4(e4m3x2_to_f16x2((uint16_t)u.x), e4m3x2_to_f16x2((uint16_t)(u.x >> 16)), e4m3x2_to_f16x2((uint16_t)u.y),
-                              e4m3x2_to_f16x2((uint16_t)(u.y >> 16)));
-          };
-          uint32_t nans = 0;
-          if (v == 0 || !part) {
-            // (a tile of V that every row sees whole has no row past the end)
-            constexpr int kAhead = 8;
+      for (int m = 0; ok && m < 2 * w.count; ++m) {
+        const bool is_v = m > 0 && (!(m & 1) || m == 2 * w.count - 1);
+        const int gt = g + (is_v ? (m == 2 * w.count - 1 ? w.count - 1 : m / 2 - 1) : (m + 1) / 2), s = gt % NS;
+        uint64_t* const full = is_v ? v_full : k_full;
+        uint64_t* const empty = is_v ? v_empty : k_empty;
+        ok = tc::mbar_wait(raw_full + rs, rphase, abort_flag) && (gt < NS || tc::mbar_wait(empty + s, ((gt - NS) / NS) & 1, abort_flag)) &&
+             (!is_v || tc::mbar_wait(sc_full + gt % kScaleRing, (gt / kScaleRing) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, ok);  // (the warp stays together)
+        if (!ok) break;
+        const unsigned char* src = src0 + rs * C::kRawBytes;
+        unsigned char* dst = dst0 + (is_v ? C::kVOff : C::kKOff) + s * C::kTileBytes;
+        auto widen = [](uint2 u) {
+          return make_uint4(e4m3x2_to_f16x2((uint16_t)u.x), e4m3x2_to_f16x2((uint16_t)(u.x >> 16)), e4m3x2_to_f16x2((uint16_t)u.y),
+                            e4m3x2_to_f16x2((uint16_t)(u.y >> 16)));
+        };
+        const float4* sca = s_sca + (gt % kScaleRing) * kGroups;
+        if (!is_v || !__float_as_int(sca[1].w)) {
+          constexpr int kAhead = 8;
 #pragma unroll
-            for (int n0 = 0; n0 < kPieces; n0 += kAhead) {
-              uint2 u[kAhead];
+          for (int n0 = 0; n0 < kPieces; n0 += kAhead) {
+            uint2 u[kAhead];
 #pragma unroll
-              for (int n = 0; n < kAhead; ++n) u[n] = *reinterpret_cast<const uint2*>(src + (n0 + n) * 1024);
+            for (int n = 0; n < kAhead; ++n) u[n] = *reinterpret_cast<const uint2*>(src + (n0 + n) * 1024);
 #pragma unroll
-              for (int n = 0; n < kAhead; ++n) *reinterpret_cast<uint4*>(dst + (n0 + n) * kStep * 128) = widen(u[n]);
-            }
-          } else {
+            for (int n = 0; n < kAhead; ++n) *reinterpret_cast<uint4*>(dst + (n0 + n) * kRows * 128) = widen(u[n]);
+          }
+        } else {
+          const int key = __float_as_int(sca[0].w), need_lo = __float_as_int(sca[2].w), need_hi = __float_as_int(sca[3].w);
+          const int sinks = p.wl >= 0 ? p.sinks : 0;
+          bool nans = false;
 #pragma unroll 2
-            for (int n = 0; n < kPieces; ++n) {
-              const int row = row0 + n * kStep;
-              const uint2 u = *reinterpret_cast<const uint2*>(src + n * 1024);
-              uint4 h = widen(u);
-              if (has_nan(u.x) || has_nan(u.y)) {
-                // (what stands for a key that no row sees does not count)
-                nans |= key + row <= geo.need_hi && (key + row >= geo.need_lo || key + row < geo.sinks);
-                uint32_t* x = reinterpret_cast<uint32_t*>(&h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] &= ~__hneu2_mask(*reinterpret_cast<__half2*>(x + e), *reinterpret_cast<__half2*>(x + e));
-              }
-              if (row >= rows) h = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(dst + n * kStep * 128) = h;
-            }
+          for (int n = 0; n < kPieces; ++n) {
+            const int j = key + row0 + n * kRows;
+            const bool seen = j <= need_hi && (j >= need_lo || j < sinks);
+            uint2 u = *reinterpret_cast<const uint2*>(src + n * 1024);
+            const uint32_t mx = seen ? nan_codes(u.x) : 0xffffffffu, my = seen ? nan_codes(u.y) : 0xffffffffu;  // (a key that no row sees: 0)
+            nans |= seen && (mx | my) != 0;
+            u.x &= ~mx;
+            u.y &= ~my;
+            *reinterpret_cast<uint4*>(dst + n * kRows * 128) = widen(u);
           }
           if (nans) nan_piece[kk % kRowRing] = kk + 1;
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tc::mbar_arrive((v ? v_full : k_full) + s);
-            tc::mbar_arrive(raw_empty + rs);
-          }
-          if (++rs == NR) {
-            rs = 0;
-            rphase ^= 1;
-          }
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(raw_empty + rs);
+        if (++rs == NR) {
+          rs = 0;
+          rphase ^= 1;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(full + s);
       }
+      g += w.count;
     }
     if (!ok && lane == 0) fail(p, abort_flag, 6);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------ softmax
     const int wg = (warp - 4) >> 2, wq = warp & 3;  // warpgroup, TMEM lane quarter
@@ -738,8 +796,11 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
 #pragma unroll
         for (int c = 0; c < kHalfD / 32; ++c) nan[c] = 0;
         const int hk = un.hg * p.gp / p.G;
+        const Geo geo = geo_of(p, un);
         for (int it = 0; it < count; ++it) {
           const int tile = kt0 + it, j0 = (tile + (tile >= first ? gap : 0)) * kKeysPerTile;
+          // (in a tile that every row sees whole the products bring them)
+          if (j0 + kKeysPerTile - 1 <= geo.all_hi && (j0 >= geo.all_lo || j0 + kKeysPerTile - 1 < sinks)) continue;
           for (int j = j0; j < j0 + kKeysPerTile; ++j) {
             if (j > jhi_r || (j < jlo_r && j >= sinks)) continue;
             const int pg_i = fast_div(j, p.div_page), pg = p.block_table ? p.block_table[(int64_t)un.b * p.bt_stride + pg_i] : un.b;
