@@ -12,28 +12,39 @@
 // Bound: HBM; 4 bytes an element forward, 6 backward, about 7 and 16 flop.  A
 // thread takes 16 columns of a head (two 16-byte loads), the d / 16 lanes of a
 // head sum its squares by shuffles, and all arithmetic is fp32 with one rounding
-// at the store.  A CTA makes the (cos, sin) of up to eight tokens once, in shared
-// memory, for all heads; a thread keeps its columns' weights in registers.  The
-// backward pass runs a grid of one wave whose threads keep their columns' dw in
-// registers over all their rows; a CTA's sum goes to the workspace and a second
-// kernel adds the CTAs' in their order, in fp64: no atomics, and the result
-// does not depend on scheduling.
+// at the store.  A warp works alone on one token's heads, 32 / (d / 16) at a time (a
+// round), and makes the token's (cos, sin) once; its lanes hold the turns and
+// weights of their columns in registers.  Forward, a warp has four rounds of q or k, all
+// loads under way before the turns are made.  The backward pass is one wave of warps,
+// each with an even share of the rounds, three of them ahead by cp.async; a lane
+// holds its columns' dw in registers over all of them, a CTA's sum goes to the
+// workspace and a second kernel adds the CTAs' in their order, to about 48 bits: no atomics,
+// and the result does not depend on scheduling.
+//
+// Measured (8192 tokens, 32 + 8 heads, d 128, bf16, all columns rotated): forward 32.6 us
+// (5.2 TB/s), backward 53 us (4.7 TB/s), of it 4 for dw; one token 4 .. 6 us.  The issue
+// slots are two thirds full at that rate; what helped: turns once per token and warp (with
+// eight tokens' turns to a CTA of 256 threads, between barriers, 48 and 98 us), pairs of
+// fp32 to an instruction, whole sectors for interleaved pairs (backward, no rotation: 69 us to 43).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 
 #include <cuda_runtime.h>
 
+#include "f32x2.cuh"
 #include "rope_common.cuh"
 
 using namespace mfa;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kFwdBlocks = 3;  // CTAs per SM
-constexpr int kBwdBlocks = 2;
-constexpr int kMaxTokens = 8;  // tokens per CTA and step
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kFwdBlocks = 5;  // CTAs per SM
+constexpr int kBwdBlocks = 4;
+constexpr int kAhead = 4;      // rounds whose loads are under way, forward
+constexpr int kStages = 4;     // rounds in shared memory, backward
+constexpr int kDwThreads = 1024;
 constexpr int kMaxParts = 1024;  // CTAs of the backward pass
 static_assert(FA_QK_NORM_ROPE_BWD_WORKSPACE_BYTES >= kWsHeadBytes + (size_t)kMaxParts * 2 * 128 * 4, "partials of dw");
 
@@ -47,7 +58,9 @@ struct NormRows {
   int64_t x_sb, x_ss, x_sh, dy_sb, dy_ss, dy_sh, out_sb, out_ss, out_sh;
   const void* w;
   float* dw;  // nullable
-  int32_t w_kind, heads;
+  int32_t w_kind, w_wide, heads;  // w_wide: 16-byte loads of w
+  int32_t rounds;  // of a token
+  int64_t share, more;  // backward: every warp's rounds, and the number of warps with one more
 };
 
 struct NormParams {
@@ -59,8 +72,7 @@ struct NormParams {
   const double* inv_freq;
   int32_t half;  // pairs; 0: no rotation
   float mscale, eps;
-  int32_t tb;  // tokens per CTA and step, a power of two
-  int64_t steps;  // of tb tokens
+  int32_t units, span;  // forward: warps of a token, and rounds of a warp
   float* part;  // backward: [CTAs][2][D], null without weight gradients
   int32_t n_parts;
 };
@@ -73,8 +85,30 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// Lane c's columns; of kInterleaved's pairs both halves' 4 c .. 4 c + 3 (a warp's
+// 16 bytes are then whole sectors).
+template <int D, int LAYOUT>
+__device__ __forceinline__ Columns lane_columns(int c, int half) {
+  if (LAYOUT == kInterleaved) return {8 * c, D / 2 + 8 * c};
+  return columns_of<LAYOUT>(c, half);
+}
+
 template <bool F16>
 __device__ __forceinline__ void load_weight(const NormRows& r, Columns at, float (&w)[16]) {
+  if (r.w_wide && r.w_kind == kWeight16) {
+    const uint16_t* src = static_cast<const uint16_t*>(r.w);
+    unpack16<F16>(__ldg(reinterpret_cast<const uint4*>(src + at.xa)), __ldg(reinterpret_cast<const uint4*>(src + at.xb)), w);
+    return;
+  }
+  if (r.w_wide && r.w_kind == kWeightF32) {
+    const float* src = static_cast<const float*>(r.w);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + (e < 8 ? at.xa + e : at.xb + e - 8)));
+      w[e] = v.x; w[e + 1] = v.y; w[e + 2] = v.z; w[e + 3] = v.w;
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int col = e < 8 ? at.xa + e : at.xb + e - 8;
@@ -84,208 +118,468 @@ __device__ __forceinline__ void load_weight(const NormRows& r, Columns at, float
   }
 }
 
-// Tokens row0 .. row0 + tb - 1: their sequences (-1: no such token), rows and turns.
-template <int D>
-__device__ __forceinline__ void load_tokens(const NormParams& p, int64_t row0, bool inverse, float2* cs, int* s_b, int* s_i,
-                                            int* s_pos) {
-  const int tid = threadIdx.x;
-  if (tid < p.tb) {
-    const int64_t row = row0 + tid;
-    int b = -1, i = 0, pos = 0;
-    if (row < p.rows) {
-      b = (int)(row / p.S);
-      i = (int)(row - (int64_t)b * p.S);
-      pos = p.positions ? __ldg(p.positions + b * p.pos_sb + i * p.pos_ss) : i;
-    }
-    s_b[tid] = b;
-    s_i[tid] = i;
-    s_pos[tid] = pos;
+__device__ __forceinline__ int position_of(const NormParams& p, int b, int i) {
+  return p.positions ? __ldg(p.positions + b * p.pos_sb + i * p.pos_ss) : i;
+}
+
+// A lane's part of its warp's turns: pairs lane and lane + 32.
+__device__ __forceinline__ void turn_steps(const NormParams& p, int lane, uint64_t (&u)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) u[k] = lane + 32 * k < p.half ? turn_step(__ldg(p.inv_freq + lane + 32 * k)) : 0;
+}
+// A lane's 16 columns as 8 rotated pairs (a, b), two of each to a register pair:
+// column e and the one a half behind, or columns 2 e and 2 e + 1.
+struct Pairs {
+  float2 a[4], b[4];
+};
+template <int LAYOUT>
+__device__ __forceinline__ Pairs pairs_of(const float (&x)[16]) {
+  Pairs y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    y.a[k] = LAYOUT == kInterleaved ? make_float2(x[4 * k], x[4 * k + 2]) : make_float2(x[2 * k], x[2 * k + 1]);
+    y.b[k] = LAYOUT == kInterleaved ? make_float2(x[4 * k + 1], x[4 * k + 3]) : make_float2(x[8 + 2 * k], x[9 + 2 * k]);
+  }
+  return y;
+}
+template <int LAYOUT>
+__device__ __forceinline__ void columns_from(const Pairs& y, float (&x)[16]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[LAYOUT == kInterleaved ? 4 * k : 2 * k] = y.a[k].x;
+    x[LAYOUT == kInterleaved ? 4 * k + 2 : 2 * k + 1] = y.a[k].y;
+    x[LAYOUT == kInterleaved ? 4 * k + 1 : 8 + 2 * k] = y.b[k].x;
+    x[LAYOUT == kInterleaved ? 4 * k + 3 : 9 + 2 * k] = y.b[k].y;
+  }
+}
+template <bool F16, int LAYOUT>
+__device__ __forceinline__ Pairs unpack_pairs(const uint4& a, const uint4& b) {
+  float x[16];
+  unpack16<F16>(a, b, x);
+  return pairs_of<LAYOUT>(x);
+}
+template <bool F16, int LAYOUT>
+__device__ __forceinline__ void pack_pairs(const Pairs& y, uint4& a, uint4& b) {
+  float x[16];
+  columns_from<LAYOUT>(y, x);
+  pack16<F16>(x, a, b);
+}
+// Sum of the products of two rows, over the lanes of their head.
+template <int kLanes>
+__device__ __forceinline__ float dot(const Pairs& x, const Pairs& y) {
+  float2 s = mul2(x.a[0], y.a[0]), t = mul2(x.b[0], y.b[0]);
+#pragma unroll
+  for (int k = 1; k < 4; ++k) {
+    s = fma2(x.a[k], y.a[k], s);
+    t = fma2(x.b[k], y.b[k], t);
+  }
+  s = add2(s, t);
+  return head_sum<kLanes>(s.x + s.y);
+}
+__device__ __forceinline__ void scale(Pairs& x, float f) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x.a[k] = mul2(x.a[k], both(f));
+    x.b[k] = mul2(x.b[k], both(f));
+  }
+}
+__device__ __forceinline__ void multiply(Pairs& x, const Pairs& y) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x.a[k] = mul2(x.a[k], y.a[k]);
+    x.b[k] = mul2(x.b[k], y.b[k]);
+  }
+}
+
+// q's and k's weights, lane c's pairs at [n][0 .. 3][c].
+template <int kLanes>
+using Weights = float4[2][4][kLanes];
+template <bool F16, int LAYOUT, int kLanes>
+__device__ __forceinline__ void stage_weights(const NormParams& p, int half, Weights<kLanes>& s_w) {
+  const int n = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  if (n < 2) {
+    float w[16];
+    load_weight<F16>(p.t[n], lane_columns<16 * kLanes, LAYOUT>(c, half), w);
+    const Pairs y = pairs_of<LAYOUT>(w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s_w[n][k][c] = make_float4(y.a[k].x, y.a[k].y, y.b[k].x, y.b[k].y);
   }
   __syncthreads();
-  if (p.half > 0) {
-    const int groups = kThreads / p.half;  // half <= 64
-    if (tid < groups * p.half) {
-      const int i = tid % p.half;
-      const uint64_t u = turn_step(__ldg(p.inv_freq + i));
-      for (int t = tid / p.half; t < p.tb; t += groups) cs[t * (D / 2) + i] = position_turn(s_pos[t], u, p.mscale, inverse);
+}
+template <int kLanes>
+__device__ __forceinline__ Pairs weight_of(const Weights<kLanes>& s_w, int n, int c) {
+  Pairs w;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 v = s_w[n][k][c];
+    w.a[k] = make_float2(v.x, v.y);
+    w.b[k] = make_float2(v.z, v.w);
+  }
+  return w;
+}
+
+// The turns of a lane's pairs.
+struct Turns {
+  float2 co[4], sn[4];
+};
+// The first pair of lane c's register pairs k.
+template <int D, int LAYOUT>
+__device__ __forceinline__ int first_pair(int c, int k) {
+  return LAYOUT == kInterleaved ? (k / 2) * (D / 4) + 4 * c + 2 * (k % 2) : 8 * c + 2 * k;
+}
+// The place of pair i's turn: such that the lanes of a head read different banks, 16 bytes each.
+template <int LAYOUT>
+__device__ __forceinline__ int turn_place(int i) {
+  return LAYOUT == kInterleaved ? i ^ (i >> 4 & 1) << 1 : LAYOUT == kHalf ? i ^ (i >> 4 & 3) << 1 : i;
+}
+// The turns of position pos, to cs.  (By all the lanes of a warp.)
+template <int LAYOUT>
+__device__ __forceinline__ void make_turns(const NormParams& p, int pos, const uint64_t (&u)[2], bool inverse, int lane, float2* cs) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (lane + 32 * k < p.half) cs[turn_place<LAYOUT>(lane + 32 * k)] = position_turn(pos, u[k], p.mscale, inverse);
+  __syncwarp();
+}
+// Those of lane c's pairs (of its pairs that are not rotated: anything).
+template <int D, int LAYOUT>
+__device__ __forceinline__ void load_turns(const float2* cs, int c, Turns& tw) {
+  if (LAYOUT == kHalfOdd) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(cs + turn_place<LAYOUT>(first_pair<D, LAYOUT>(c, k)));
+    tw.co[k] = make_float2(v.x, v.z);
+    tw.sn[k] = make_float2(v.y, v.w);
+  }
+}
+
+// rotate16, of pairs and with the turns in registers where lanes do not exchange columns.
+template <int D, int LAYOUT>
+__device__ __forceinline__ void rotate(Pairs& x, const Turns& tw, const float2* cs, int c, int half, float* row) {
+  if constexpr (LAYOUT == kHalfOdd) {
+    float y[16];
+    columns_from<LAYOUT>(x, y);
+    rotate16<LAYOUT>(y, cs, c, half, row);
+    x = pairs_of<LAYOUT>(y);
+  } else {
+    // (kHalf: all eight pairs or none; kInterleaved: so for each four but where half % 4 is not 0)
+    constexpr int kSame = LAYOUT == kInterleaved ? 2 : 4;
+#pragma unroll
+    for (int k0 = 0; k0 < 4; k0 += kSame) {
+      const int left = half - first_pair<D, LAYOUT>(c, k0);  // pairs from here on that are rotated
+      if (left <= 0) continue;
+      Pairs was = x;
+#pragma unroll
+      for (int k = k0; k < k0 + kSame; ++k) {
+        const float2 t = mul2(x.b[k], tw.sn[k]), a = x.a[k];
+        x.a[k] = fma2(a, tw.co[k], make_float2(-t.x, -t.y));
+        x.b[k] = fma2(a, tw.sn[k], mul2(x.b[k], tw.co[k]));
+      }
+      if (LAYOUT == kInterleaved && left < 4) {
+#pragma unroll
+        for (int k = k0; k < k0 + kSame; ++k) {
+          if (left <= 2 * (k - k0)) x.a[k].x = was.a[k].x, x.b[k].x = was.b[k].x;
+          if (left <= 2 * (k - k0) + 1) x.a[k].y = was.a[k].y, x.b[k].y = was.b[k].y;
+        }
+      }
     }
-    __syncthreads();
   }
 }
 
 template <int D, bool F16, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_kernel(const __grid_constant__ NormParams p) {
-  constexpr int kLanes = D / 16, kSlots = kThreads / kLanes;  // threads per head; heads at a time
-  __shared__ float2 cs[kMaxTokens * D / 2];
-  __shared__ int s_b[kMaxTokens], s_i[kMaxTokens], s_pos[kMaxTokens];
-  __shared__ float s_row[LAYOUT == kHalfOdd ? kSlots * D : 1];
-  const int c = threadIdx.x % kLanes, slot = threadIdx.x / kLanes, half = p.half;
-  load_tokens<D>(p, (int64_t)blockIdx.x * p.tb, false, cs, s_b, s_i, s_pos);
-  const int per = kSlots / p.tb;  // slots per token
-  const int t = slot / per, b = s_b[t], i = s_i[t];
-  const Columns at = columns_of<LAYOUT>(c, half);
-  float* row = s_row + (LAYOUT == kHalfOdd ? slot * D : 0);
-  const int step = per * gridDim.y;
-  // (the lanes of a warp stay together through the shuffles: a slot without a
-  // token or head computes on zeros and stores nothing)
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes per head; heads of a round
+  __shared__ __align__(16) float2 s_cs[kWarps][D / 2];
+  __shared__ Weights<kLanes> s_w;
+  __shared__ float s_row[LAYOUT == kHalfOdd ? kWarps * kHeads * D : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes, slot = lane / kLanes, half = p.half;
+  const uint32_t group = blockIdx.x / (uint32_t)p.units;
+  const int r0 = (int)(blockIdx.x - group * p.units) * p.span, rq = p.t[0].rounds, r1 = min(r0 + p.span, rq + p.t[1].rounds);
+  const int64_t at_row = (int64_t)group * kWarps + warp;
+  const bool live = at_row < p.rows;
+  const int b = live ? (int)at_row / p.S : 0, i = live ? (int)at_row - b * p.S : 0;
+  const Columns at = lane_columns<D, LAYOUT>(c, half);
+  const uint16_t* const src[2] = {p.t[0].x + b * p.t[0].x_sb + i * p.t[0].x_ss, p.t[1].x + b * p.t[1].x_sb + i * p.t[1].x_ss};
+  auto load = [&](int r, uint4& va, uint4& vb) {
+    const int n = r >= rq, h = (n ? r - rq : r) * kHeads + slot;
+    va = vb = make_uint4(0, 0, 0, 0);
+    if (live && r < r1 && h < p.t[n].heads) {
+      const uint16_t* from = (n ? src[1] : src[0]) + h * p.t[n].x_sh;
+      va = *reinterpret_cast<const uint4*>(from + at.xa);
+      vb = *reinterpret_cast<const uint4*>(from + at.xb);
+    }
+  };
+  uint4 va[kAhead], vb[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) load(r0 + k, va[k], vb[k]);
+  uint64_t u[2] = {0, 0};
+  int pos = 0;
+  if (half > 0) {
+    if (live) pos = position_of(p, b, i);
+    turn_steps(p, lane, u);
+  }
+  stage_weights<F16, LAYOUT, kLanes>(p, half, s_w);
+  if (!live) return;
+  Turns tw;
+  if (half > 0) {
+    make_turns<LAYOUT>(p, pos, u, false, lane, s_cs[warp]);
+    load_turns<D, LAYOUT>(s_cs[warp], c, tw);
+  }
+  uint16_t* const dst[2] = {p.t[0].out + b * p.t[0].out_sb + i * p.t[0].out_ss, p.t[1].out + b * p.t[1].out_sb + i * p.t[1].out_ss};
+  // (the lanes of a warp stay together through the shuffles: those without a head
+  // compute on zeros and store nothing)
 #pragma unroll 1
-  for (int n = 0; n < 2; ++n) {
-    const NormRows& r = p.t[n];
-    if (r.heads == 0) continue;
-    float w[16];
-    load_weight<F16>(r, at, w);
-    const uint16_t* src = r.x + b * r.x_sb + i * r.x_ss;
-    uint16_t* dst = r.out + b * r.out_sb + i * r.out_ss;
-    // as many rounds for every slot
-    for (int h0 = blockIdx.y * per; h0 < r.heads; h0 += 2 * step) {
-      uint4 va[2], vb[2];
-      int h[2];
+  for (int r = r0; r < r1; r += kAhead) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        h[k] = h0 + k * step + slot % per;
-        if (b < 0 || h[k] >= r.heads) h[k] = -1;
-        va[k] = vb[k] = make_uint4(0, 0, 0, 0);
-        if (h[k] >= 0) {
-          va[k] = *reinterpret_cast<const uint4*>(src + h[k] * r.x_sh + at.xa);
-          vb[k] = *reinterpret_cast<const uint4*>(src + h[k] * r.x_sh + at.xb);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x[16];
-        unpack16<F16>(va[k], vb[k], x);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        const float inv = rsqrtf(fmaf(head_sum<kLanes>(ss), 1.f / D, p.eps));
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * w[e];
-        rotate16<LAYOUT>(x, cs + t * (D / 2), c, half, row);
-        if (h[k] >= 0) {
-          pack16<F16>(x, va[k], vb[k]);
-          *reinterpret_cast<uint4*>(dst + h[k] * r.out_sh + at.xa) = va[k];
-          *reinterpret_cast<uint4*>(dst + h[k] * r.out_sh + at.xb) = vb[k];
-        }
+    for (int k = 0; k < kAhead; ++k) {
+      if (r + k >= r1) break;
+      const int n = r + k >= rq, h = (n ? r + k - rq : r + k) * kHeads + slot;
+      Pairs x = unpack_pairs<F16, LAYOUT>(va[k], vb[k]);
+      load(r + k + kAhead, va[k], vb[k]);
+      const float inv = rsqrtf(fmaf(dot<kLanes>(x, x), 1.f / D, p.eps));
+      scale(x, inv);
+      multiply(x, weight_of<kLanes>(s_w, n, c));
+      rotate<D, LAYOUT>(x, tw, s_cs[warp], c, half, s_row + (LAYOUT == kHalfOdd ? (warp * kHeads + slot) * D : 0));
+      if (h < p.t[n].heads) {
+        uint16_t* to = (n ? dst[1] : dst[0]) + h * p.t[n].out_sh;
+        uint4 ya, yb;
+        pack_pairs<F16, LAYOUT>(x, ya, yb);
+        *reinterpret_cast<uint4*>(to + at.xa) = ya;
+        *reinterpret_cast<uint4*>(to + at.xb) = yb;
       }
     }
   }
+}
+
+// A warp's rounds of the backward pass: an even share of q's, then one of k's.
+struct Walk {
+  int n, left, b, i, round;
+  __device__ __forceinline__ void start(const NormParams& p, int tensor) {
+    n = tensor;
+    const NormRows& r = p.t[n];
+    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), lo = w * r.share + min(w, r.more);
+    left = (int)(r.share + (w < r.more));
+    if (left == 0) return;
+    // (a 64-bit division takes a microsecond)
+    const int64_t row = lo <= UINT32_MAX ? (uint32_t)lo / (uint32_t)r.rounds : lo / r.rounds;
+    round = (int)(lo - row * r.rounds);
+    b = (int)((uint32_t)row / (uint32_t)p.S);
+    i = (int)row - b * p.S;
+  }
+  __device__ __forceinline__ void begin(const NormParams& p) {
+    start(p, 0);
+    if (left == 0) start(p, 1);
+  }
+  // To the next round; true if its token is another (or its tensor).
+  __device__ __forceinline__ bool next(const NormParams& p) {
+    if (--left == 0) {
+      if (n == 0) start(p, 1);
+      return true;
+    }
+    if (++round < p.t[n].rounds) return false;
+    round = 0;
+    if (++i == p.S) {
+      i = 0;
+      ++b;
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
+  const int bytes = valid ? 16 : 0;  // (0: the rest is zeros, and nothing is read)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes)
+               : "memory");
 }
 
 template <int D, bool F16, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_bwd_kernel(const __grid_constant__ NormParams p) {
-  constexpr int kLanes = D / 16, kSlots = kThreads / kLanes;
-  // the turns of a step; after the last step the slots' sums of dw
-  __shared__ union {
-    float2 cs[kMaxTokens * D / 2];
-    float sum[kThreads / 32][D];
-  } u;
-  __shared__ int s_b[kMaxTokens], s_i[kMaxTokens], s_pos[kMaxTokens];
-  __shared__ float s_row[LAYOUT == kHalfOdd ? kSlots * D : 1];
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+  __shared__ uint4 s_in[kWarps][kStages][4][32];  // a lane reads what it copied: x and dy, 32 bytes each
+  __shared__ __align__(16) float2 s_cs[kWarps][D / 2];
+  __shared__ int s_pos[kWarps][kStages];
+  __shared__ float s_sum[2][kWarps][D];
+  __shared__ Weights<kLanes> s_w;
+  __shared__ float s_row[LAYOUT == kHalfOdd ? kWarps * kHeads * D : 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int c = threadIdx.x % kLanes, slot = threadIdx.x / kLanes, half = p.half, lane = threadIdx.x & 31;
-  const int per = kSlots / p.tb, t = slot / per;
-  const Columns at = columns_of<LAYOUT>(c, half);
-  float* row = s_row + (LAYOUT == kHalfOdd ? slot * D : 0);
-  float dw[2][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes, slot = lane / kLanes, half = p.half;
+  const Columns at = lane_columns<D, LAYOUT>(c, half);
+  float* row = s_row + (LAYOUT == kHalfOdd ? (warp * kHeads + slot) * D : 0);
+  uint64_t u[2] = {0, 0};
+  if (half > 0) turn_steps(p, lane, u);
+  Pairs dw;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = both(0.f);
 #pragma unroll
   for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) dw[n][e] = 0.f;
+    for (int col = lane; col < D; col += 32) s_sum[n][warp][col] = 0.f;
+  __syncwarp();
 
-  for (int64_t s = blockIdx.x; s < p.steps; s += gridDim.x) {
-    load_tokens<D>(p, s * p.tb, true, u.cs, s_b, s_i, s_pos);
-    const int b = s_b[t], i = s_i[t];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const NormRows& r = p.t[n];
-      if (r.heads == 0) continue;
-      float w[16];
-      load_weight<F16>(r, at, w);
-      const uint16_t* src = r.x + b * r.x_sb + i * r.x_ss;
-      const uint16_t* grad = r.dy + b * r.dy_sb + i * r.dy_ss;
-      uint16_t* dst = r.out + b * r.out_sb + i * r.out_ss;
-      for (int h0 = 0; h0 < r.heads; h0 += per) {
-        int h = h0 + slot % per;
-        if (b < 0 || h >= r.heads) h = -1;
-        uint4 xa = make_uint4(0, 0, 0, 0), xb = xa, ga = xa, gb = xa;
-        if (h >= 0) {
-          xa = *reinterpret_cast<const uint4*>(src + h * r.x_sh + at.xa);
-          xb = *reinterpret_cast<const uint4*>(src + h * r.x_sh + at.xb);
-          ga = *reinterpret_cast<const uint4*>(grad + h * r.dy_sh + at.xa);
-          gb = *reinterpret_cast<const uint4*>(grad + h * r.dy_sh + at.xb);
-        }
-        float x[16], g[16];
-        unpack16<F16>(xa, xb, x);
-        unpack16<F16>(ga, gb, g);
-        rotate16<LAYOUT>(g, u.cs + t * (D / 2), c, half, row);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        const float inv = rsqrtf(fmaf(head_sum<kLanes>(ss), 1.f / D, p.eps));
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] *= inv;  // the unit row
-          dw[n][e] = fmaf(g[e], x[e], dw[n][e]);
-          g[e] *= w[e];
-          dot = fmaf(g[e], x[e], dot);
-        }
-        dot = head_sum<kLanes>(dot) * (1.f / D);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = inv * fmaf(-x[e], dot, g[e]);
-        if (h >= 0) {
-          pack16<F16>(g, xa, xb);
-          *reinterpret_cast<uint4*>(dst + h * r.out_sh + at.xa) = xa;
-          *reinterpret_cast<uint4*>(dst + h * r.out_sh + at.xb) = xb;
-        }
-      }
-    }
-    __syncthreads();  // the turns are read
-  }
-  if (!p.part) return;
-  // the CTA's sums: over the heads of a warp by shuffles, over its warps in order
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
+  // the warp's sums of dw, over its heads by shuffles
+  auto flush = [&](int n) {
+    if (!p.part) return;
+    float sums[16];
+    columns_from<LAYOUT>(dw, sums);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float v = dw[n][e];
+      float v = sums[e];
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane < kLanes) u.sum[threadIdx.x / 32][e < 8 ? at.xa + e : at.xb + e - 8] = v;
+      if (lane < kLanes) s_sum[n][warp][e < 8 ? at.xa + e : at.xb + e - 8] = v;
     }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kThreads / 32; ++k) v += u.sum[k][threadIdx.x];
-      p.part[((int64_t)blockIdx.x * 2 + n) * D + threadIdx.x] = v;
+    for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = both(0.f);
+  };
+  // (the next round's x and dy of this lane)
+  const uint16_t *f_x = nullptr, *f_dy = nullptr;
+  const int apart = at.xb - at.xa;
+  auto issue = [&](const Walk& f, bool fresh, int stage) {
+    const NormRows& r = p.t[f.n];
+    if (fresh) {
+      const int h = f.round * kHeads + slot;
+      f_x = r.x + f.b * r.x_sb + f.i * r.x_ss + h * r.x_sh + at.xa;
+      f_dy = r.dy + f.b * r.dy_sb + f.i * r.dy_ss + h * r.dy_sh + at.xa;
     }
-    __syncthreads();
+    const bool valid = f.round * kHeads + slot < r.heads;
+    uint4* to = &s_in[warp][stage][0][lane];
+    const uint16_t *src = valid ? f_x : r.x, *grad = valid ? f_dy : r.dy;
+    copy16(to, src, valid);
+    copy16(to + 32, src + apart, valid);
+    copy16(to + 64, grad, valid);
+    copy16(to + 96, grad + apart, valid);
+    f_x += kHeads * r.x_sh;
+    f_dy += kHeads * r.dy_sh;
+    if (half > 0 && lane == 0) {
+      int* at_pos = &s_pos[warp][stage];
+      if (p.positions)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(at_pos)),
+                     "l"(p.positions + f.b * p.pos_sb + f.i * p.pos_ss)
+                     : "memory");
+      else *at_pos = f.i;
+    }
+  };
+
+  Walk f, v;
+  f.begin(p);
+  v = f;
+  bool f_fresh = true;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (f.left > 0) {
+      issue(f, f_fresh, s);
+      f_fresh = f.next(p);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  stage_weights<F16, LAYOUT, kLanes>(p, half, s_w);
+  int stage = 0, n = -1;
+  bool fresh = true;
+  while (v.left > 0) {
+    if (v.n != n) {
+      if (n >= 0) flush(n);
+      n = v.n;
+    }
+    const NormRows& r = p.t[n];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    if (half > 0) {
+      __syncwarp();  // the position came by lane 0's copy
+      if (fresh) make_turns<LAYOUT>(p, s_pos[warp][stage], u, true, lane, s_cs[warp]);
+    }
+    const uint4* in = &s_in[warp][stage][0][lane];
+    Pairs x = unpack_pairs<F16, LAYOUT>(in[0], in[32]), g = unpack_pairs<F16, LAYOUT>(in[64], in[96]);
+    if (f.left > 0) {
+      issue(f, f_fresh, (stage + kStages - 1) % kStages);
+      f_fresh = f.next(p);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    stage = (stage + 1) % kStages;
+    {
+      Turns tw;
+      load_turns<D, LAYOUT>(s_cs[warp], c, tw);
+      rotate<D, LAYOUT>(g, tw, s_cs[warp], c, half, row);
+    }
+    const float inv = rsqrtf(fmaf(dot<kLanes>(x, x), 1.f / D, p.eps));
+    scale(x, inv);  // the unit row
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      dw.a[k] = fma2(g.a[k], x.a[k], dw.a[k]);
+      dw.b[k] = fma2(g.b[k], x.b[k], dw.b[k]);
+    }
+    multiply(g, weight_of<kLanes>(s_w, n, c));
+    const float2 m = both(-dot<kLanes>(g, x) * (1.f / D));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      g.a[k] = fma2(x.a[k], m, g.a[k]);
+      g.b[k] = fma2(x.b[k], m, g.b[k]);
+    }
+    scale(g, inv);
+    const int h = v.round * kHeads + slot;
+    if (h < r.heads) {
+      uint4 a, b;
+      pack_pairs<F16, LAYOUT>(g, a, b);
+      uint16_t* dst = r.out + v.b * r.out_sb + v.i * r.out_ss + h * r.out_sh;
+      *reinterpret_cast<uint4*>(dst + at.xa) = a;
+      *reinterpret_cast<uint4*>(dst + at.xb) = b;
+    }
+    fresh = v.next(p);
+  }
+  if (!p.part) return;
+  if (n >= 0) flush(n);
+  __syncthreads();
+  for (int k = threadIdx.x; k < 2 * D; k += kThreads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += s_sum[k / D][w][k % D];
+    p.part[(int64_t)blockIdx.x * 2 * D + k] = sum;
   }
 }
 
-// dw: 32 columns of q's or k's per CTA, the parts dealt to its warps.
+// dw: eight columns of q's or k's per CTA, a part for every eight threads at a time.
 template <int D>
-__global__ void __launch_bounds__(kThreads) norm_dw_kernel(const __grid_constant__ NormParams p) {
-  __shared__ double s[kThreads / 32][32];
+__global__ void __launch_bounds__(kDwThreads) norm_dw_kernel(const __grid_constant__ NormParams p) {
+  constexpr int kDwWarps = kDwThreads / 32;
+  __shared__ float2 s[kDwWarps][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = blockIdx.x / (D / 32), col = blockIdx.x % (D / 32) * 32 + lane;
+  const int n = blockIdx.x / (D / 8), col = blockIdx.x % (D / 8) * 8 + lane % 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!p.t[n].dw) return;
-  double v = 0.0;
-#pragma unroll 4
-  for (int k = warp; k < p.n_parts; k += kThreads / 32) v += p.part[((int64_t)k * 2 + n) * D + col];
-  s[warp][lane] = v;
-  __syncthreads();
-  if (warp == 0) {
+  // (in two fp32 words, the second the first's rounding errors: fp64 would take 16 us)
+  float v = 0.f, rest = 0.f;
+  auto add = [&](float x) {
+    const float sum = v + x, t = sum - v;
+    rest += (v - (sum - t)) + (x - t);
+    v = sum;
+  };
+#pragma unroll 8
+  for (int k = threadIdx.x / 8; k < p.n_parts; k += kDwThreads / 8) add(p.part[((int64_t)k * 2 + n) * D + col]);
 #pragma unroll
-    for (int k = 1; k < kThreads / 32; ++k) v += s[k][lane];
-    p.t[n].dw[col] = (float)v;
+  for (int o = 8; o < 32; o <<= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v, o), y = __shfl_xor_sync(0xffffffffu, rest, o);
+    add(x);
+    rest += y;
   }
+  if (lane < 8) s[warp][lane] = make_float2(v, rest);
+  __syncthreads();
+  if (warp > 0) return;
+  v = rest = 0.f;
+#pragma unroll
+  for (int k = 0; k < kDwWarps; k += 4) {
+    const float2 x = s[k + lane / 8][lane % 8];
+    add(x.x);
+    rest += x.y;
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v, o), y = __shfl_xor_sync(0xffffffffu, rest, o);
+    add(x);
+    rest += y;
+  }
+  // (an infinite or NaN sum has a NaN rest)
+  if (lane < 8) p.t[n].dw[col] = isfinite(v) ? v + rest : v;
 }
 
 template <int D, bool F16>
-void launch_fwd(const NormParams& p, int layout, dim3 grid, cudaStream_t st) {
+void launch_fwd(const NormParams& p, int layout, unsigned grid, cudaStream_t st) {
   if (layout == kInterleaved) norm_kernel<D, F16, kInterleaved><<<grid, kThreads, 0, st>>>(p);
   else if (layout == kHalf) norm_kernel<D, F16, kHalf><<<grid, kThreads, 0, st>>>(p);
   else norm_kernel<D, F16, kHalfOdd><<<grid, kThreads, 0, st>>>(p);
@@ -299,8 +593,8 @@ void launch_bwd(const NormParams& p, int layout, int grid, cudaStream_t st) {
 template <int D>
 cudaError_t launch_dw(const NormParams& p, bool overlap, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(2 * D / 32);
-  c.blockDim = dim3(kThreads);
+  c.gridDim = dim3(2 * D / 8);
+  c.blockDim = dim3(kDwThreads);
   c.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -319,6 +613,7 @@ int check_weight(const fa_tensor* w, const fa_tensor* x, NormRows& r) {
     return FA_ERR_INVALID_ARG;
   r.w = w->data;
   r.w_kind = f32 ? kWeightF32 : kWeight16;
+  r.w_wide = (reinterpret_cast<uintptr_t>(w->data) & 15u) == 0;
   return FA_OK;
 }
 int check_dw(const fa_tensor* w, const fa_tensor* x, NormRows& r) {
@@ -350,6 +645,8 @@ int check_norm(const fa_tensor* const (&x)[2], const fa_tensor* const (&out)[2],
     heads += h;
     if (heads > INT32_MAX / 1024) return FA_ERR_INVALID_ARG;
     r.heads = (int32_t)h;
+    const int64_t at_once = 32 / (d / 16);
+    r.rounds = (int32_t)((h + at_once - 1) / at_once);
     r.x = static_cast<const uint16_t*>(x[n]->data);
     r.out = static_cast<uint16_t*>(out[n]->data);
     strides_of(x[n], r.x_sb, r.x_ss, r.x_sh);
@@ -390,21 +687,17 @@ int fa_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_w
   cudaError_t e = record(opts->event_begin, st);
   const int d = (int)q->shape[q->ndim - 1], layout = layout_of(interleaved != 0, p.half);
   const bool f16 = q->dtype == FA_DTYPE_F16;
-  // Tokens per CTA: the fewest that one wave of CTAs takes, at most eight; with
-  // one, its heads go over the grid's second dimension too.
-  const int slots = kThreads / (d / 16), sms = sm_count();
-  p.tb = 1;
-  while (p.tb < kMaxTokens && p.rows > (int64_t)sms * kFwdBlocks * p.tb) p.tb *= 2;
-  p.steps = (p.rows + p.tb - 1) / p.tb;
-  int ysplit = 1;
-  if (p.tb == 1) {
-    const int most = (std::max(p.t[0].heads, p.t[1].heads) + slots - 1) / slots;
-    ysplit = p.steps * most <= 8 * sms ? most : 1;
-  }
+  // A warp takes a whole token where that makes two waves of warps, otherwise the
+  // token's rounds are dealt to as many warps as do.
+  const int64_t rounds = p.t[0].rounds + p.t[1].rounds, groups = (p.rows + kWarps - 1) / kWarps;
+  const int64_t ctas = 2 * (int64_t)sm_count() * kFwdBlocks, units = std::min(rounds, (ctas + groups - 1) / std::max<int64_t>(1, groups));
+  p.span = (int32_t)((rounds + units - 1) / units);
+  p.units = (int32_t)((rounds + p.span - 1) / p.span);
+  const int64_t grid = groups * p.units;
+  if (grid > INT32_MAX) return FA_ERR_INVALID_ARG;
   if (e == cudaSuccess && p.rows > 0) {
-    const dim3 grid((unsigned)p.steps, (unsigned)ysplit);
-    if (d == 64) f16 ? launch_fwd<64, true>(p, layout, grid, st) : launch_fwd<64, false>(p, layout, grid, st);
-    else f16 ? launch_fwd<128, true>(p, layout, grid, st) : launch_fwd<128, false>(p, layout, grid, st);
+    if (d == 64) f16 ? launch_fwd<64, true>(p, layout, (unsigned)grid, st) : launch_fwd<64, false>(p, layout, (unsigned)grid, st);
+    else f16 ? launch_fwd<128, true>(p, layout, (unsigned)grid, st) : launch_fwd<128, false>(p, layout, (unsigned)grid, st);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) e = record(opts->event_end, st);
@@ -448,10 +741,13 @@ int fa_qk_norm_rope_bwd(const fa_tensor* dq_out, const fa_tensor* dk_out, const 
   const int d = (int)q->shape[q->ndim - 1], layout = layout_of(interleaved != 0, p.half);
   const bool f16 = q->dtype == FA_DTYPE_F16;
   const int most = std::min(sm_count() * kBwdBlocks, kMaxParts);
-  p.tb = 1;
-  while (p.tb < kMaxTokens && p.rows > (int64_t)most * p.tb) p.tb *= 2;
-  p.steps = (p.rows + p.tb - 1) / p.tb;
-  p.n_parts = (int32_t)std::min<int64_t>(most, p.steps);
+  const int64_t rounds = p.rows * (p.t[0].rounds + p.t[1].rounds);
+  p.n_parts = (int32_t)std::min<int64_t>(most, (rounds + kWarps - 1) / kWarps);
+  for (NormRows& r : p.t) {
+    const int64_t warps = std::max<int64_t>(1, (int64_t)p.n_parts * kWarps);
+    r.share = p.rows * r.rounds / warps;
+    r.more = p.rows * r.rounds % warps;
+  }
   if (e == cudaSuccess && p.rows > 0) {
     if (d == 64) f16 ? launch_bwd<64, true>(p, layout, p.n_parts, st) : launch_bwd<64, false>(p, layout, p.n_parts, st);
     else f16 ? launch_bwd<128, true>(p, layout, p.n_parts, st) : launch_bwd<128, false>(p, layout, p.n_parts, st);
