@@ -14,8 +14,12 @@
 // packed rows takes the cache blocks whose first new row lies in the run.  A
 // team of warps holds one head's block in registers, 16 columns of up to four
 // tokens a thread, so that the maximum and the rounding need one read; old
-// tokens of the block stand beside the new ones as their values.  Other CTAs
-// (the grid's second dimension) rotate the same rows of q.
+// tokens of the block stand beside the new ones as their values.  Other CTAs work
+// on q, a warp to a token as in qknorm.cu.
+// Measured (4 prompts of 4096 tokens, 32 + 8 heads, d 128, bf16, norms and rotation, pages
+// of 64 keys): 92 us (4.0 TB/s), 45 of it k and v and 43 q, both by their instructions;
+// 64 single tokens 8 us.  Three CTAs per SM, their values made twice, took 112 us, q's CTAs
+// between those of k and v 94.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -23,8 +27,8 @@
 
 #include <cuda_runtime.h>
 
+#include "norm_rows.cuh"
 #include "q8_device.cuh"
-#include "rope_common.cuh"
 
 using namespace mfa;
 
@@ -33,6 +37,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPasses = 4;  // tokens of a block per thread at most
+constexpr int kAppendBlocks = 2;  // CTAs per SM
+constexpr int kAhead = 4;   // rounds of q under way
 
 struct Q8Params {
   const uint16_t *q, *k, *v;
@@ -42,7 +48,6 @@ struct Q8Params {
   float* scale[2];
   int64_t c_sb[2], c_ss[2], c_sh[2], s_sb[2], s_ss[2], s_sh[2];
   int32_t hq, hk;
-  FastDiv div_hq;
   int64_t rows;
   int32_t S;
   const int32_t* cu_q;
@@ -57,11 +62,12 @@ struct Q8Params {
   const double* inv_freq;
   int32_t half;
   float mscale, eps;  // eps 0: no norm
-  const void* w[2];   // weights of q, k
-  int32_t w_f32[2];
-  int32_t block, team;  // tokens of a block, warps that hold one
+  HeadWeight w[2];    // of q, k
+  int32_t block, block_shift, team;  // tokens of a block (and its log2), warps that hold one
+  FastDiv div_page;
   int32_t span;         // packed rows per CTA
-  int32_t kv_y, q_y;    // CTAs per run for k and v, for q
+  int32_t kv_y, kv_ctas;  // CTAs per run for k and v, and all of them; the others are q's
+  int32_t q_units, q_span, q_rounds;  // q: warps of a token, rounds of heads of a warp and of a token
   WsHeader* ws;
 };
 
@@ -90,82 +96,70 @@ __device__ __forceinline__ bool seq_bad(const Q8Params& p, int64_t L, int64_t c0
   return L < 0 || n < 0 || c0 < 0 || c0 + n > p.rows || L + n > p.cap;
 }
 
-template <bool F16>
-__device__ __forceinline__ void load_weight(const void* w, bool f32, Columns at, float (&x)[16]) {
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int col = e < 8 ? at.xa + e : at.xb + e - 8;
-    x[e] = !w ? 1.f : f32 ? __ldg(static_cast<const float*>(w) + col) : to_float<F16>(__ldg(static_cast<const uint16_t*>(w) + col));
-  }
+// Where sequence s of the step has its rows; bad: its lengths do not fit.
+struct Step {
+  int64_t c0, n, L;
+  bool bad;
+};
+__device__ __forceinline__ Step step_of(const Q8Params& p, int s) {
+  Step t;
+  t.c0 = p.cu_q ? __ldg(p.cu_q + s) : (int64_t)s * p.S;
+  t.n = p.cu_q ? (int64_t)__ldg(p.cu_q + s + 1) - t.c0 : p.S;
+  t.L = __ldg(p.cache_len + s);
+  t.bad = seq_bad(p, t.L, t.c0, t.n);
+  return t;
 }
-
-// The row's columns x divided by its root mean square, times w.
-template <int kLanes>
-__device__ __forceinline__ void norm16(float (&x)[16], const float (&w)[16], float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float inv = rsqrtf(fmaf(ss, 1.f / (16 * kLanes), eps));
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * w[e];
+__device__ __forceinline__ int position_of(const Q8Params& p, int s, int64_t row, int64_t i, int64_t L) {
+  return p.positions ? __ldg(p.positions + (p.cu_q ? row * p.pos_ss : s * p.pos_sb + i * p.pos_ss)) : (int)(L + i);
 }
 
 // One head's block of a cache (n_new new tokens after n_old old ones), by a team of warps.
-// src: the first new token's row of the head, or null (a team without a head).
+// va, vb: this lane's columns of tokens tok (new rows, or old codes in x and y).
 template <int D, bool F16, int LAYOUT, bool IS_K>
-__device__ __forceinline__ void enter_block(const Q8Params& p, const uint16_t* src, int64_t src_ss, uint8_t* code,
-                                            int64_t code_ss, float* scale, int n_old, int n_new, const float2* cs,
-                                            const float (&w)[16], float* row_mem, float* s_top) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // tokens of a warp's pass
+__device__ __forceinline__ void enter_block(const Q8Params& p, const uint4 (&va)[kPasses], const uint4 (&vb)[kPasses],
+                                            const int (&tok)[kPasses], bool any, uint8_t* code, int64_t code_ss, float* scale,
+                                            float before, int n_old, int n_new, const float2* cs, const Weights<D / 16>& s_w,
+                                            float* row_mem, float* s_top) {
+  constexpr int kLanes = D / 16, kLayout = IS_K ? LAYOUT : kInterleaved;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % kLanes;
   const int member = warp % p.team;
-  const Columns at = columns_of<IS_K ? LAYOUT : kInterleaved>(c, p.half);
-  float x[kPasses][16];
-  float before = 0.f;
-  if (src && n_old > 0) before = *scale;
+  const Columns at = lane_columns<D, kLayout>(c, p.half);
   const float held = pow2f(scale_exponent(before));
-  int tok[kPasses];
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) tok[k] = (member * kPasses + k) * kRows + lane / kLanes;
-  uint4 va[kPasses], vb[kPasses];
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    va[k] = vb[k] = make_uint4(0, 0, 0, 0);
-    if (!src || tok[k] >= n_old + n_new) continue;
-    if (tok[k] < n_old) {
-      const uint2 a = *reinterpret_cast<const uint2*>(code + tok[k] * code_ss + at.xa);
-      const uint2 b = *reinterpret_cast<const uint2*>(code + tok[k] * code_ss + at.xb);
-      va[k].x = a.x; va[k].y = a.y; vb[k].x = b.x; vb[k].y = b.y;
-    } else {
-      const uint16_t* s = src + (tok[k] - n_old) * src_ss;
-      va[k] = *reinterpret_cast<const uint4*>(s + at.xa);
-      vb[k] = *reinterpret_cast<const uint4*>(s + at.xb);
-    }
-  }
+  Pairs y[kPasses];
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const bool old = tok[k] < n_old;
-    unpack16<F16>(va[k], vb[k], x[k]);
+    y[k] = unpack_pairs<F16, kLayout>(va[k], vb[k]);
     if constexpr (IS_K) {
-      if (p.eps > 0.f) norm16<kLanes>(x[k], w, p.eps);
-      if (p.half > 0) rotate16<LAYOUT>(x[k], cs + min(max(tok[k] - n_old, 0), max(n_new - 1, 0)) * (D / 2), c, p.half, row_mem);
+      if (p.eps > 0.f) {
+        scale_by(y[k], rsqrtf(fmaf(dot<kLanes>(y[k], y[k]), 1.f / D, p.eps)));
+        multiply(y[k], weight_of<kLanes>(s_w, 1, c));
+      }
+      if (p.half > 0) {
+        const float2* of = cs + min(max(tok[k] - n_old, 0), max(n_new - 1, 0)) * (D / 2);
+        Turns tw;
+        load_turns<D, LAYOUT>(of, c, tw);
+        rotate<D, LAYOUT>(y[k], tw, of, c, p.half, row_mem);
+      }
     }
-    if (old) {
+    if (tok[k] < n_old) {
       const uint32_t u[4] = {va[k].x, va[k].y, vb[k].x, vb[k].y};
+      float x[16];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 a = e4m3x2_to_float2((uint16_t)u[e]), b = e4m3x2_to_float2((uint16_t)(u[e] >> 16));
-        x[k][4 * e] = a.x * held; x[k][4 * e + 1] = a.y * held;
-        x[k][4 * e + 2] = b.x * held; x[k][4 * e + 3] = b.y * held;
+        x[4 * e] = a.x * held; x[4 * e + 1] = a.y * held;
+        x[4 * e + 2] = b.x * held; x[4 * e + 3] = b.y * held;
       }
+      y[k] = pairs_of<kLayout>(x);
     } else if (tok[k] < n_old + n_new) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[k][e] = fmaf(x[k][e], 0.f, x[k][e]);  // an infinity becomes a NaN, which the maximum leaves out
-        top = fmaxf(top, fabsf(x[k][e]));
+      for (int i = 0; i < 4; ++i) {
+        // an infinity becomes a NaN, which the maximum leaves out
+        y[k].a[i] = fma2(y[k].a[i], both(0.f), y[k].a[i]);
+        y[k].b[i] = fma2(y[k].b[i], both(0.f), y[k].b[i]);
+        top = fmaxf(top, fmaxf(fabsf(y[k].a[i].x), fabsf(y[k].a[i].y)));
+        top = fmaxf(top, fmaxf(fabsf(y[k].b[i].x), fabsf(y[k].b[i].y)));
       }
     }
   }
@@ -180,36 +174,106 @@ __device__ __forceinline__ void enter_block(const Q8Params& p, const uint16_t* s
     for (int m = 0; m < p.team; ++m) top = fmaxf(top, s_top[w0 + m]);
     meet();
   }
-  if (!src) return;
   const int e_old = scale_exponent(before), e_new = block_exponent(top);
   const bool grows = n_old == 0 || e_new > e_old;
   const int e = grows ? e_new : e_old;
-  if (grows && member == 0 && lane == 0) *scale = pow2f(e);
+  if (any && grows && member == 0 && lane == 0) *scale = pow2f(e);
   const float down = pow2f(-e);
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    if (tok[k] >= n_old + n_new || (tok[k] < n_old && !grows)) continue;
+    if (!any || tok[k] >= n_old + n_new || (tok[k] < n_old && !grows)) continue;
+    scale_by(y[k], down);
+    float x[16];
+    columns_from<kLayout>(y[k], x);
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      u[i] = to_e4m3x4(x[k][4 * i] * down, x[k][4 * i + 1] * down, x[k][4 * i + 2] * down, x[k][4 * i + 3] * down);
+    for (int i = 0; i < 4; ++i) u[i] = to_e4m3x4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     *reinterpret_cast<uint2*>(code + tok[k] * code_ss + at.xa) = make_uint2(u[0], u[1]);
     *reinterpret_cast<uint2*>(code + tok[k] * code_ss + at.xb) = make_uint2(u[2], u[3]);
   }
 }
 
+// q's token of this warp: its rounds r0 .. of heads.
 template <int D, bool F16, int LAYOUT>
-__global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_constant__ Q8Params p) {
-  constexpr int kLanes = D / 16, kSlots = kThreads / kLanes;
-  extern __shared__ float2 cs[];  // [block][D / 2]
+__device__ __forceinline__ void q_rows(const Q8Params& p, int64_t row, int r0, float2* cs, const Weights<D / 16>& s_w, float* row_mem) {
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+  const int lane = threadIdx.x & 31, c = lane % kLanes, slot = lane / kLanes, r1 = min(r0 + p.q_span, p.q_rounds);
+  const Columns at = lane_columns<D, LAYOUT>(c, p.half);
+  const int b = p.cu_q ? 0 : (int)row / p.S;
+  const int64_t i = p.cu_q ? row : row - (int64_t)b * p.S;
+  const uint16_t* src = p.q + b * p.q_sb + i * p.q_ss;
+  uint4 va[kAhead], vb[kAhead];
+  auto load = [&](int r, uint4& x, uint4& y) {
+    const int h = r * kHeads + slot;
+    x = y = make_uint4(0, 0, 0, 0);
+    if (r < r1 && h < p.hq) {
+      x = *reinterpret_cast<const uint4*>(src + h * p.q_sh + at.xa);
+      y = *reinterpret_cast<const uint4*>(src + h * p.q_sh + at.xb);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) load(r0 + k, va[k], vb[k]);
+  const int s = p.cu_q ? find_seq(p.cu_q, p.n_seq, row, lane) : b;
+  if (s < 0) return;
+  const Step st = step_of(p, s);
+  if (st.bad) return;
+  Turns tw;
+  if (p.half > 0) {
+    const int pos = position_of(p, s, row, p.cu_q ? row - st.c0 : i, st.L);
+    uint64_t u[2];
+    turn_steps(p.inv_freq, p.half, lane, u);
+    make_turns<LAYOUT>(pos, u, p.half, p.mscale, false, lane, cs);
+    load_turns<D, LAYOUT>(cs, c, tw);
+  }
+  uint16_t* dst = p.q_out + b * p.qo_sb + i * p.qo_ss;
+#pragma unroll 1
+  for (int r = r0; r < r1; r += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (r + k >= r1) break;
+      uint4 ya = va[k], yb = vb[k];
+      load(r + k + kAhead, va[k], vb[k]);
+      if (p.eps > 0.f || p.half > 0) {  // (else the bits are copied)
+        Pairs x = unpack_pairs<F16, LAYOUT>(ya, yb);
+        if (p.eps > 0.f) {
+          scale_by(x, rsqrtf(fmaf(dot<kLanes>(x, x), 1.f / D, p.eps)));
+          multiply(x, weight_of<kLanes>(s_w, 0, c));
+        }
+        if (p.half > 0) rotate<D, LAYOUT>(x, tw, cs, c, p.half, row_mem);
+        pack_pairs<F16, LAYOUT>(x, ya, yb);
+      }
+      const int h = (r + k) * kHeads + slot;
+      if (h < p.hq) {
+        *reinterpret_cast<uint4*>(dst + h * p.qo_sh + at.xa) = ya;
+        *reinterpret_cast<uint4*>(dst + h * p.qo_sh + at.xb) = yb;
+      }
+    }
+  }
+}
+
+template <int D, bool F16, int LAYOUT>
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) append_q8_kernel(const __grid_constant__ Q8Params p) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kSlots = kThreads / kLanes;
+  extern __shared__ __align__(16) float2 cs[];  // [block, at least the warps][D / 2]
+  __shared__ Weights<kLanes> s_w;
   __shared__ float s_row[LAYOUT == kHalfOdd ? kSlots * D : 1];
   __shared__ float s_top[kWarps];
-  __shared__ int s_seq[kQ8MaxBlock], s_i[kQ8MaxBlock], s_pos[kQ8MaxBlock];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row0 = (int64_t)blockIdx.x * p.span;
-  const int slot = tid / kLanes, c = tid % kLanes;
-  float* row_mem = s_row + (LAYOUT == kHalfOdd ? slot * D : 0);
+  __shared__ int s_seq[kQ8MaxBlock], s_i[kQ8MaxBlock];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = tid % kLanes;
+  float* row_mem = s_row + (LAYOUT == kHalfOdd ? tid / kLanes * D : 0);
 
+  if ((int)blockIdx.x >= p.kv_ctas) {
+    const uint32_t x = blockIdx.x - p.kv_ctas, group = x / (uint32_t)p.q_units;
+    const int64_t row = (int64_t)group * kWarps + warp;
+    if (p.eps > 0.f) stage_weights<F16, LAYOUT, kLanes>(p.w[0], p.w[1], p.half, s_w);
+    if (row < p.rows) q_rows<D, F16, LAYOUT>(p, row, (int)(x - group * p.q_units) * p.q_span, cs + warp * (D / 2), s_w, row_mem);
+    return;
+  }
+
+  // ------------------------------------------------------------------ k and v
+  const uint32_t run = blockIdx.x / (uint32_t)p.kv_y;
+  const int y = (int)(blockIdx.x - run * p.kv_y);
+  const int64_t row0 = (int64_t)run * p.span;
   // ---- the run's rows: sequence (-1: none, or one whose lengths do not fit) and place in it
   int s0 = -1;
   if (p.cu_q && p.n_seq > 0) {
@@ -226,128 +290,90 @@ __global__ void __launch_bounds__(kThreads, 2) append_q8_kernel(const __grid_con
   }
   if (tid < p.span) {
     const int64_t row = row0 + tid;
-    int s = -1, i = 0, pos = 0;
-    if (row < p.rows) s = p.cu_q ? (s0 >= 0 ? seq_from(p.cu_q, p.n_seq, s0, row) : -1) : (int)(row / p.S);
+    int s = -1, i = 0;
+    if (row < p.rows) s = p.cu_q ? (s0 >= 0 ? seq_from(p.cu_q, p.n_seq, s0, row) : -1) : (int)((uint32_t)row / (uint32_t)p.S);
     if (s >= 0) {
-      const int64_t c0 = p.cu_q ? __ldg(p.cu_q + s) : (int64_t)s * p.S;
-      const int64_t n = p.cu_q ? (int64_t)__ldg(p.cu_q + s + 1) - c0 : p.S;
-      const int64_t L = __ldg(p.cache_len + s);
-      i = (int)(row - c0);
-      if (seq_bad(p, L, c0, n)) s = -1;  // recorded below, once per sequence
-      else pos = p.positions ? __ldg(p.positions + (p.cu_q ? row * p.pos_ss : s * p.pos_sb + i * p.pos_ss)) : (int)(L + i);
+      const Step st = step_of(p, s);
+      i = (int)(row - st.c0);
+      if (st.bad) s = -1;  // recorded below, once per sequence
+      else if (i > 0 && ((int)st.L + i & p.block - 1) != 0) s = -1;  // not the block's first new row
     }
     s_seq[tid] = s;
     s_i[tid] = i;
-    s_pos[tid] = pos;
   }
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  if (blockIdx.x == 0) {
     for (int s = tid; s < p.n_seq; s += kThreads) {
-      const int64_t L = __ldg(p.cache_len + s), c0 = p.cu_q ? __ldg(p.cu_q + s) : (int64_t)s * p.S;
-      const int64_t n = p.cu_q ? (int64_t)__ldg(p.cu_q + s + 1) - c0 : p.S;
-      const bool bad = seq_bad(p, L, c0, n);
-      if (bad) q8_error(p.ws, (uint32_t)s);
-      if (p.len_out) p.len_out[s] = (int32_t)(bad ? L : L + n);
+      const Step st = step_of(p, s);
+      if (st.bad) q8_error(p.ws, (uint32_t)s);
+      if (p.len_out) p.len_out[s] = (int32_t)(st.bad ? st.L : st.L + st.n);
     }
   }
-  __syncthreads();
-
   // this thread's pair and its step, for the turns it makes
   const int groups = p.half > 0 ? kThreads / p.half : 0, pair = p.half > 0 ? tid % p.half : 0;
   const uint64_t step = p.half > 0 ? turn_step(__ldg(p.inv_freq + pair)) : 0;
+  stage_weights<F16, LAYOUT, kLanes>(p.w[0], p.w[1], p.half, s_w);  // (and the rows are there)
 
-  if ((int)blockIdx.y >= p.kv_y) {
-    // ---------------------------------------------------------------- q
-    for (int t = p.half > 0 ? tid / p.half : p.span; t < p.span && tid < groups * p.half; t += groups)
-      cs[t * (D / 2) + pair] = position_turn(s_pos[t], step, p.mscale, false);
-    __syncthreads();
-    const Columns at = columns_of<LAYOUT>(c, p.half);
-    float w[16];
-    load_weight<F16>(p.w[0], p.w_f32[0], at, w);
-    const int n = p.span * p.hq;
-    for (int e0 = (blockIdx.y - p.kv_y) * kSlots; e0 < n; e0 += 2 * kSlots * p.q_y) {
-      uint4 va[2], vb[2];
-      uint16_t* dst[2];
-      int t[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int e = e0 + k * kSlots * p.q_y + slot;
-        t[k] = 0;
-        dst[k] = nullptr;
-        va[k] = vb[k] = make_uint4(0, 0, 0, 0);
-        if (e < n) {
-          t[k] = divide(e, p.div_hq);
-          const int h = e - t[k] * p.hq, s = s_seq[t[k]];
-          if (s >= 0) {
-            const int64_t b = p.cu_q ? 0 : s, i = p.cu_q ? row0 + t[k] : s_i[t[k]];
-            const uint16_t* src = p.q + b * p.q_sb + i * p.q_ss + h * p.q_sh;
-            dst[k] = p.q_out + b * p.qo_sb + i * p.qo_ss + h * p.qo_sh;
-            va[k] = *reinterpret_cast<const uint4*>(src + at.xa);
-            vb[k] = *reinterpret_cast<const uint4*>(src + at.xb);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (p.eps > 0.f || p.half > 0) {  // (else the bits are copied)
-          float x[16];
-          unpack16<F16>(va[k], vb[k], x);
-          if (p.eps > 0.f) norm16<kLanes>(x, w, p.eps);
-          if (p.half > 0) rotate16<LAYOUT>(x, cs + t[k] * (D / 2), c, p.half, row_mem);
-          pack16<F16>(x, va[k], vb[k]);
-        }
-        if (dst[k]) {
-          *reinterpret_cast<uint4*>(dst[k] + at.xa) = va[k];
-          *reinterpret_cast<uint4*>(dst[k] + at.xb) = vb[k];
-        }
-      }
-    }
-    return;
-  }
-
-  // ------------------------------------------------------------------ k and v
-  const int teams = kWarps / p.team, team = warp / p.team;
-  float w[16];
-  load_weight<F16>(p.w[1], p.w_f32[1], columns_of<LAYOUT>(c, p.half), w);
+  const int teams = kWarps / p.team, team = warp / p.team, member = warp % p.team;
+  uint32_t starts = 0;  // of these 32 rows, those that begin a block, from t on
   for (int t = 0; t < p.span; ++t) {
+    if (t % 32 == 0) starts = __ballot_sync(0xffffffffu, t + lane < p.span && s_seq[t + lane] >= 0);
+    if (starts == 0) {
+      t |= 31;
+      continue;
+    }
+    t = t & ~31 | __ffs(starts) - 1;
+    starts &= starts - 1;
     const int s = s_seq[t], i = s_i[t];
-    if (s < 0) continue;
-    const int64_t L = __ldg(p.cache_len + s), j = L + i;
-    if (i > 0 && j % p.block != 0) continue;  // not the block's first new row
-    const int64_t c0 = p.cu_q ? __ldg(p.cu_q + s) : (int64_t)s * p.S;
-    const int n_left = (int)((p.cu_q ? (int64_t)__ldg(p.cu_q + s + 1) - c0 : p.S) - i);
-    const int n_old = (int)(j % p.block), n_new = min(p.block - n_old, n_left);
-    const int64_t j0 = j - n_old;
+    const Step st = step_of(p, s);
+    const int j = (int)st.L + i, n_old = j & p.block - 1, n_new = min(p.block - n_old, (int)st.n - i), j0 = j - n_old;
     int64_t page = s, r = j0;
     if (p.block_table) {
-      page = __ldg(p.block_table + s * p.bt_stride + j0 / p.page_size);
-      r = j0 % p.page_size;
+      const int column = divide(j0, p.div_page);
+      page = __ldg(p.block_table + s * p.bt_stride + column);
+      r = j0 - (int64_t)column * p.page_size;
       if (page < 0 || page >= p.num_pages) {
-        if (blockIdx.y == 0 && tid == 0) q8_error(p.ws, (uint32_t)page);
+        if (y == 0 && tid == 0) q8_error(p.ws, (uint32_t)page);
         continue;
       }
     }
-    if (p.half > 0 && tid < groups * p.half) {
-      const int64_t row = row0 + t;
-      for (int m = tid / p.half; m < n_new; m += groups) {
-        const int pos = p.positions ? __ldg(p.positions + (p.cu_q ? (row + m) * p.pos_ss : s * p.pos_sb + (i + m) * p.pos_ss)) : (int)(j + m);
-        cs[m * (D / 2) + pair] = position_turn(pos, step, p.mscale, false);
-      }
-    }
-    __syncthreads();
     const int64_t sb = p.cu_q ? 0 : s, si = p.cu_q ? row0 + t : i;
-    for (int e0 = blockIdx.y * teams; e0 < 2 * p.hk; e0 += teams * p.kv_y) {
+    for (int e0 = y * teams; e0 < 2 * p.hk; e0 += teams * p.kv_y) {
       // (a team's head is K or V by itself; a round may hold both)
-      const int e = e0 + team, h = e < p.hk ? e : e - p.hk;
-      const bool any = e < 2 * p.hk;
-      const int which = e < p.hk ? 0 : 1;
+      const int e = min(e0 + team, 2 * p.hk - 1), which = e < p.hk ? 0 : 1, h = e - which * p.hk;
+      const bool any = e0 + team < 2 * p.hk;
+      const uint16_t* src = which == 0 ? p.k + sb * p.k_sb + si * p.k_ss + h * p.k_sh : p.v + sb * p.v_sb + si * p.v_ss + h * p.v_sh;
+      const int64_t src_ss = which == 0 ? p.k_ss : p.v_ss, code_ss = p.c_ss[which];
       uint8_t* code = p.code[which] + page * p.c_sb[which] + r * p.c_ss[which] + h * p.c_sh[which];
-      float* scale = p.scale[which] + page * p.s_sb[which] + (r / p.block) * p.s_ss[which] + h * p.s_sh[which];
-      if (which == 0)
-        enter_block<D, F16, LAYOUT, true>(p, p.k + sb * p.k_sb + si * p.k_ss + h * p.k_sh, p.k_ss, code, p.c_ss[0], scale, n_old,
-                                          n_new, cs, w, row_mem, s_top);
-      else
-        enter_block<D, F16, LAYOUT, false>(p, any ? p.v + sb * p.v_sb + si * p.v_ss + h * p.v_sh : nullptr, p.v_ss, code, p.c_ss[1],
-                                           scale, n_old, n_new, cs, w, row_mem, s_top);
+      float* scale = p.scale[which] + page * p.s_sb[which] + (r >> p.block_shift) * p.s_ss[which] + h * p.s_sh[which];
+      const Columns at = which == 0 ? lane_columns<D, LAYOUT>(c, p.half) : lane_columns<D, kInterleaved>(c, p.half);
+      int tok[kPasses];
+      uint4 va[kPasses], vb[kPasses];
+      const float before = any && n_old > 0 ? *scale : 0.f;
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        tok[k] = (member * kPasses + k) * kRows + lane / kLanes;
+        va[k] = vb[k] = make_uint4(0, 0, 0, 0);
+        if (!any || tok[k] >= n_old + n_new) continue;
+        if (tok[k] < n_old) {
+          const uint2 a = *reinterpret_cast<const uint2*>(code + tok[k] * code_ss + at.xa);
+          const uint2 b = *reinterpret_cast<const uint2*>(code + tok[k] * code_ss + at.xb);
+          va[k].x = a.x; va[k].y = a.y; vb[k].x = b.x; vb[k].y = b.y;
+        } else {
+          const uint16_t* from = src + (tok[k] - n_old) * src_ss;
+          va[k] = *reinterpret_cast<const uint4*>(from + at.xa);
+          vb[k] = *reinterpret_cast<const uint4*>(from + at.xb);
+        }
+      }
+      if (e0 == y * teams && e0 < p.hk && p.half > 0) {
+        // the block's turns, while the rows come
+        if (tid < groups * p.half) {
+          for (int m = tid / p.half; m < n_new; m += groups)
+            cs[m * (D / 2) + turn_place<LAYOUT>(pair)] = position_turn(position_of(p, s, row0 + t + m, i + m, st.L), step, p.mscale, false);
+        }
+        __syncthreads();
+      }
+      if (which == 0) enter_block<D, F16, LAYOUT, true>(p, va, vb, tok, any, code, code_ss, scale, before, n_old, n_new, cs, s_w, row_mem, s_top);
+      else enter_block<D, F16, LAYOUT, false>(p, va, vb, tok, any, code, code_ss, scale, before, n_old, n_new, cs, s_w, row_mem, s_top);
     }
     __syncthreads();  // the turns are read
   }
@@ -378,7 +404,7 @@ struct ReadParams {
 // (one load) into 16 values (two stores), four of them in flight.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) read_q8_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int kChunks = D / 16, kAhead = 4;
+  constexpr int kChunks = D / 16;
   __shared__ int64_t s_page[kReadRows], s_at[kReadRows], s_b[kReadRows], s_i[kReadRows];  // page (-1: none), row in it; output row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = (int64_t)blockIdx.x * kReadRows;
@@ -513,7 +539,7 @@ int check_error_word(const fa_opts* opts) {
 
 template <int D, bool F16, int LAYOUT>
 cudaError_t launch_append(const Q8Params& p, dim3 grid, cudaStream_t st) {
-  const int smem = p.block * (D / 2) * (int)sizeof(float2);
+  const int smem = std::max(p.block, kWarps) * (D / 2) * (int)sizeof(float2);
   static std::atomic<uint64_t> done{0};  // devices where the kernel may have all the shared memory it can want
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -535,17 +561,6 @@ cudaError_t launch_append(const Q8Params& p, int layout, dim3 grid, cudaStream_t
 
 cudaError_t record(void* ev, cudaStream_t st) {
   return ev ? cudaEventRecord(static_cast<cudaEvent_t>(ev), st) : cudaSuccess;
-}
-
-int check_weight(const fa_tensor* w, const fa_tensor* x, const void** at, int32_t* is_f32) {
-  if (!w) return FA_OK;
-  const bool f32 = w->dtype == FA_DTYPE_F32;
-  if (!w->data || (!f32 && w->dtype != x->dtype) || w->ndim != 1 || w->shape[0] != x->shape[x->ndim - 1] || w->stride[0] != 1 ||
-      (reinterpret_cast<uintptr_t>(w->data) & (f32 ? 3u : 1u)) != 0)
-    return FA_ERR_INVALID_ARG;
-  *at = w->data;
-  *is_f32 = f32;
-  return FA_OK;
 }
 
 }  // namespace
@@ -598,15 +613,13 @@ int fa_kvcache_append_q8(const fa_tensor* q, const fa_tensor* q_out, const fa_te
   }
   if (hq > INT32_MAX / 1024) return FA_ERR_INVALID_ARG;
   p.hq = (int32_t)hq;
-  p.div_hq = make_fastdiv((uint32_t)std::max<int64_t>(hq, 1));
   p.k = static_cast<const uint16_t*>(k_new->data);
   p.v = static_cast<const uint16_t*>(v_new->data);
   strides_of(k_new, p.k_sb, p.k_ss, p.k_sh);
   strides_of(v_new, p.v_sb, p.v_ss, p.v_sh);
   if (!(eps >= 0.f) || !std::isfinite(eps) || (eps == 0.f && (q_weight || k_weight)) || (!q && q_weight)) return FA_ERR_INVALID_ARG;
   p.eps = eps;
-  if ((rc = check_weight(q_weight, k_new, &p.w[0], &p.w_f32[0])) || (rc = check_weight(k_weight, k_new, &p.w[1], &p.w_f32[1])))
-    return rc;
+  if ((rc = check_weight(q_weight, k_new, p.w[0])) || (rc = check_weight(k_weight, k_new, p.w[1]))) return rc;
   if (positions && (rc = check_positions(positions, k_new, p))) return rc;
   if (inv_freq) {
     if ((rc = check_freq(inv_freq, d, &p.half))) return rc;
@@ -622,6 +635,8 @@ int fa_kvcache_append_q8(const fa_tensor* q, const fa_tensor* q_out, const fa_te
   }
   if ((rc = check_error_word(opts)) || (rc = check_device())) return rc;
   p.ws = static_cast<WsHeader*>(opts->workspace);
+  p.div_page = make_fastdiv((uint32_t)std::max(p.page_size, 1));
+  while ((1 << p.block_shift) < p.block) ++p.block_shift;
 
   TraceRange tr("mfa.kvcache_append_q8");
   cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
@@ -633,13 +648,29 @@ int fa_kvcache_append_q8(const fa_tensor* q, const fa_tensor* q_out, const fa_te
   p.span = p.block;
   while (p.span > 1 && p.rows < (int64_t)p.span * sms) p.span /= 2;
   const int64_t runs = (p.rows + p.span - 1) / p.span;
-  const int teams = kWarps / p.team, slots = kThreads / ((int)d / 16);
-  const int kv_most = (2 * p.hk + teams - 1) / teams, q_most = (int)std::min<int64_t>(1024, ((int64_t)p.span * hq + slots - 1) / slots);
-  const int room = (int)std::max<int64_t>(1, 4 * sms / std::max<int64_t>(runs, 1));  // CTAs per run, about
-  p.kv_y = std::min(kv_most, room);
-  p.q_y = hq ? std::min(q_most, std::max(room, (int)((hq + 2 * hk - 1) / (2 * hk)))) : 0;
+  // Their heads go over more CTAs where the runs do not make four waves.
+  const int64_t wave = (int64_t)sms * kAppendBlocks;
+  const int teams = kWarps / p.team, kv_most = (2 * p.hk + teams - 1) / teams;
+  const int64_t kv_want = std::min<int64_t>(kv_most, (4 * wave + runs - 1) / std::max<int64_t>(runs, 1));
+  const int64_t kv_each = (kv_most + kv_want - 1) / kv_want;  // (as many rounds to each)
+  p.kv_y = (int32_t)((kv_most + kv_each - 1) / kv_each);
+  const int64_t kv_ctas = std::max<int64_t>(runs, 1) * p.kv_y;
+  // q: a warp takes a whole token where that makes two waves, else fewer of its heads.
+  int64_t q_ctas = 0;
+  p.q_units = 1;
+  if (hq && p.rows > 0) {
+    const int at_once = 512 / (int)d;
+    const int64_t groups = (p.rows + kWarps - 1) / kWarps;
+    p.q_rounds = (p.hq + at_once - 1) / at_once;
+    const int64_t units = std::min<int64_t>(p.q_rounds, (2 * wave + groups - 1) / groups);
+    p.q_span = (int32_t)((p.q_rounds + units - 1) / units);
+    p.q_units = (p.q_rounds + p.q_span - 1) / p.q_span;
+    q_ctas = groups * p.q_units;
+  }
+  if (kv_ctas + q_ctas > INT32_MAX) return FA_ERR_INVALID_ARG;
+  p.kv_ctas = (int32_t)kv_ctas;
   if (e == cudaSuccess && (runs > 0 || n_seq > 0)) {
-    const dim3 grid((unsigned)std::max<int64_t>(runs, 1), (unsigned)(p.kv_y + p.q_y));
+    const dim3 grid((unsigned)(kv_ctas + q_ctas));
     const int layout = layout_of(interleaved != 0, p.half);
     const bool f16 = k_new->dtype == FA_DTYPE_F16;
     if (d == 64) e = f16 ? launch_append<64, true>(p, layout, grid, st) : launch_append<64, false>(p, layout, grid, st);
