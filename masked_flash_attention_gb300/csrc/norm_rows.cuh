@@ -179,12 +179,13 @@ __device__ __forceinline__ void make_turns(int pos, const uint64_t (&u)[2], int 
 // Those of lane c's pairs (of its pairs that are not rotated: anything).
 template <int D, int LAYOUT>
 __device__ __forceinline__ void load_turns(const float2* cs, int c, Turns& tw) {
-  if (LAYOUT == kHalfOdd) return;
+  if constexpr (LAYOUT != kHalfOdd) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(cs + turn_place<LAYOUT>(first_pair<D, LAYOUT>(c, k)));
-    tw.co[k] = make_float2(v.x, v.z);
-    tw.sn[k] = make_float2(v.y, v.w);
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(cs + turn_place<LAYOUT>(first_pair<D, LAYOUT>(c, k)));
+      tw.co[k] = make_float2(v.x, v.z);
+      tw.sn[k] = make_float2(v.y, v.w);
+    }
   }
 }
 
