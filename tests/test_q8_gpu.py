@@ -688,3 +688,86 @@ def test_shared_and_repeated_pages():
     c["bt"][1, :3] = c["bt"][0, :3]
     c["bt"][2, 4] = c["bt"][2, 1]
     check(c)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [4, 30]])
+def test_wait_that_runs_out_is_reported(q_lens):
+    """The first copy of K is never sent (FA_DEBUG_WITHHOLD): the bounded waits give up, the
+    status is reported, and the next call on the workspace is right."""
+    m = fa()
+    c = chunk_case(27, q_lens, [60, 200])
+    _, _, ws = run(c, check=False, debug_flags=m.FA_DEBUG_WITHHOLD)
+    assert m.fa_check_device_error(ws)[0] == m._lib.FA_ERR_DEVICE_TIMEOUT
+    out, lse, _ = run(c, workspace=ws)
+    assert_close(c, out, lse, oracle(c))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 2], [5000, 60, 700]), ([300, 1, 90], [1500, 60, 700])])
+def test_two_streams_at_once(q_lens, kv_lens):
+    """Two steps on two streams, each with its own workspace, a few times over."""
+    m = fa()
+    cs = [chunk_case(28 + i, q_lens, kv_lens, hq=8, window_left=900 + i, sink_keys=3) for i in range(2)]
+    on = [on_device(c) for c in cs]
+    st = [{k: dev(c[k]) for k in ("q", "cu", "lens", "bt")} for c in cs]
+
+    def step(i, stream=None):
+        return m.fa_fwd_chunk_q8(st[i]["q"], *on[i], st[i]["lens"], cu_seqlens_q=st[i]["cu"], block_table=st[i]["bt"], max_seqlen_q=max(q_lens),
+                                 max_seqlen_k=max(kv_lens), workspace=ws[i], stream=stream, **cs[i]["params"])[:2]
+    ws = [torch.zeros(64 << 20, dtype=torch.uint8, device=DEV) for _ in cs]
+    one = [[t.clone() for t in step(i)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        got = [step(i, s.cuda_stream) for i, s in enumerate(streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for a, b in zip(one, got) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d", [(3000, 40, 3, 128), (900, 17, 8, 64), (6000, 9, 1, 64)])
+def test_append_shares_of_warps(rows, hq, hkv, d):
+    """q's heads in one share of rounds and in several, the last one not full; weights off a 16-byte boundary."""
+    g = gen(rows)
+    c = append_case(rows, [7, 0, 40], [rows // 2, 3, rows - rows // 2 - 3], hkv=hkv, d=d, page=32, block=32, hq=hq)
+    w = (1 + 0.3 * torch.randn(2, d + 1, generator=g)).to(BF)
+    qo, on, _, _ = run_append(c, freqs(d), eps=1e-5, q_weight=dev(w)[0, 1:], k_weight=dev(w)[1, 1:])
+    qa, on2, _, _ = run_append(c, freqs(d), eps=1e-5, q_weight=w[0, 1:].clone(), k_weight=w[1, 1:].clone())
+    assert torch.equal(qo, qa) and all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(on, on2))
+    check_append(c, freqs(d), eps=1e-5, q_weight=w[0, 1:].clone(), k_weight=w[1, 1:].clone())
+
+
+@pytest.mark.parametrize("n_seq", [1, 31, 33, 1100])
+def test_read_finds_the_sequence_of_each_row(n_seq):
+    """Short and empty sequences, packed, with rows of none before and behind."""
+    rng = np.random.default_rng(n_seq)
+    lens = rng.integers(0, 5, n_seq).tolist()
+    lens[n_seq // 2] = 70
+    c = cache(n_seq, lens, 1, 64, 16, 16)
+    cu = np.concatenate([[0], np.cumsum(lens)]) + 3
+    ko, vo = (torch.full((int(cu[-1]) + 40, 1, 64), 7.0, dtype=BF, device=DEV) for _ in range(2))
+    _, _, ws = fa().fa_kvcache_read_q8(*on_device(c), cu_seqlens_k=dev(torch.tensor(cu, dtype=torch.int32)), block_table=dev(c["bt"]), k_out=ko, v_out=vo)
+    assert fa().fa_check_device_error(ws) == (0, 0)
+    for n, got in (("k", ko.cpu()), ("v", vo.cpu())):
+        full = Q.dequantised(c[n], c[n + "_scale"])
+        assert (got[:3] == 7).all() and (got[int(cu[-1]):] == 7).all()
+        for s, L in enumerate(lens):
+            rows = full[c["bt"][s].numpy()[:-(-L // 16)]].reshape(-1, 1, 64)[:L]
+            assert np.array_equal(got[int(cu[s]):int(cu[s]) + L].double().numpy(), rows)
+
+
+def test_nan_far_back_in_a_long_cache():
+    """A NaN in V far back in a long cache reaches the rows that see it, with tiles that are seen whole before and behind it."""
+    c = chunk_case(30, [300, 40], [3000, 1700], hq=4, hkv=1, page=64, block=32, window_left=1200)
+    pg, r = int(c["bt"][0, 2000 // 64]), 2000 % 64
+    c["v"][pg, r, 0, 5] = np.nan
+    out, lse, _ = run(c)
+    assert np.isfinite(lse.cpu().numpy()).all()
+    i = np.arange(300) + 2700  # the positions of the first sequence's rows
+    sees = (i >= 2000) & (i - 1200 <= 2000)
+    got = torch.isnan(out[:300]).any(-1).all(-1).cpu().numpy()
+    assert np.array_equal(got, sees) and sees.all()
+    clean = dict(c, v=c["v"].copy())
+    clean["v"][pg, r, 0, 5] = 0.0
+    a, b, _ = run(clean)
+    keep = torch.ones(128, dtype=torch.bool)
+    keep[5] = False
+    assert torch.isfinite(a).all() and torch.equal(a[..., keep.to(a.device)], out[..., keep.to(out.device)]) and torch.equal(b, lse)

@@ -244,3 +244,66 @@ def test_binding_refusals_on_the_device():
             call()
     with pytest.raises(TypeError):
         m.fa_qk_norm_rope(q, eps=None)
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d", [(1000, 32, 8, 128), (700, 13, 3, 64), (9000, 9, 1, 64), (6500, 12, 3, 128)])
+def test_shares_of_warps(rows, hq, hkv, d):
+    """Some rounds of a token to a warp, a whole token, and a last round that is not full; several rounds to a warp of the gradient."""
+    g = gen(rows)
+    q, k, gq, gk = (rnd(g, rows, h, d) for h in (hq, hkv, hq, hkv))
+    pos = torch.randint(0, 5000, (rows,), generator=g, dtype=torch.int32)
+    both(q, k, gq, gk, rnd(g, d), rnd(g, d), freqs(d), pos)
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_weights_at_any_address(half):
+    """Weights that begin off a 16-byte boundary."""
+    g = gen(9)
+    q, gq = rnd(g, 1, 33, 5, 128), rnd(g, 1, 33, 5, 128)
+    base = rnd(g, 132) if half else torch.randn(132, generator=g)
+    m = fa()
+    for off in (1, 3):
+        w = dev(base)[off:off + 128]
+        y, _ = m.fa_qk_norm_rope(dev(q), q_weight=w, inv_freq=dev(freqs(128)))
+        dq, _, dw, _, _ = m.fa_qk_norm_rope_bwd(dev(gq), None, dev(q), q_weight=w, inv_freq=dev(freqs(128)))
+        at = np.arange(33)[None]
+        assert_normed(y, q, at, freqs(128), w=base[off:off + 128])
+        assert_grad(dq, dw, gq, q, at, freqs(128), w=base[off:off + 128])
+
+
+def test_broadcast_gradient():
+    """One dy row for all heads and tokens (strides of 0)."""
+    g = gen(10)
+    q, gq = rnd(g, 2, 30, 6, 64, dtype=H), rnd(g, 1, 1, 1, 64, dtype=H)
+    dq, _, dw, _, _ = fa().fa_qk_norm_rope_bwd(dev(gq).expand(2, 30, 6, 64), None, dev(q), q_weight=dev(torch.ones(64)), inv_freq=dev(freqs(64)))
+    assert_grad(dq, dw, gq.expand(2, 30, 6, 64).contiguous(), q, np.broadcast_to(np.arange(30), (2, 30)), freqs(64), w=torch.ones(64))
+
+
+def test_infinite_gradient_reaches_its_column():
+    """An infinite dy makes its column of dw infinite or NaN, no other."""
+    g = gen(11)
+    q, gq = rnd(g, 1, 50, 4, 64), rnd(g, 1, 50, 4, 64)
+    gq[0, 20, 1, 7] = float("inf")
+    dq, _, dw, _, _ = fa().fa_qk_norm_rope_bwd(dev(gq), None, dev(q), q_weight=dev(torch.ones(64)))
+    bad = ~torch.isfinite(dw.cpu())
+    assert bad[7] and bad.sum() == 1
+    rows = ~torch.isfinite(dq.cpu()).all(-1)
+    assert rows[0, 20, 1] and rows.sum() == 1
+
+
+def test_two_streams_at_once():
+    """Gradients of two layers on two streams, each with its own workspace."""
+    m = fa()
+    g = gen(12)
+    layers = [tuple(dev(rnd(g, 1, 2000, h, 128)) for h in (8, 2, 8, 2)) for _ in range(2)]
+    w, f = dev(rnd(g, 128)), dev(freqs(128))
+    one = [m.fa_qk_norm_rope_bwd(a, b, c, d, q_weight=w, k_weight=w, inv_freq=f)[:4] for a, b, c, d in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [None, None]
+    for _ in range(5):
+        for i, (s, (a, b, c, d)) in enumerate(zip(streams, layers)):
+            with torch.cuda.stream(s):
+                got[i] = m.fa_qk_norm_rope_bwd(a, b, c, d, q_weight=w, k_weight=w, inv_freq=f)[:4]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for a, b in zip(one, got) for x, y in zip(a, b))
