@@ -346,7 +346,12 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
       ls[k] = have ? pl[k * ROWS] : -INFINITY;
     }
     float mx = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
-    for (int k = kAhead; k < sp.n; ++k) mx = fmaxf(mx, pl[k * ROWS]);
+    if (sp.n > kAhead) {  // a lane for each of the others
+      for (int k = kAhead + c; k < sp.n; k += kLanes) mx = fmaxf(mx, pl[k * ROWS]);
+      const uint32_t group = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+      for (int x = 1; x < kLanes; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(group, mx, x));
+    }
     const float ref = mx == -INFINITY ? 0.f : mx;  // no piece has a key of the row: all weights 0
     float sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -357,7 +362,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     };
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) add(ls[k], v[k]);
-#pragma unroll 4
+    // (one token of one K/V head over 60000 keys, 300 pieces: eight at a time 45 us, four 53)
+#pragma unroll 8
     for (int k = kAhead; k < sp.n; ++k)
       add(pl[k * ROWS], *reinterpret_cast<const float4*>(po + (int64_t)k * ROWS * D));
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -370,13 +376,16 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
   }
 }
 
-// A cache in 8 bits, and at most 32 rows (tokens x q-heads of a K/V head) in a sequence:
-// one query tile of 8, 16 or 32 rows in the form for few rows (chunk_q8.cu).
+// A cache in 8 bits, and at most 16 rows (tokens x q-heads of a K/V head) in a sequence:
+// one query tile of 8 or 16 rows in the form for few rows (chunk_q8.cu).  More rows go to
+// the tensor cores (chunk_q8_sm103.cu): 64 sequences over 4096 keys, 32 heads on 8, took
+// there and here with 16 rows 187 and 147 us, with 32 rows 189 and 222; one sequence over
+// 32000 keys, 32 rows, 40 and 45.
 void plan_q8_rows(ChunkParams& p) {
-  if ((int64_t)p.Sq * p.G > 32) return;
+  const int64_t rows = (int64_t)p.Sq * p.G;
+  if (rows > 16) return;
   p.gp = p.G;
-  const int64_t rows = (int64_t)p.Sq * p.gp;
-  p.form = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  p.form = rows <= 8 ? 1 : 2;
   p.part_rows = 8 * p.form;
   p.rt_tokens = p.part_rows / p.gp;
   p.n_hg = p.Hq / p.gp;
@@ -546,7 +555,7 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   const int64_t longest = cu_q ? std::min(Sq, p.tot_q) : Sq;
   if (rtiles * p.n_hg > (1 << 27) || (longest + p.rt_tokens - 1) / p.rt_tokens > kMaxSeqTiles) return FA_ERR_INVALID_ARG;
   const int64_t units = rtiles * p.n_hg, n_kt = std::max<int64_t>(1, (Sk + kKeysPerTile - 1) / kKeysPerTile);
-  const int64_t ctas = (int64_t)sm_count() * (p.form ? q8_ctas(p.form) : p.pair ? 2 : 1);
+  const int64_t ctas = (int64_t)sm_count() * (p.form ? kQ8Ctas : p.pair ? 2 : 1);
   // partials: at most two rounds of the grid, and no more than all tiles alone;
   // none where no sequence has more than 8 key tiles: such units then need no
   // planner either (below).  One token over 700 keys, 6 tiles, in a graph: cut in
@@ -606,7 +615,6 @@ template <int D, bool F16>
 cudaError_t launch_join(const ChunkParams& p, bool overlap, cudaStream_t st) {
   if (p.part_rows == 8) return launch_join<D, F16, 8>(p, overlap, st);
   if (p.part_rows == 16) return launch_join<D, F16, 16>(p, overlap, st);
-  if (p.part_rows == 32) return launch_join<D, F16, 32>(p, overlap, st);
   return launch_join<D, F16, kChunkRows>(p, overlap, st);
 }
 

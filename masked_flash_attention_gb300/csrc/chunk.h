@@ -76,11 +76,11 @@ struct ChunkParams {
   int32_t block_shift;  // tokens of a block = 2^block_shift
   int32_t sinks;        // first keys that the window does not hide
   int32_t part_rows;    // rows of a partial (kChunkRows, fewer for the 8-bit forms of few rows)
-  int32_t form;         // 8 bits: 8-row tiles of the form for few rows (1, 2, 4), 0 = the tensor-core form
+  int32_t form;         // 8 bits: 8-row tiles of the form for few rows (1, 2), 0 = the tensor-core form
 };
 
 // CTAs per SM of the 8-bit form for few rows.
-constexpr int q8_ctas(int form) { return form <= 2 ? 2 : 1; }
+constexpr int kQ8Ctas = 2;
 
 // `overlap`: the kernel may start while the one before it on the stream runs
 // (programmatic dependent launch; it waits for that one's results itself).

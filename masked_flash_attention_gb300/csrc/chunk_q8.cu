@@ -6,6 +6,10 @@
 // keys (the planner of chunk.cu); of each 128-key tile its eight warps take 16 keys
 // each.  A warp streams its keys through a ring of its own, by two TMA copies for 16
 // keys, and waits for nobody else.  With two CTAs per SM 190 KB are in flight.
+// Measured (64 single tokens over 128 .. 8192 keys, window 4096, soft-cap, 32 heads on 8,
+// d 128, pages of 16): 114 us (3.9 TB/s) with the planner and the join, which are 10 of it;
+// the copies alone take 90 (a head's 16 rows of a page are 128 bytes each, 1 KB apart),
+// the products alone 75.  Four sums instead of one for S change nothing.
 //
 // Products are m16n8k16 in fp16 with fp32 sums, S^T = K Q^T and O^T = V^T P^T, so that
 // the 16 rows of an operand are keys or columns and eight query rows fill the other.
@@ -52,13 +56,12 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 16;                   // tiles that a warp looks up at once
 constexpr float kTop = 7.f, kRaise = 15.f;  // log2 of the weights at the top
 
-// NT: 8-row tiles of a query tile.
+// NT: 8-row tiles of a query tile, 1 or 2.
 template <int D, int NT>
 struct QCfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = q8_ctas(NT);             // per SM
   static constexpr int kStageBytes = 2 * 16 * D;        // K and V of 16 keys
-  static constexpr int kStages = (NT <= 2 ? 3 : 6) * 128 / D;
+  static constexpr int kStages = 3 * 128 / D;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQStride = 2 * D + 16;           // bytes of a Q row
   static constexpr int kOStride = D + 36;               // floats of a row of the join: eight runs of D / 8 + 4, and 4
@@ -71,7 +74,7 @@ struct QCfg {
   static constexpr int kGeoOff = kOwnOff + 32;  // what only the look-ups need of the piece
   static constexpr int kSmem = kGeoOff + 48 + 1024;                  // (the ring starts on a 1024-byte boundary)
   static_assert(kWarps * kRows * kOStride * 4 <= kRing, "the join's rows take the ring's place");
-  static_assert(kSmem <= (kCtas == 1 ? 227 : 113) * 1024, "shared memory budget");
+  static_assert(kQ8Ctas * kSmem <= 226 * 1024, "shared memory budget");
 };
 
 // The transposed of an 8 x 8 matrix of 16-bit elements, lane (g, t) holding row g, columns 2 t and 2 t + 1.
@@ -85,7 +88,7 @@ __device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_
 
 // GEN: soft-cap and / or ALiBi.
 template <int D, int NT, bool GEN>
-__global__ void __launch_bounds__(kThreads, QCfg<D, NT>::kCtas)
+__global__ void __launch_bounds__(kThreads, kQ8Ctas)
     chunk_q8_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv) {
   using C = QCfg<D, NT>;
@@ -545,8 +548,8 @@ cudaError_t launch(const ChunkParams& p, bool overlap, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_chunk_q8(const ChunkParams& p, bool overlap, cudaStream_t st) {
-  if (p.d == 64) return p.form == 1 ? launch<64, 1>(p, overlap, st) : p.form == 2 ? launch<64, 2>(p, overlap, st) : launch<64, 4>(p, overlap, st);
-  return p.form == 1 ? launch<128, 1>(p, overlap, st) : p.form == 2 ? launch<128, 2>(p, overlap, st) : launch<128, 4>(p, overlap, st);
+  if (p.d == 64) return p.form == 1 ? launch<64, 1>(p, overlap, st) : launch<64, 2>(p, overlap, st);
+  return p.form == 1 ? launch<128, 1>(p, overlap, st) : launch<128, 2>(p, overlap, st);
 }
 
 }  // namespace mfa
