@@ -391,6 +391,14 @@ void plan_q8_rows(ChunkParams& p) {
   p.n_hg = p.Hq / p.gp;
 }
 
+// Key tiles of a unit that its rows see at most, of n_kt: fewer with a window.
+int64_t seen_tiles(const ChunkParams& p, int64_t n_kt) {
+  const int64_t right = p.wr >= 0 ? p.wr : p.causal && !p.prefix ? 0 : -1;  // (with both, the nearer: this is enough)
+  if (p.wl < 0 || right < 0 || (p.debug_flags & FA_DEBUG_NO_SKIP)) return n_kt;
+  const int64_t keys = (int64_t)p.wl + p.rt_tokens + right;
+  return std::min(n_kt, (keys + kKeysPerTile - 2) / kKeysPerTile + 1 + (p.sinks + kKeysPerTile - 1) / kKeysPerTile);
+}
+
 // Arguments checked, geometry and workspace laid out (offsets from `base`,
 // which may be null for a plan).
 // q8: the scales and the visible first keys of a cache in 8 bits, null for one in q's type.
@@ -562,7 +570,14 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // six and joined 13.3 us, whole with the planner 14.0, whole without it 10.2.
   // None either for more tiles than 32-bit sums hold, on which the planner's bound
   // on the partials rests (there are thousands of units then).
-  const int64_t slots = n_kt > 8 && rtiles * n_kt <= INT32_MAX ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
+  const int64_t all = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens) * p.n_hg;
+  // The 8-bit form for few rows is through a tile sooner: where every unit has a CTA,
+  // whole up to 11 tiles that a window leaves, up to 16 where the units fill a third of
+  // them (whole and cut, in a graph: one token of 2 K/V heads, 10 tiles, 12.7 and 16.5 us;
+  // of 8 heads, 16 tiles, 21.3 and 18.5; 16 tokens of 8 heads, 16 tiles, 22.6 and 24.7; 32
+  // of 8, 31.0 and 37.1).
+  const bool whole = p.form && all <= ctas && seen_tiles(p, n_kt) <= (3 * all >= ctas ? 16 : 11);
+  const int64_t slots = n_kt > 8 && !whole && rtiles * n_kt <= INT32_MAX ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
   const int64_t pieces = units + slots;
   p.max_rtiles = (int32_t)rtiles;
   p.max_slots = (int32_t)slots;
@@ -572,7 +587,6 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   // us in a graph, with the planner 10.8).  More units than CTAs are left to
   // the planner's order: 8 x 1024 tokens of 12 heads, 768 units of 1 to 8 tiles,
   // took 42 us in turn, 34 us longest first.
-  const int64_t all = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens) * p.n_hg;
   p.direct = slots == 0 && all <= ctas ? (int32_t)all : 0;
   if (p.direct) p.grid = p.direct;
   size_t off = kWsHeadBytes;

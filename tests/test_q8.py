@@ -137,6 +137,19 @@ def test_plan_geometry():
         assert plan(kc=T(10, 128, 2, 128, dtype=E4), ks=f32(10, 128 // block, 2))[0] == 0
 
 
+def test_plan_of_few_short_units():
+    """One launch where a window leaves few tiles and every unit has a CTA; a planner and a join where not."""
+    tokens = lambda n, sk, **kw: plan(T(n, 8, 128), cu_seqlens_q=i32(n + 1), block_table=i32(n, 500), lens=i32(n), max_seqlen_q=1,  # noqa: E731
+                                      max_seqlen_k=sk, **kw)[1]["n_kernels"]
+    assert tokens(2, 16000) == 3 and tokens(2, 16000, window_left=1100) == 1 and tokens(2, 16000, window_left=1700) == 3
+    assert tokens(2, 16000, window_left=1100, sink_keys=4) == 1 and tokens(2, 16000, window_left=1100, sink_keys=500) == 3
+    assert tokens(2, 16000, window_left=1100, prefix_lens=i32(2)) == 3
+    assert tokens(2, 16000, window_left=1100, causal=False, window_right=50) == 1
+    assert tokens(2, 16000, window_left=1100, causal=False) == 3
+    assert tokens(2, 1400) == 1 and tokens(2, 2000) == 3 and tokens(64, 2000) == 1 and tokens(64, 2100) == 3
+    assert tokens(160, 1400) == 3  # more units than CTAs
+
+
 def test_plan_refusals():
     kc = T(10, 32, 2, 128, dtype=E4)
     bad = [

@@ -382,7 +382,7 @@ def test_long_caches_are_split(hq, hkv, d, params):
     c = chunk_case(hq, [1, 2, 1], [9000, 3333, 40], hq=hq, hkv=hkv, d=d, page=64, **params)
     rc, p = fa().fa_fwd_chunk_q8_plan(c["q"], *(t.cpu() for t in on_device(c)), c["lens"], cu_seqlens_q=c["cu"], block_table=c["bt"],
                                       max_seqlen_q=c["max_q"], max_seqlen_k=c["max_k"], **params)
-    assert rc == 0 and p["n_splits"] > 1
+    assert rc == 0 and (p["n_splits"] > 1) == (params.get("window_left") != 100)  # (a window of three tiles stays whole)
     check(c)
 
 
@@ -771,3 +771,12 @@ def test_nan_far_back_in_a_long_cache():
     keep = torch.ones(128, dtype=torch.bool)
     keep[5] = False
     assert torch.isfinite(a).all() and torch.equal(a[..., keep.to(a.device)], out[..., keep.to(out.device)]) and torch.equal(b, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens,params", [([1, 1, 2], [5000, 1300, 40], dict(window_left=1200, sink_keys=40)),
+                                                   ([1, 1, 1], [5000, 1100, 1000], dict(window_left=900, causal=False, window_right=100)),
+                                                   ([1, 4], [1400, 1407], {}), ([1] * 64, [2000 - 31 * i for i in range(64)], {})])
+def test_units_that_stay_whole(d, q_lens, kv_lens, params):
+    """Up to 16 tiles to a CTA, without a planner: whole caches, and windows far along them with and without first keys."""
+    check(chunk_case(31, q_lens, kv_lens, d=d, **params))
