@@ -9,7 +9,8 @@
 // Measured (64 single tokens over 128 .. 8192 keys, window 4096, soft-cap, 32 heads on 8,
 // d 128, pages of 16): 114 us (3.9 TB/s) with the planner and the join, which are 10 of it;
 // the copies alone take 90 (a head's 16 rows of a page are 128 bytes each, 1 KB apart),
-// the products alone 75.  Four sums instead of one for S change nothing.
+// the products alone 75.  Four sums instead of one for S change nothing;
+// two tiles at a time, with barriers of their own for K and V, took 134.
 //
 // Products are m16n8k16 in fp16 with fp32 sums, S^T = K Q^T and O^T = V^T P^T, so that
 // the 16 rows of an operand are keys or columns and eight query rows fill the other.
