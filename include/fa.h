@@ -414,8 +414,8 @@ int fa_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_w
 /* Its gradients, for the same arguments: dq and dk from dq_out and dk_out (the
  * gradients of the rotated rows), and the weights' (fp32 [d], each may be NULL;
  * dk_weight only with k), summed over all rows and heads.  The sums are fp32 in
- * a fixed order, their last stage fp64: the result does not depend on
- * scheduling.  dq may be q or dq_out itself, dk likewise (same pointer and
+ * a fixed order, their last stage in two fp32 words: the result does not depend
+ * on scheduling.  dq may be q or dq_out itself, dk likewise (same pointer and
  * strides), else they overlap neither.  Workspace (only with a weight gradient):
  * FA_QK_NORM_ROPE_BWD_WORKSPACE_BYTES. */
 #define FA_QK_NORM_ROPE_BWD_WORKSPACE_BYTES ((size_t)256 + ((size_t)1 << 20))

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 // there and here with 16 rows 187 and 147 us, with 32 rows 189 and 222; one sequence over
 // 32000 keys, 32 rows, 40 and 45.
 void plan_q8_rows(ChunkParams& p) {
-  const int64_t rows = (int64_t)p.Sq * p.G;
+  const int64_t rows = std::max<int64_t>(p.Sq, 1) * p.G;
   if (rows > 16) return;
   p.gp = p.G;
   p.form = rows <= 8 ? 1 : 2;
@@ -396,7 +396,7 @@ int64_t seen_tiles(const ChunkParams& p, int64_t n_kt) {
   const int64_t right = p.wr >= 0 ? p.wr : p.causal && !p.prefix ? 0 : -1;  // (with both, the nearer: this is enough)
   if (p.wl < 0 || right < 0 || (p.debug_flags & FA_DEBUG_NO_SKIP)) return n_kt;
   const int64_t keys = (int64_t)p.wl + p.rt_tokens + right;
-  return std::min(n_kt, (keys + kKeysPerTile - 2) / kKeysPerTile + 1 + (p.sinks + kKeysPerTile - 1) / kKeysPerTile);
+  return std::min(n_kt, (keys + kKeysPerTile - 2) / kKeysPerTile + 1 + ((int64_t)p.sinks + kKeysPerTile - 1) / kKeysPerTile);
 }
 
 // Arguments checked, geometry and workspace laid out (offsets from `base`,

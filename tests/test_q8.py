@@ -137,6 +137,15 @@ def test_plan_geometry():
         assert plan(kc=T(10, 128, 2, 128, dtype=E4), ks=f32(10, 128 // block, 2))[0] == 0
 
 
+@pytest.mark.parametrize("hq", [2, 16, 18, 24, 80])
+def test_plan_without_tokens(hq):
+    """No tokens, with more heads of a group than a tile of few rows has rows."""
+    rc, p = plan(T(2, 0, hq, 64), T(2, 64, 2, 64, dtype=E4), cu_seqlens_q=None, block_table=None, max_seqlen_k=64)
+    assert rc == 0 and p["n_items"] == 0 and p["n_kernels"] == 0
+    rc, p = plan(T(0, hq, 64), T(10, 32, 2, 64, dtype=E4), max_seqlen_q=0)
+    assert rc == 0 and p["n_items"] == 0
+
+
 def test_plan_of_few_short_units():
     """One launch where a window leaves few tiles and every unit has a CTA; a planner and a join where not."""
     tokens = lambda n, sk, **kw: plan(T(n, 8, 128), cu_seqlens_q=i32(n + 1), block_table=i32(n, 500), lens=i32(n), max_seqlen_q=1,  # noqa: E731
@@ -148,6 +157,7 @@ def test_plan_of_few_short_units():
     assert tokens(2, 16000, window_left=1100, causal=False) == 3
     assert tokens(2, 1400) == 1 and tokens(2, 2000) == 3 and tokens(64, 2000) == 1 and tokens(64, 2100) == 3
     assert tokens(160, 1400) == 3  # more units than CTAs
+    assert tokens(2, 16000, window_left=1100, sink_keys=2**31 - 1) == 3
 
 
 def test_plan_refusals():

@@ -780,3 +780,13 @@ def test_nan_far_back_in_a_long_cache():
 def test_units_that_stay_whole(d, q_lens, kv_lens, params):
     """Up to 16 tiles to a CTA, without a planner: whole caches, and windows far along them with and without first keys."""
     check(chunk_case(31, q_lens, kv_lens, d=d, **params))
+
+
+@pytest.mark.parametrize("d,hkv,params", [(64, 3, {}), (128, 2, dict(window_left=70, sink_keys=9)), (128, 1, dict(softcap=20.0))])
+def test_many_pieces_of_a_cta(d, hkv, params):
+    """Many sequences of many rows, some without tokens or keys of their own before them: several pieces to each CTA, one behind another."""
+    rng = np.random.default_rng(d + hkv)
+    q = [0 if x < 3 else int(x) for x in rng.integers(0, 90, 500)]
+    q[7] = 150
+    kv = [n + int(x) for n, x in zip(q, rng.integers(0, 260, 500))]
+    check(chunk_case(d + hkv, q, kv, hq=2 * hkv, hkv=hkv, d=d, page=32, block=32, **params))
