@@ -32,7 +32,8 @@
 // keys 197 us (2.8 TB/s).  With eight pieces of the conversion's loads ahead; one at a time
 // takes 334 us for the second.  A second warpgroup for the conversion (20 warps of fewer
 // registers) took 207, 256 rows to a CTA 219, codes by plain loads straight into
-// registers more than 230.
+// registers more than 230, a half of the columns of every tile to each softmax warpgroup 203.
+// Without conversion and softmax the copies and products alone take 138, with either 165 .. 173.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -66,8 +67,10 @@ struct TCfg {
   static_assert(128 * kOtherRegs + 128 * kWidenRegs + 256 * kSoftmaxRegs <= kThreads * kLaunchRegs, "the register split must fit the launch");
   static constexpr uint32_t kCols = 512, kOCol = 384;  // TMEM: three S buffers, each overwritten by its P, and O
   static constexpr int NB = 3;
-  static constexpr int NS = D == 128 ? 2 : 4;          // tiles of K, and of V
-  static constexpr int NR = D == 128 ? 3 : 6;          // raw tiles of both
+  // (more of them at d = 64 are slower: 8 x 512 tokens of 12 heads over 4608 keys 150 us, with
+  // four and six 165; at d = 128 two or three raw tiles are the same)
+  static constexpr int NS = D == 128 ? 2 : 3;          // tiles of K, and of V
+  static constexpr int NR = 3;                         // raw tiles of both
   static constexpr int kRawBytes = 128 * D, kTileBytes = 2 * kRawBytes;
   static constexpr int kHalfStep = 16384;  // D / 64 halves of 128 rows by 128 bytes
   static constexpr int kQOff = 0;
