@@ -5,9 +5,9 @@
 // Bound: HBM, one byte per cached element.  A CTA runs one piece of a query tile's
 // keys (the planner of chunk.cu); of each 128-key tile its eight warps take 16 keys
 // each.  A warp streams its keys through a ring of its own, by two TMA copies for 16
-// keys, and waits for nobody else.  With two CTAs per SM 190 KB are in flight.
+// keys, and waits for nobody else.  With two CTAs per SM 128 KB are in flight.
 // Measured (64 single tokens over 128 .. 8192 keys, window 4096, soft-cap, 32 heads on 8,
-// d 128, pages of 16): 114 us (3.9 TB/s) with the planner and the join, which are 10 of it;
+// d 128, pages of 16): 109 us (4.1 TB/s) with the planner and the join, which are 10 of it;
 // the copies alone take 90 (a head's 16 rows of a page are 128 bytes each, 1 KB apart),
 // the products alone 75.  Four sums instead of one for S change nothing;
 // two tiles at a time, with barriers of their own for K and V, took 134.
@@ -62,7 +62,9 @@ template <int D, int NT>
 struct QCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = 2 * 16 * D;        // K and V of 16 keys
-  static constexpr int kStages = 3 * 128 / D;
+  // (two at d = 128: 109 us for the decoding step at the top, three 114; what shared memory leaves
+  // is L1.  16 rows need three for the join's)
+  static constexpr int kStages = (NT == 1 ? 2 : 3) * 128 / D;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQStride = 2 * D + 16;           // bytes of a Q row
   static constexpr int kOStride = D + 36;               // floats of a row of the join: eight runs of D / 8 + 4, and 4
