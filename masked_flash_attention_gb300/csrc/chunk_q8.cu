@@ -62,13 +62,14 @@ template <int D, int NT>
 struct QCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = 2 * 16 * D;        // K and V of 16 keys
-  // (two at d = 128: 109 us for the decoding step at the top, three 114; what shared memory leaves
-  // is L1.  16 rows need three for the join's)
-  static constexpr int kStages = (NT == 1 ? 2 : 3) * 128 / D;
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  // (two at d = 128: 109 us for the decoding step at the top and 133 for 16 rows of 64
+  // sequences over 4000 keys, three 114 and 147: what shared memory leaves is L1)
+  static constexpr int kStages = 2 * 128 / D;
   static constexpr int kQStride = 2 * D + 16;           // bytes of a Q row
   static constexpr int kOStride = D + 36;               // floats of a row of the join: eight runs of D / 8 + 4, and 4
-  static constexpr int kQOff = kRing;
+  // (the join's rows take the ring's place)
+  static constexpr int kRing = kWarps * (kStages * kStageBytes > kRows * kOStride * 4 ? kStages * kStageBytes : kRows * kOStride * 4);
+  static constexpr int kQOff = (kRing + 127) / 128 * 128;
   static constexpr int kRowOff = kQOff + kRows * kQStride;           // per row: factor, keys, place, slope
   static constexpr int kSumOff = kRowOff + kRows * 5 * 4;            // ref and sum [kWarps][kRows]
   static constexpr int kInfoOff = kSumOff + kWarps * kRows * 8;      // {page, row, first key, exponents} [kWarps][2 kBatch]
@@ -76,7 +77,6 @@ struct QCfg {
   static constexpr int kOwnOff = kBarOff + kWarps * kStages * 8 + 16;
   static constexpr int kGeoOff = kOwnOff + 32;  // what only the look-ups need of the piece
   static constexpr int kSmem = kGeoOff + 48 + 1024;                  // (the ring starts on a 1024-byte boundary)
-  static_assert(kWarps * kRows * kOStride * 4 <= kRing, "the join's rows take the ring's place");
   static_assert(kQ8Ctas * kSmem <= 226 * 1024, "shared memory budget");
 };
 
