@@ -32,8 +32,9 @@
 //
 // Sixteen keys that the masks hide from every row of the tile are never read.  A key
 // that some rows see and others do not, or one behind the sequence's end in its
-// block, is multiplied by a weight of 0; where such a key's V holds a NaN, its
-// product is made apart, so that it reaches the rows that see it and no others.
+// block, is multiplied by a weight of 0; where 16 keys with such a one among them hold a
+// NaN in V, it is left out of the products and set in the rows that the masks let see it,
+// whatever its key's weight, and in no others.
 #include <climits>
 
 #include <cuda_fp16.h>
@@ -86,8 +87,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t u) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(u));
   return r;
 }
-__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
 // GEN: soft-cap and / or ALiBi.
 template <int D, int NT, bool GEN>
@@ -441,33 +440,52 @@ __global__ void __launch_bounds__(kThreads, kQ8Ctas)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) nan |= (vw[n][i] & 0x7f7f7f7fu) + 0x01010101u;
-        apart = __any_sync(0xffffffffu, (nan & 0x80808080u) != 0);
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t x = nan_codes(vw[n][i]);
+            vw[n][i] &= ~x;
+            nan |= x;
+          }
+        apart = __any_sync(0xffffffffu, nan != 0);
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t sel = i & 1 ? 0x7362 : 0x5140;  // columns 2 i and 2 i + 1 of two keys
         const uint32_t x0 = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel), x1 = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
-        uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)x1),
-                         e4m3x2_to_f16x2((uint16_t)(x1 >> 16))};
-        if (apart) {
-          uint32_t is_nan[4];  // 1 where V is NaN, and V without those
+        const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)x0), e4m3x2_to_f16x2((uint16_t)(x0 >> 16)), e4m3x2_to_f16x2((uint16_t)x1),
+                               e4m3x2_to_f16x2((uint16_t)(x1 >> 16))};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            is_nan[c] = half2_bits(__hneu2(bits_half2(a[c]), bits_half2(a[c])));
-            a[c] &= ~__hneu2_mask(bits_half2(a[c]), bits_half2(a[c]));
+        for (int m = 0; m < NT; ++m) mma_bf16<true>(o[m][i], a, pb[m][0], pb[m][1]);
+      }
+      if (apart) {
+        // the NaNs by what the masks admit, not by the weights: a visible key's may be 0 in fp16
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          float e[4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int row = 8 * m + 2 * t + r, lo = s_lo[row], hi = s_hi[row], j = j0 + g;
+            e[r] = j <= hi && (j >= lo || j < sinks) ? 1.f : 0.f;
+            e[2 + r] = j + 8 <= hi && (j + 8 >= lo || j + 8 < sinks) ? 1.f : 0.f;
           }
+          const uint32_t s0 = transpose_8x8(pack2<true>(e[0], e[1])), s1 = transpose_8x8(pack2<true>(e[2], e[3]));
 #pragma unroll
-          for (int m = 0; m < NT; ++m) {
+          for (int i = 0; i < D / 16; ++i) {
+            // (V is read again, by volatile loads: kept from before it would cost registers on the way here)
+            const unsigned char* at_v = src + 16 * D + 4 * (i / 2);
+            auto word = [&](int at) { return *reinterpret_cast<const volatile uint32_t*>(at_v + at); };
+            const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
+            const uint32_t x0 = nan_codes(__byte_perm(word(v_at[0]), word(v_at[1]), sel));
+            const uint32_t x1 = nan_codes(__byte_perm(word(v_at[0] + 8 * D), word(v_at[1] + 8 * D), sel));
+            const uint32_t one = 0x3c003c00;  // 1 where V is NaN
+            const uint32_t a[4] = {one & __byte_perm(x0, 0, 0x1100), one & __byte_perm(x0, 0, 0x3322), one & __byte_perm(x1, 0, 0x1100),
+                                   one & __byte_perm(x1, 0, 0x3322)};
             float hit[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_bf16<true>(hit, is_nan, pb[m][0], pb[m][1]);
+            mma_bf16<true>(hit, a, s0, s1);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               if (hit[c] > 0.f) o[m][i][c] = __int_as_float(0x7fffffff);
           }
         }
-#pragma unroll
-        for (int m = 0; m < NT; ++m) mma_bf16<true>(o[m][i], a, pb[m][0], pb[m][1]);
       }
     }
 

@@ -143,11 +143,6 @@ __device__ __forceinline__ Geo geo_of(const ChunkParams& p, const ChunkPiece& w)
   return g;
 }
 
-// 0xff in the bytes that are NaN codes.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t codes) {
-  const uint32_t m = ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return m | (m - (m >> 7));
-}
 // GEN: soft-cap and / or ALiBi.
 template <int D, bool GEN>
 __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tmk,

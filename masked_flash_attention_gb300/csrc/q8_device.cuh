@@ -53,6 +53,12 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// 0xff in the bytes that are NaN codes.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t codes) {
+  const uint32_t m = ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return m | (m - (m >> 7));
+}
+
 // Two e4m3 bytes (the low half of u) as two fp16 values: exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t u) {
   uint32_t r;

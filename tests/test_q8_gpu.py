@@ -790,3 +790,49 @@ def test_many_pieces_of_a_cta(d, hkv, params):
     q[7] = 150
     kv = [n + int(x) for n, x in zip(q, rng.integers(0, 260, 500))]
     check(chunk_case(d + hkv, q, kv, hq=2 * hkv, hkv=hkv, d=d, page=32, block=32, **params))
+
+
+def nan_tokens(c, s, js, quiet=None, scale=None):
+    """V of keys js of sequence s all NaN; quiet: their K such that a q of ones times d has a logit of -7 d sqrt(1 / d)
+    (-448 in a block of scale 2^-6); scale: that of V's blocks they stand in."""
+    page, block = c["k"].shape[1], c["k"].shape[1] // c["k_scale"].shape[1]
+    for j in js:
+        pg, r = int(c["bt"][s, j // page]), j % page
+        c["v"][pg, r] = np.nan
+        if quiet:
+            c["k"][pg, r], c["k_scale"][pg, r // block] = -448.0, 2.0 ** -6
+        if scale:
+            c["v_scale"][pg, r // block] = scale
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_len,hq", [(1, 4), (3, 4), (3, 8), (40, 4)])
+@pytest.mark.parametrize("kv_len", [1024, 1025, 1030, 161])
+@pytest.mark.parametrize("which", ["last block", "last key"])
+def test_nan_of_a_small_block_after_earlier_keys(d, q_len, hq, kv_len, which):
+    """The newest tokens' V all NaN, as the append leaves a block that holds nothing else: scale 2^-40.  Its keys' weights,
+    2^-34 and less of those of the blocks before it, still bring the NaN to the rows that see them, and to no others."""
+    c = chunk_case(q_len + kv_len, [q_len, 1], [kv_len, 200], hq=hq, hkv=2, d=d, page=16)
+    first = (kv_len - 1) // 16 * 16
+    nan_tokens(c, 0, range(first if which == "last block" else kv_len - 1, kv_len), scale=2.0 ** -40)
+    ro, rl, mass, size = ref = oracle(c)
+    assert np.isnan(ro[q_len - 1]).all() and not np.isnan(ro[q_len]).any() and not np.isnan(mass).any()
+    out, lse, _ = run(c)
+    assert_close(c, out, lse, ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_len,hq", [(1, 4), (3, 4), (3, 8), (40, 4)])
+@pytest.mark.parametrize("scale", [None, 1.0])
+@pytest.mark.parametrize("at", [1028, 129, 31, 9])
+def test_nan_of_a_key_of_no_weight(d, q_len, hq, scale, at):
+    """A NaN whose key has a logit 56 to 896 below the others: weights under fp16's, and under those of fp32.  The rows that
+    see the key are NaN, in runs of keys that all rows see and in those at both ends of a window."""
+    c = chunk_case(at, [q_len], [1030], hq=hq, hkv=2, d=d, page=16, window_left=1030 - q_len - at if at < 100 else -1, scale=scale)
+    c["q"] = torch.ones_like(c["q"])
+    nan_tokens(c, 0, [at], quiet=True)
+    ro, rl, mass, size = ref = oracle(c)
+    sees = np.isnan(ro).all((1, 2))
+    assert sees.any() and np.array_equal(sees, np.isnan(ro).any((1, 2))) and (q_len == 1 or not sees.all() or at == 129)
+    out, lse, _ = run(c)
+    assert_close(c, out, lse, ref)
