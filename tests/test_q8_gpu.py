@@ -836,3 +836,61 @@ def test_nan_of_a_key_of_no_weight(d, q_len, hq, scale, at):
     assert sees.any() and np.array_equal(sees, np.isnan(ro).any((1, 2))) and (q_len == 1 or not sees.all() or at == 129)
     out, lse, _ = run(c)
     assert_close(c, out, lse, ref)
+
+
+def by_value(c, on, r, err):
+    """K's codes times the scales that were written, of all blocks, whatever scale each came out with: the new tokens' and the
+    old ones' values to half a step of that scale (a code: 2^-4 of it, at least 2^-10), and fp32's error of new ones."""
+    page, shape = c["k"].shape[1], c["k"].shape
+    block = page // c["k_scale"].shape[1]
+    wide = lambda s: np.repeat(s, block, 1)[..., None]  # noqa: E731
+    got, scale = Q.values(on[0]), on[2].double().cpu().numpy()
+    was = c["k"] * wide(c["k_scale"])  # (the old tokens; NaN elsewhere)
+    new = r["k_exact"] * wide(r["k_scale"])
+    e, fresh = np.zeros(shape), np.zeros(shape, dtype=bool)
+    lead = c["kn"].shape[:-2]
+    for at, (s, i) in zip(np.ndindex(*lead), R.seq_of_rows(lead[0], c["cu"])):
+        if s >= 0:
+            j = int(c["lens"][s]) + i
+            e[int(c["bt"][s, j // page]), j % page] = err[at]
+            fresh[int(c["bt"][s, j // page]), j % page] = True
+    ref = np.where(fresh, new, was)
+    kept = ~np.isnan(ref)
+    assert np.array_equal(kept, ~np.isnan(got)) and kept.any()
+    with np.errstate(invalid="ignore"):
+        tol = np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * wide(scale)) * (1 + 2.0 ** -20) + e
+        bad = kept & ~(np.abs(got * wide(scale) - ref) <= tol)
+    assert not bad.any(), f"{int(bad.sum())}, first {np.argwhere(bad)[0]}"
+    return scale
+
+
+@pytest.mark.parametrize("n_new,d,dtype", [(1, 128, BF), (2, 64, H)])
+def test_append_codes_where_a_scale_is_a_step_off(n_new, d, dtype):
+    """Normalised rows whose every element is 448 but for fp32's error: the scale is 1, or 2 where that error carries an
+    element past 448, and the codes are those of the scale that was written, the old tokens' among them."""
+    g, n = gen(d), 300
+    c = append_case(d, [5, 0, 16] * (n // 3), [n_new] * n, hkv=2, d=d, page=16, block=16, dtype=dtype, spread=0.0)
+    rows = 1.0 + torch.rand(n * n_new, 2, 1, generator=g)
+    c["kn"] = (rows * torch.sign(torch.randn(n * n_new, 2, d, generator=g) + 1e-3)).to(dtype)
+    # old tokens at up to 448 times a scale of 1
+    old = ~np.isnan(c["k_scale"])
+    c["k_scale"] = np.where(old, 1.0, np.nan)
+    w, eps = torch.full((d,), 448.0), 1e-12
+    qo, on, lens, _ = run_append(c, None, eps=eps, k_weight=w)
+    r = Q.append(c["kn"], c["vn"], c["k"], c["v"], c["k_scale"], c["v_scale"], c["lens"], cu_seqlens_q=c["cu"], block_table=c["bt"],
+                 k_weight=w, eps=eps)
+    scale = by_value(c, on, r, NORM * np.abs(N.norm(c["kn"], w, eps)))
+    there = ~np.isnan(r["k_scale"])
+    assert (r["k_scale"][there] == 1).all() and np.isin(scale[there], (1.0, 2.0)).all()
+
+
+@pytest.mark.parametrize("rot,interleaved,d,block,eps", [(128, False, 128, 16, 1e-5), (64, True, 64, 32, None), (42, False, 128, 64, 1e-5)])
+def test_append_codes_by_value(rot, interleaved, d, block, eps):
+    c = append_case(rot + 50, [5, 0, 90, 200], [300, 70, 1, 40], d=d, page=block, block=block, hq=2, extra_rows=(1, 1))
+    f = freqs(rot)
+    w = 1 + 0.3 * torch.randn(d, generator=gen(rot)) if eps else None
+    qo, on, lens, _ = run_append(c, f, interleaved=interleaved, eps=eps, k_weight=w)
+    r = Q.append(c["kn"], c["vn"], c["k"], c["v"], c["k_scale"], c["v_scale"], c["lens"], cu_seqlens_q=c["cu"], block_table=c["bt"],
+                 inv_freq=f, interleaved=interleaved, k_weight=w, eps=eps)
+    raw = N.norm(c["kn"], w, eps) if eps else c["kn"].double().numpy()
+    by_value(c, on, r, ((NORM if eps else 0.0) + 5e-7) * 1.01 * pair_size(raw, len(f), interleaved))
