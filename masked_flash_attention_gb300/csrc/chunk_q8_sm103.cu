@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(512, 1) chunk_q8_tc_kernel(const __grid_consta
             *reinterpret_cast<uint4*>(smem + C::kQOff + (qc >> 3) * C::kHalfStep + row * 128 + (((qc & 7) ^ (row & 7)) << 4)) =
                 make_uint4(pack2<true>(x[0] * down, x[1] * down), pack2<true>(x[2] * down, x[3] * down),
                            pack2<true>(x[4] * down, x[5] * down), pack2<true>(x[6] * down, x[7] * down));
-            if (qc == 0) fac[row] = GEN ? pow2f(e) : pow2f(e) * p.scale_log2;
+            // (never so small that a scale of K makes it 0, which times a masked -inf would be NaN; 2^-36 of a logit at most)
+            if (qc == 0) fac[row] = GEN ? pow2f(e) : fmaxf(pow2f(e) * p.scale_log2, 0x1p-100f);
           }
         }
         tc::fence_proxy_async_smem();

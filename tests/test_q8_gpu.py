@@ -894,3 +894,14 @@ def test_append_codes_by_value(rot, interleaved, d, block, eps):
                  inv_freq=f, interleaved=interleaved, k_weight=w, eps=eps)
     raw = N.norm(c["kn"], w, eps) if eps else c["kn"].double().numpy()
     by_value(c, on, r, ((NORM if eps else 0.0) + 5e-7) * 1.01 * pair_size(raw, len(f), interleaved))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens", [[2, 3], [40, 33]])
+def test_logits_under_the_range_of_fp32(d, q_lens):
+    """Rows of Q of 1e-30 over keys of zeros (scale 2^-40), with a scale of 1e-6: all logits are 0, masks hold."""
+    c = chunk_case(32, q_lens, [100, 90], d=d, page=16, scale=1e-6)
+    c["q"] = c["q"] * 1e-30
+    c["k"] = np.where(np.isnan(c["k"]), np.nan, 0.0)
+    c["k_scale"] = np.where(np.isnan(c["k_scale"]), np.nan, 2.0 ** -40)
+    check(c)
