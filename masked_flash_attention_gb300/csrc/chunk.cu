@@ -573,9 +573,12 @@ int plan_chunk(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const
   const int64_t all = n_seq * ((Sq + p.rt_tokens - 1) / p.rt_tokens) * p.n_hg;
   // The 8-bit form for few rows is through a tile sooner: where every unit has a CTA,
   // whole up to 11 tiles that a window leaves, up to 16 where the units fill a third of
-  // them (whole and cut, in a graph: one token of 2 K/V heads, 10 tiles, 12.7 and 16.5 us;
-  // of 8 heads, 16 tiles, 21.3 and 18.5; 16 tokens of 8 heads, 16 tiles, 22.6 and 24.7; 32
-  // of 8, 31.0 and 37.1).
+  // them.  Whole and cut, in a graph, us, by this bound on the tiles (d = 128, 8 K/V heads):
+  //   1 token            10: 14.4, 16.5   11: 14.4, 18.5   12: 16.4, 18.5   14: 16.5, 16.5   15: 18.5, 16.5
+  //   the same, soft-cap 10: 16.4, 17.3   11: 16.5, 16.5   12: 17.7, 17.7   13: 18.5, 16.5
+  //   4 tokens, 16 rows   9: 18.6, 20.5   10: 20.5, 20.5   11: 20.6, 20.5   12: 22.6, 18.5
+  //   16 tokens          13: 16.5, 22.6   17: 20.5, 24.7; of 4 tokens each  16: 28.0, 31.8
+  // so 11 lies between where one token (14, with a soft-cap 12) and 16 rows (10) cross.
   const bool whole = p.form && all <= ctas && seen_tiles(p, n_kt) <= (3 * all >= ctas ? 16 : 11);
   const int64_t slots = n_kt > 8 && !whole && rtiles * n_kt <= INT32_MAX ? std::min<int64_t>(2 * ctas, units * n_kt) : 0;
   const int64_t pieces = units + slots;
