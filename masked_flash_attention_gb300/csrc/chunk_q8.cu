@@ -81,13 +81,6 @@ struct QCfg {
   static_assert(kQ8Ctas * kSmem <= 226 * 1024, "shared memory budget");
 };
 
-// The transposed of an 8 x 8 matrix of 16-bit elements, lane (g, t) holding row g, columns 2 t and 2 t + 1.
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t u) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(u));
-  return r;
-}
-
 // GEN: soft-cap and / or ALiBi.
 template <int D, int NT, bool GEN>
 __global__ void __launch_bounds__(kThreads, kQ8Ctas)
@@ -417,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, kQ8Ctas)
           e[2 + r] = fast_exp2(s[m][2 + r] - base);
           l[m][r] = fmaf(e[r] + e[2 + r], per_v, l[m][r]);
         }
-        pb[m][0] = transpose_8x8(pack2<true>(e[0], e[1]));
-        pb[m][1] = transpose_8x8(pack2<true>(e[2], e[3]));
+        pb[m][0] = movmatrix_t(pack2<true>(e[0], e[1]));
+        pb[m][1] = movmatrix_t(pack2<true>(e[2], e[3]));
       }
 
       // ---- O^T += V^T P^T
@@ -467,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, kQ8Ctas)
             e[r] = j <= hi && (j >= lo || j < sinks) ? 1.f : 0.f;
             e[2 + r] = j + 8 <= hi && (j + 8 >= lo || j + 8 < sinks) ? 1.f : 0.f;
           }
-          const uint32_t s0 = transpose_8x8(pack2<true>(e[0], e[1])), s1 = transpose_8x8(pack2<true>(e[2], e[3]));
+          const uint32_t s0 = movmatrix_t(pack2<true>(e[0], e[1])), s1 = movmatrix_t(pack2<true>(e[2], e[3]));
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             // (V is read again, by volatile loads: kept from before it would cost registers on the way here)
