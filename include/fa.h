@@ -405,7 +405,8 @@ int fa_rope_inv_freq(int32_t rot, double base, const fa_rope_scaling* scaling, d
  *   q_weight, k_weight  [d], fp32 or q's element type, or NULL (ones); k_weight
  *                     only with k
  *   eps               > 0
- * Sums and products are fp32 and each element is rounded once.  opts: stream and
+ * Sums and products are fp32 and each element is rounded once; a row whose sum of
+ * squares leaves fp32 (elements of 1e18 and more) becomes zeros.  opts: stream and
  * the event_begin / event_end pair are used; no workspace. */
 int fa_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_weight, const fa_tensor* k_weight,
                     const fa_tensor* q_out, const fa_tensor* k_out, const fa_tensor* positions,
@@ -494,7 +495,9 @@ int fa_kvcache_append_q8(const fa_tensor* q, const fa_tensor* q_out, const fa_te
                          float eps, const fa_tensor* seqlens_out, const fa_opts* opts);
 
 /* Keys and values read back from an 8-bit cache, in bf16 or fp16 (each product
- * code * scale rounded once; bf16 holds all of them exactly).
+ * code * scale rounded once; bf16 holds all of them exactly, fp16 those below 65520:
+ * larger ones become infinities, as does an fp16 value of 63488 or more that entered a
+ * block of scale 2^8, where it is held as 65536).
  *   k_out, v_out      [total_k, Hkv, d] with cu_seqlens_k (int32 [n_seq + 1]): key j
  *                     of sequence s goes to row cu_seqlens_k[s] + j, and the sums tell
  *                     how many there are; or [n_seq, S, Hkv, d] with seqlens_k (int32
@@ -562,10 +565,13 @@ int fa_fwd_chunk_plan(const fa_tensor* q, const fa_tensor* k_cache, const fa_ten
  *     the other rules let see them
  * (sink_keys 0: none; without a window every key is visible anyway).  Q enters the
  * products in fp16 after a power of two per row and the codes of K and V as they are; the
- * scales join in fp32, and the weights are fp16 against fp32 sums.
- * A run of 16 keys that the masks hide from every row of a query tile is not read: table
- * entries that only such keys would use may hold anything, as may the cache's rows past
- * a sequence's keys.  A NaN in V reaches the rows that see its key and no others.
+ * scales join in fp32, and the weights are fp16 against fp32 sums: V's scale is part of a
+ * weight, so a key's term is off by 2^-11 of itself or, where that is more, by 2^-31 of the
+ * largest |V| that the row sees, and below that it is lost (the sum keeps its weight).
+ * A page of which no row of a query tile sees a key is not read for that tile: table
+ * entries that only such pages stand in may hold anything, as may the cache's rows past
+ * a sequence's keys (hidden keys of the other pages may be copied, and change nothing).
+ * A NaN in V reaches the rows that see its key, whatever its weight, and no others.
  * FA_ERR_UNSUPPORTED: a stride of 0 along more than one element of k_cache or
  * v_cache.  Workspace: fa_fwd_chunk_q8_plan's. */
 int fa_fwd_chunk_q8(const fa_tensor* q, const fa_tensor* k_cache, const fa_tensor* v_cache, const fa_tensor* k_scale,

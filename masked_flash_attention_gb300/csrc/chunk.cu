@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 // A cache in 8 bits, and at most 16 rows (tokens x q-heads of a K/V head) in a sequence:
 // one query tile of 8 or 16 rows in the form for few rows (chunk_q8.cu).  More rows go to
 // the tensor cores (chunk_q8_sm103.cu): 64 sequences over 4096 keys, 32 heads on 8, took
-// there and here with 16 rows 187 and 133 us, with 32 rows 189 and 222; one sequence over
+// there and here with 16 rows 187 and 131 us, with 32 rows 189 and 222; one sequence over
 // 32000 keys, 32 rows, 40 and 45.
 void plan_q8_rows(ChunkParams& p) {
   const int64_t rows = std::max<int64_t>(p.Sq, 1) * p.G;

@@ -7,10 +7,10 @@
 // each.  A warp streams its keys through a ring of its own, by two TMA copies for 16
 // keys, and waits for nobody else.  With two CTAs per SM 128 KB are in flight.
 // Measured (64 single tokens over 128 .. 8192 keys, window 4096, soft-cap, 32 heads on 8,
-// d 128, pages of 16): 109 us (4.1 TB/s) with the planner and the join, which are 10 of it;
-// the copies alone take 90 (a head's 16 rows of a page are 128 bytes each, 1 KB apart),
-// the products alone 75.  Four sums instead of one for S change nothing;
-// two tiles at a time, with barriers of their own for K and V, took 134.
+// d 128, pages of 16): 103 us (4.3 TB/s) with the planner and the join, which are 10 of it.
+// With three stages of copies it was 114, the copies alone 90 (a head's 16 rows of a page
+// are 128 bytes each, 1 KB apart), the products alone 75; four sums instead of one for S
+// changed nothing, two tiles at a time, with barriers of their own for K and V, took 134.
 //
 // Products are m16n8k16 in fp16 with fp32 sums, S^T = K Q^T and O^T = V^T P^T, so that
 // the 16 rows of an operand are keys or columns and eight query rows fill the other.
@@ -63,8 +63,9 @@ template <int D, int NT>
 struct QCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = 2 * 16 * D;        // K and V of 16 keys
-  // (two at d = 128: 109 us for the decoding step at the top and 133 for 16 rows of 64
-  // sequences over 4000 keys, three 114 and 147: what shared memory leaves is L1)
+  // (d = 128, two and three: the decoding step at the top 109 and 114 us, 16 rows of 64
+  // sequences over 4000 keys 133 and 147, before the NaNs of V left the loop of the
+  // products (103 and 131 since): what shared memory leaves is L1)
   static constexpr int kStages = 2 * 128 / D;
   static constexpr int kQStride = 2 * D + 16;           // bytes of a Q row
   static constexpr int kOStride = D + 36;               // floats of a row of the join: eight runs of D / 8 + 4, and 4
